@@ -381,6 +381,130 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
                    int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
                    void* c, int c_dtype, int64_t ldc, void* stream);
 
+/* Residual addition and root-mean-square norm with an FP8 output: the input
+ * of a pre-norm Linear, quantized for its fprop and (transposed copy) wgrad
+ * GEMMs without a high-precision copy in memory.  For each row
+ *
+ *     h    = x + residual         rounded once to dtype (h = x without one)
+ *     rstd = 1 / sqrt(sum_c h[c]^2 / cols + eps)
+ *     y[c] = fp32(fp32(h[c] * rstd) * gamma[c])
+ *
+ * in binary32, and y is quantized from binary32 (it is not rounded to bf16
+ * first) as qsg_quantize quantizes a tensor.
+ *   x          rows x cols (dtype, ldx); residual the same (ldr), or NULL.
+ *   gamma      cols weights of gamma_dtype (QSG_F32 or QSG_BF16).
+ *   eps        finite, >= 0.
+ *   recipe     NULL: no FP8 output (y only).  QSG_TENSORWISE, QSG_DELAYED,
+ *              QSG_MXFP8 and QSG_BLOCK_1X128 with their fmt, margin and
+ *              mx_rule (margin is not used by DELAYED, whose scale is given);
+ *              QSG_BLOCK_128X128 is a weight recipe: QSG_ERR_UNSUPPORTED.
+ *   scale_dev  in, DELAYED only: 1 float, the scale in force.
+ *   h          out: rows x cols of dtype (ldh), the new residual stream;
+ *              needed with a residual, may be NULL without.  h may be x or
+ *              residual itself (same leading dimension); it may not overlap
+ *              them otherwise.
+ *   rstd       out: rows floats, what qsg_rmsnorm_bwd reads; may be NULL
+ *              unless qt or the TENSORWISE recipe is asked for.
+ *   y          out: rows x cols of dtype (dense), y rounded to nearest even;
+ *              or NULL.
+ *   q, s       out: rows x cols FP8 bytes and their row-wise scales
+ *              (TENSORWISE: s = 3 floats {amax, scale, scale_inv}, needed for
+ *              either copy; DELAYED: s unused; MXFP8: uint8 rows x (cols/32),
+ *              cols % 32 == 0; 1X128: fp32 rows x (cols/128),
+ *              cols % 128 == 0); or NULL.
+ *   qt, st     out: the column-wise copy, cols x rows, as qsg_quantize
+ *              (MXFP8: rows % 32 == 0; 1X128: rows % 128 == 0); or NULL.
+ *   amax_out_dev  out, DELAYED only: 1 float, max |y| (for qsg_amax_update),
+ *              or NULL.
+ * One of y, q and qt is needed.  Pointers are aligned to their elements.
+ * One pass over the data row-wise; with qt or TENSORWISE a second kernel
+ * reads h (x without a residual) back.  rows == 0 or cols == 0 writes only
+ * TENSORWISE's s (amax 0) and DELAYED's amax (0).  A row of zeros with
+ * eps == 0, and a row that holds a NaN, give NaN; a row whose sum of squares
+ * overflows binary32 gives rstd = 0. */
+int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         int64_t ldr, const void* gamma, int gamma_dtype, float eps, const qsg_recipe* recipe,
+                         const float* scale_dev, void* h, int64_t ldh, float* rstd, void* y, uint8_t* q, void* s,
+                         uint8_t* qt, void* st, float* amax_out_dev, void* stream);
+
+/* Bytes of the workspace that qsg_rmsnorm_bwd needs for this shape (0 for an
+ * empty one), or a negative qsg_status. */
+int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* Backward of qsg_rmsnorm_quantize, through y (the quantization passes the
+ * gradient of its input unchanged).  With n = h rstd, per row
+ *
+ *     dx[c]     = rstd (dy[c] gamma[c] - n[c] sum_k(dy[k] gamma[k] n[k]) / cols) + dres[c]
+ *     dgamma[c] = sum over rows of dy[c] n[c]
+ *
+ * dx is the gradient of x and of the residual alike.
+ *   dy         rows x cols (dtype, lddy), the gradient of y (dgrad's output).
+ *   h, rstd    as qsg_rmsnorm_quantize left them (ldh); rstd holds rows floats.
+ *   dres       rows x cols (lddres), the gradient that reaches h by the
+ *              residual stream, or NULL.
+ *   gamma      cols weights of gamma_dtype.
+ *   dx         out: rows x cols of dtype (lddx), rounded once.  It may be dy
+ *              or dres itself (same leading dimension); it may not overlap
+ *              dy, dres or h otherwise.
+ *   dgamma     cols floats: written (accumulate = 0), or added to
+ *              (accumulate = 1: the fp32 main gradient); or NULL.
+ *   workspace  device memory of qsg_rmsnorm_bwd_workspace(rows, cols) bytes,
+ *              4-byte aligned; nothing has to be in it before, and calls that
+ *              overlap in time need one each.
+ * Sums are binary32 in an order that depends on the shape alone, so equal
+ * calls give equal bits.  rows == 0 writes dgamma = 0 unless accumulate. */
+int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
+                    int64_t lddy, int64_t ldh, int64_t lddres, const void* gamma, int gamma_dtype, const float* rstd,
+                    void* dx, int64_t lddx, float* dgamma, int accumulate, void* workspace, void* stream);
+
+/* One gradient tensor, or one chunk of it: n contiguous elements of dtype at
+ * g (device), and where its clipped values go (out may be g: in place; it may
+ * not overlap any other gradient). */
+typedef struct {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t dtype; /* qsg_dtype of g and out */
+  int32_t reserved;
+} qsg_grad;
+
+/* Bytes of the workspace of qsg_grad_sumsq. */
+#define QSG_GRAD_WORKSPACE_BYTES 8192
+
+/* Cuts a list of gradient tensors into chunks of one size (a host function:
+ * it touches no device).
+ *   list, count  host array of the tensors; out may be NULL where the table
+ *                is used by qsg_grad_sumsq alone.
+ *   chunks       host array for the table, or NULL to learn its length.
+ *   n_chunks     in: entries that chunks has room for (chunks not NULL);
+ *                out: entries of the table.
+ * The caller copies the table to device memory once and keeps it as long as
+ * the tensors stay where they are. */
+int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t* n_chunks);
+
+/* *sumsq_dev = sum of the squares of all gradients of a table, in binary64.
+ * Ranks that hold different gradients all-reduce it before qsg_grad_clip.
+ *   chunks_dev, n_chunks  a table of qsg_grad_plan in device memory.
+ *   workspace             QSG_GRAD_WORKSPACE_BYTES bytes of device memory,
+ *                         8-byte aligned; nothing has to be in it before, and
+ *                         calls that overlap in time need one each.
+ * The order of the sum depends on the table alone, so equal calls give equal
+ * bits. */
+int qsg_grad_sumsq(const qsg_grad* chunks_dev, int64_t n_chunks, double* sumsq_dev, void* workspace, void* stream);
+
+/* Clips by the global norm:
+ *
+ *     norm = fp32(sqrt(*sumsq_dev)),  k = min(1, max_norm / (norm + 1e-6)),
+ *     out  = g * k                    (binary32, rounded once to dtype)
+ *
+ *   sumsq_dev    in: 1 double.
+ *   max_norm     >= 0; infinity copies (or, in place, leaves) the gradients.
+ *   norm_out_dev out: 1 float, norm, or NULL.
+ * A NaN norm gives k = NaN and an infinite one k = 0, and so NaN where it
+ * meets an infinite gradient. */
+int qsg_grad_clip(const qsg_grad* chunks_dev, int64_t n_chunks, const double* sumsq_dev, float max_norm,
+                  float* norm_out_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

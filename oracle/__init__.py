@@ -70,3 +70,4 @@ from .activation import (  # noqa: F401
     act_fp8_store_bwd,
     elementwise_check,
 )
+from . import norm  # noqa: F401  (residual + RMS norm, its gradient, gradient clipping)

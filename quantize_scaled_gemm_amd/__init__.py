@@ -42,6 +42,12 @@ ENTRY_POINTS = (
     "qsg_wgrad_bf16",
     "qsg_quantize_nvfp4",
     "qsg_gemm_nvfp4",
+    "qsg_rmsnorm_quantize",
+    "qsg_rmsnorm_bwd_workspace",
+    "qsg_rmsnorm_bwd",
+    "qsg_grad_plan",
+    "qsg_grad_sumsq",
+    "qsg_grad_clip",
 )
 
 
@@ -52,6 +58,11 @@ class QsgError(RuntimeError):
 class Recipe(ctypes.Structure):
     _fields_ = [("scaling", ctypes.c_int32), ("fmt", ctypes.c_int32),
                 ("margin", ctypes.c_int32), ("mx_rule", ctypes.c_int32)]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -98,6 +109,15 @@ def load_library(path=LIB_PATH):
     lib.qsg_scaled_gemm_accumulate.argtypes = [P, I, I, P, P, I, I, P, I64, I64, I64, I64, I64, P, I64, P]
     lib.qsg_quantize_nvfp4.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P]
     lib.qsg_gemm_nvfp4.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I64, P, I, I64, P]
+    R = ctypes.POINTER(Recipe)
+    lib.qsg_rmsnorm_quantize.argtypes = [P, P, I, I64, I64, I64, I64, P, I, ctypes.c_float, R, F, P, I64, F, P, P, P,
+                                         P, P, F, P]
+    lib.qsg_rmsnorm_bwd_workspace.restype = I64
+    lib.qsg_rmsnorm_bwd_workspace.argtypes = [I64, I64]
+    lib.qsg_rmsnorm_bwd.argtypes = [P, P, P, I, I64, I64, I64, I64, I64, P, I, F, P, I64, F, I, P, P]
+    lib.qsg_grad_plan.argtypes = [ctypes.POINTER(Grad), I64, ctypes.POINTER(Grad), ctypes.POINTER(I64)]
+    lib.qsg_grad_sumsq.argtypes = [P, I64, P, P, P]
+    lib.qsg_grad_clip.argtypes = [P, I64, P, ctypes.c_float, P, P]
     _lib = lib
     return lib
 
@@ -140,7 +160,7 @@ def _matrix(t):
 
 def _buffer(t, name, numel, dtype, required=True):
     """Check a buffer the library reads or writes densely: on the GPU,
-    contiguous, exactly ``numel`` elements of ``dtype`` ("u8", "f32", "bf16").
+    contiguous, exactly ``numel`` elements of ``dtype`` ("u8", "f32", "bf16", "f64").
     Raw integer pointers are passed through unchecked (the C ABI's own
     contract applies to them)."""
     if t is None:
@@ -151,7 +171,7 @@ def _buffer(t, name, numel, dtype, required=True):
         return
     import torch
 
-    want = {"u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    want = {"u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16, "f64": torch.float64}[dtype]
     if not t.is_cuda:
         raise QsgError(f"{name} must live on the GPU")
     if t.dtype != want:
@@ -431,3 +451,153 @@ def qsg_gemm_nvfp4(a, sa, ts_a, b, sb, ts_b, c, stream=None):
     sdec_b = _ptr(ts_b) + 8 if not isinstance(ts_b, int) else ts_b
     _check(load_library().qsg_gemm_nvfp4(_ptr(a), _ptr(sa), sdec_a, _ptr(b), _ptr(sb), sdec_b, M, N, K, lda, ldb,
                                          _ptr(c), _dtype_code(c), ldc, _stream(stream)))
+
+
+def _rows(t, name):
+    """_matrix of a view whose rows do not overlap."""
+    rows, cols, ld = _matrix(t)
+    if rows > 1 and cols > 0 and t.stride(0) < cols:
+        raise QsgError(f"{name}: the rows overlap (stride {t.stride(0)} for {cols} columns)")
+    return rows, cols, ld
+
+
+def _same_matrix(t, name, like):
+    """(ld) of a matrix of the shape and type of ``like``."""
+    rows, cols, ld = _rows(t, name)
+    if t.shape != like.shape:
+        raise QsgError(f"{name} is {rows}x{cols}, expected {like.shape[0]}x{like.shape[1]}")
+    if t.dtype != like.dtype:
+        raise QsgError(f"{name} must be {like.dtype} (got {t.dtype})")
+    return ld
+
+
+def _workspace(t, nbytes):
+    if nbytes == 0 and t is None or isinstance(t, int):
+        return
+    if t is None:
+        raise QsgError("workspace is required")
+    if not t.is_cuda or not t.is_contiguous():
+        raise QsgError("workspace must be a contiguous GPU tensor")
+    if t.numel() * t.element_size() < nbytes:
+        raise QsgError(f"workspace must hold at least {nbytes} bytes")
+
+
+def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h=None, rstd=None, y=None, q=None,
+                         s=None, qt=None, st=None, scale=None, amax_out=None, margin=0, mx_rule=MX_CEIL, stream=None):
+    """h = x + residual; y = RMS norm of h times gamma; FP8 copies of y under a
+    recipe (scaling None: y only).  x, residual and h are 2-D with a unit
+    column stride; h may be x or residual itself.  gamma (cols) is fp32 or
+    bf16, rstd (rows) fp32; DELAYED takes its scale and returns amax_out."""
+    rows, cols, ld = _rows(x, "x")
+    dt = _dtype_code(x)
+    ldr = _same_matrix(residual, "residual", x) if residual is not None else 0
+    ldh = _same_matrix(h, "h", x) if h is not None else 0
+    gt = _dtype_code(gamma)
+    _buffer(gamma, "gamma", cols, "bf16" if gt == BF16 else "f32")
+    _buffer(rstd, "rstd", rows, "f32", required=False)
+    _buffer(y, "y", rows * cols, "bf16" if dt == BF16 else "f32", required=False)
+    _buffer(q, "q", rows * cols, "u8", required=False)
+    _buffer(qt, "qt", rows * cols, "u8", required=False)
+    _buffer(scale, "scale", 1, "f32", required=scaling == DELAYED)
+    _buffer(amax_out, "amax_out", 1, "f32", required=False)
+    if scaling == TENSORWISE:
+        _buffer(s, "s", 3, "f32")
+    elif scaling in (MXFP8, BLOCK_1X128):
+        row, col = _scale_layout(scaling, rows, cols), _scale_layout(scaling, cols, rows)
+        if row is not None and q is not None:
+            _buffer(s, "s", row[0], row[1])
+        if col is not None and qt is not None:
+            _buffer(st, "st", col[0], col[1])
+    rec = None if scaling is None else ctypes.byref(Recipe(scaling, fmt, margin, mx_rule))
+    _check(load_library().qsg_rmsnorm_quantize(_ptr(x), _ptr(residual), dt, rows, cols, ld, ldr, _ptr(gamma), gt, eps,
+                                               rec, _ptr(scale), _ptr(h), ldh, _ptr(rstd), _ptr(y), _ptr(q), _ptr(s),
+                                               _ptr(qt), _ptr(st), _ptr(amax_out), _stream(stream)))
+
+
+def qsg_rmsnorm_bwd_workspace(rows, cols):
+    """Bytes of the workspace of qsg_rmsnorm_bwd."""
+    n = load_library().qsg_rmsnorm_bwd_workspace(rows, cols)
+    if n < 0:
+        _check(n)
+    return n
+
+
+def qsg_rmsnorm_bwd(dy, h, gamma, rstd, dx, dres=None, dgamma=None, accumulate=False, workspace=None, stream=None):
+    """dx = gradient of x (and of the residual) from dy, the gradient of y, plus
+    dres, the gradient that reaches h directly; dgamma (cols fp32) written or
+    accumulated.  workspace: qsg_rmsnorm_bwd_workspace(rows, cols) bytes."""
+    rows, cols, lddy = _rows(dy, "dy")
+    dt = _dtype_code(dy)
+    ldh = _same_matrix(h, "h", dy)
+    lddx = _same_matrix(dx, "dx", dy)
+    lddres = _same_matrix(dres, "dres", dy) if dres is not None else 0
+    gt = _dtype_code(gamma)
+    _buffer(gamma, "gamma", cols, "bf16" if gt == BF16 else "f32")
+    _buffer(rstd, "rstd", rows, "f32")
+    _buffer(dgamma, "dgamma", cols, "f32", required=False)
+    _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))
+    _check(load_library().qsg_rmsnorm_bwd(_ptr(dy), _ptr(h), _ptr(dres), dt, rows, cols, lddy, ldh, lddres, _ptr(gamma),
+                                          gt, _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), 1 if accumulate else 0,
+                                          _ptr(workspace), _stream(stream)))
+
+
+GRAD_WORKSPACE_BYTES = 8192  # QSG_GRAD_WORKSPACE_BYTES of include/qsg.h
+
+
+class GradPlan:
+    """The chunk table of a list of gradients, on the GPU (``table``,
+    ``n_chunks``), with the tensors that it points into."""
+
+    def __init__(self, table, n_chunks, grads, outs):
+        self.table, self.n_chunks, self.grads, self.outs = table, n_chunks, grads, outs
+
+
+def qsg_grad_plan(grads, outs=None):
+    """GradPlan of contiguous fp32 or bf16 gradients of any shapes; clipped
+    values go to ``outs`` (same shapes and types; default: in place).  It is
+    made once for gradients that stay where they are, and keeps them alive."""
+    import torch
+
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise QsgError(f"{len(grads)} gradients, but {len(outs)} outputs")
+    for k, (g, o) in enumerate(zip(grads, outs)):
+        for t, name in ((g, "gradient"), (o, "output")):
+            if not t.is_cuda:
+                raise QsgError(f"{name} {k} must live on the GPU")
+            if not t.is_contiguous():
+                raise QsgError(f"{name} {k} must be contiguous")
+            if t.device != grads[0].device:
+                raise QsgError(f"{name} {k} is on {t.device}, the first gradient on {grads[0].device}")
+        if o.shape != g.shape or o.dtype != g.dtype:
+            raise QsgError(f"output {k} must have the shape and type of its gradient")
+    entries = (Grad * max(1, len(grads)))()
+    for k, (g, o) in enumerate(zip(grads, outs)):
+        entries[k] = Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g), 0)
+    n = ctypes.c_int64(0)
+    lib = load_library()
+    _check(lib.qsg_grad_plan(entries, len(grads), None, ctypes.byref(n)))
+    chunks = (Grad * max(1, n.value))()
+    _check(lib.qsg_grad_plan(entries, len(grads), chunks, ctypes.byref(n)))
+    host = torch.frombuffer(chunks, dtype=torch.uint8)
+    table = host.to(grads[0].device if grads else "cuda")
+    return GradPlan(table, n.value, grads, outs)
+
+
+def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
+    """sumsq (1 fp64 on the GPU) = sum of the squares of the plan's gradients.
+    workspace: GRAD_WORKSPACE_BYTES bytes on the GPU."""
+    _buffer(sumsq, "sumsq", 1, "f64")
+    _workspace(workspace, GRAD_WORKSPACE_BYTES)
+    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), _ptr(workspace),
+                                         _stream(stream)))
+
+
+def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
+    """The plan's outputs = gradients * min(1, max_norm / (norm + 1e-6)) with
+    norm = sqrt(sumsq), written to norm_out (1 fp32) if given."""
+    _buffer(sumsq, "sumsq", 1, "f64")
+    _buffer(norm_out, "norm_out", 1, "f32", required=False)
+    _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), max_norm, _ptr(norm_out),
+                                        _stream(stream)))

@@ -1,6 +1,7 @@
 // C ABI of libqsg.so (declared in include/qsg.h): argument validation, then
 // the launchers.  No exception crosses this boundary; nothing here allocates
 // device memory or synchronises with the device.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -341,6 +342,173 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
     if (lda < K / 2 || ldb < K / 2) return fail(QSG_ERR_ARG, "%s: lda/ldb < K/2 bytes", fn);
   }
   qsg::launch_gemm_nvfp4(a, sa, sdec_a_dev, b, sb, sdec_b_dev, M, N, K, lda, ldb, c, c_dtype, ldc, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         int64_t ldr, const void* gamma, int gamma_dtype, float eps, const qsg_recipe* recipe,
+                         const float* scale_dev, void* h, int64_t ldh, float* rstd, void* y, uint8_t* q, void* s,
+                         uint8_t* qt, void* st, float* amax_out_dev, void* stream) {
+  const char* fn = "qsg_rmsnorm_quantize";
+  int rc = check_matrix(fn, x, dtype, rows, cols, ldx);
+  if (rc) return rc;
+  if (!valid_dtype(gamma_dtype)) return fail(QSG_ERR_ARG, "%s: bad gamma dtype %d", fn, gamma_dtype);
+  if (!(eps >= 0.0f && eps <= FLT_MAX)) return fail(QSG_ERR_ARG, "%s: eps must be finite and not negative", fn);
+  const bool empty = rows == 0 || cols == 0;
+  const int esz = esize(dtype);
+  if (!empty) {
+    if (!gamma) return fail(QSG_ERR_ARG, "%s: null gamma", fn);
+    if (!aligned(gamma, esize(gamma_dtype))) return fail(QSG_ERR_ALIGN, "%s: gamma not aligned to its element size", fn);
+    if (residual) {
+      if (ldr < cols) return fail(QSG_ERR_ARG, "%s: ldr %lld < cols %lld", fn, (long long)ldr, (long long)cols);
+      if (!aligned(residual, esz)) return fail(QSG_ERR_ALIGN, "%s: residual not aligned to its element size", fn);
+      if (!h) return fail(QSG_ERR_ARG, "%s: a residual needs h", fn);
+    }
+    if (h) {
+      if (ldh < cols) return fail(QSG_ERR_ARG, "%s: ldh %lld < cols %lld", fn, (long long)ldh, (long long)cols);
+      if (!aligned(h, esz)) return fail(QSG_ERR_ALIGN, "%s: h not aligned to its element size", fn);
+      if ((h == x && ldh != ldx) || (h == residual && ldh != ldr))
+        return fail(QSG_ERR_ARG, "%s: h in place of an input needs its leading dimension", fn);
+    }
+    if (y && !aligned(y, esz)) return fail(QSG_ERR_ALIGN, "%s: y not aligned to its element size", fn);
+    if (!y && !q && !qt) return fail(QSG_ERR_ARG, "%s: y, q and qt are all null", fn);
+  }
+  if (rstd && !aligned(rstd, 4)) return fail(QSG_ERR_ALIGN, "%s: rstd not aligned", fn);
+  if (amax_out_dev && !aligned(amax_out_dev, 4)) return fail(QSG_ERR_ALIGN, "%s: amax_out not aligned", fn);
+  if (!recipe) {
+    if (q || qt) return fail(QSG_ERR_ARG, "%s: an FP8 output needs a recipe", fn);
+    if (amax_out_dev) return fail(QSG_ERR_ARG, "%s: amax_out belongs to the delayed recipe", fn);
+    if (empty) return QSG_OK;
+    qsg::launch_rmsnorm_quantize(x, residual, dtype, rows, cols, ldx, ldr, gamma, gamma_dtype, eps, -1, QSG_E4M3, 0,
+                                 true, nullptr, h, ldh, rstd, y, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                 as_stream(stream));
+    return check_launch(fn);
+  }
+  const int scaling = recipe->scaling, fmt = recipe->fmt, margin = recipe->margin;
+  if (!valid_fmt(fmt)) return fail(QSG_ERR_ARG, "%s: bad fmt %d", fn, fmt);
+  if (margin < 0 || margin > 64) return fail(QSG_ERR_ARG, "%s: margin %d outside [0, 64]", fn, margin);
+  if (scaling == QSG_BLOCK_128X128) return fail(QSG_ERR_UNSUPPORTED, "%s: 128x128 blocks are for weights", fn);
+  if (scaling < QSG_TENSORWISE || scaling > QSG_BLOCK_1X128) return fail(QSG_ERR_ARG, "%s: bad scaling %d", fn, scaling);
+  if (amax_out_dev && scaling != QSG_DELAYED)
+    return fail(QSG_ERR_ARG, "%s: amax_out belongs to the delayed recipe", fn);
+  if (!empty && !q && !qt) return fail(QSG_ERR_ARG, "%s: q and qt are both null", fn);
+  if (!empty && !rstd && (qt || scaling == QSG_TENSORWISE))
+    return fail(QSG_ERR_ARG, "%s: qt and the tensorwise recipe need rstd", fn);
+  if (scaling == QSG_TENSORWISE) {
+    if (!s) return fail(QSG_ERR_ARG, "%s: tensorwise needs s = {amax, scale, scale_inv}", fn);
+    if (!aligned(s, 4)) return fail(QSG_ERR_ALIGN, "%s: s not aligned", fn);
+  } else if (scaling == QSG_DELAYED) {
+    if (!scale_dev) return fail(QSG_ERR_ARG, "%s: null scale", fn);
+    if (!aligned(scale_dev, 4)) return fail(QSG_ERR_ALIGN, "%s: scale not aligned", fn);
+  } else {
+    if (scaling == QSG_MXFP8 && recipe->mx_rule != QSG_MX_CEIL && recipe->mx_rule != QSG_MX_OCP_FLOOR)
+      return fail(QSG_ERR_ARG, "%s: bad mx_rule %d", fn, recipe->mx_rule);
+    if (empty) return QSG_OK;
+    if ((q && !s) || (qt && !st)) return fail(QSG_ERR_ARG, "%s: a requested copy has a null scale tensor", fn);
+    if (scaling == QSG_BLOCK_1X128 && ((s && !aligned(s, 4)) || (st && !aligned(st, 4))))
+      return fail(QSG_ERR_ALIGN, "%s: fp32 scales not aligned", fn);
+    const int64_t B = scaling == QSG_MXFP8 ? 32 : 128;
+    if (q && cols % B)
+      return fail(QSG_ERR_SHAPE, "%s: row-wise blocks need cols %% %lld == 0 (cols %lld)", fn, (long long)B, (long long)cols);
+    if (qt && rows % B)
+      return fail(QSG_ERR_SHAPE, "%s: column-wise blocks need rows %% %lld == 0 (rows %lld)", fn, (long long)B, (long long)rows);
+  }
+  qsg::launch_rmsnorm_quantize(x, residual, dtype, rows, cols, ldx, ldr, gamma, gamma_dtype, eps, scaling, fmt, margin,
+                               recipe->mx_rule == QSG_MX_CEIL, scale_dev, h, ldh, rstd, y, q, s, qt, st, amax_out_dev,
+                               as_stream(stream));
+  return check_launch(fn);
+}
+
+int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0)
+    return fail(QSG_ERR_ARG, "qsg_rmsnorm_bwd_workspace: negative shape %lld x %lld", (long long)rows, (long long)cols);
+  return qsg::rmsnorm_bwd_workspace(rows, cols);
+}
+
+int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
+                    int64_t lddy, int64_t ldh, int64_t lddres, const void* gamma, int gamma_dtype, const float* rstd,
+                    void* dx, int64_t lddx, float* dgamma, int accumulate, void* workspace, void* stream) {
+  const char* fn = "qsg_rmsnorm_bwd";
+  int rc = check_matrix(fn, dy, dtype, rows, cols, lddy);
+  if (rc) return rc;
+  rc = check_matrix(fn, h, dtype, rows, cols, ldh);
+  if (rc) return rc;
+  if (!valid_dtype(gamma_dtype)) return fail(QSG_ERR_ARG, "%s: bad gamma dtype %d", fn, gamma_dtype);
+  if (dgamma && !aligned(dgamma, 4)) return fail(QSG_ERR_ALIGN, "%s: dgamma not aligned", fn);
+  if (rows > 0 && cols > 0) {
+    const int esz = esize(dtype);
+    if (!gamma || !rstd || !dx || !workspace) return fail(QSG_ERR_ARG, "%s: null pointer", fn);
+    if (!aligned(gamma, esize(gamma_dtype))) return fail(QSG_ERR_ALIGN, "%s: gamma not aligned to its element size", fn);
+    if (!aligned(rstd, 4) || !aligned(workspace, 4)) return fail(QSG_ERR_ALIGN, "%s: rstd or workspace not aligned", fn);
+    if (!aligned(dx, esz)) return fail(QSG_ERR_ALIGN, "%s: dx not aligned to its element size", fn);
+    if (lddx < cols) return fail(QSG_ERR_ARG, "%s: lddx %lld < cols %lld", fn, (long long)lddx, (long long)cols);
+    if (dres) {
+      if (lddres < cols) return fail(QSG_ERR_ARG, "%s: lddres %lld < cols %lld", fn, (long long)lddres, (long long)cols);
+      if (!aligned(dres, esz)) return fail(QSG_ERR_ALIGN, "%s: dres not aligned to its element size", fn);
+    }
+    if (dx == h) return fail(QSG_ERR_ARG, "%s: dx may not be h", fn);
+    if ((dx == dy && lddx != lddy) || (dx == dres && lddx != lddres))
+      return fail(QSG_ERR_ARG, "%s: dx in place of an input needs its leading dimension", fn);
+  }
+  if (cols == 0 || (rows == 0 && (!dgamma || accumulate))) return QSG_OK;  // nothing to write
+  qsg::launch_rmsnorm_bwd(dy, h, dres, dtype, rows, cols, lddy, ldh, lddres, gamma, gamma_dtype, rstd, dx, lddx, dgamma,
+                          accumulate != 0, workspace, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t* n_chunks) {
+  const char* fn = "qsg_grad_plan";
+  constexpr int64_t kChunk = 32768;  // elements
+  if (!n_chunks || count < 0 || (count > 0 && !list)) return fail(QSG_ERR_ARG, "%s: null list or negative count", fn);
+  int64_t total = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const qsg_grad& t = list[k];
+    if (!valid_dtype(t.dtype)) return fail(QSG_ERR_ARG, "%s: tensor %lld: bad dtype %d", fn, (long long)k, t.dtype);
+    if (t.n < 0) return fail(QSG_ERR_ARG, "%s: tensor %lld: negative length", fn, (long long)k);
+    if (t.n > 0 && !t.g) return fail(QSG_ERR_ARG, "%s: tensor %lld: null pointer", fn, (long long)k);
+    if (!aligned(t.g, esize(t.dtype)) || !aligned(t.out, esize(t.dtype)))
+      return fail(QSG_ERR_ALIGN, "%s: tensor %lld not aligned to its element size", fn, (long long)k);
+    total += (t.n + kChunk - 1) / kChunk;
+  }
+  const int64_t room = *n_chunks;
+  *n_chunks = total;
+  if (!chunks) return QSG_OK;
+  if (room < total)
+    return fail(QSG_ERR_ARG, "%s: the table needs %lld entries, there is room for %lld", fn, (long long)total, (long long)room);
+  for (int64_t k = 0; k < count; ++k) {
+    const qsg_grad& t = list[k];
+    const int64_t esz = esize(t.dtype);
+    for (int64_t at = 0; at < t.n; at += kChunk) {
+      qsg_grad c = t;
+      c.g = reinterpret_cast<const char*>(t.g) + at * esz;
+      c.out = t.out ? reinterpret_cast<char*>(t.out) + at * esz : nullptr;
+      c.n = t.n - at < kChunk ? t.n - at : kChunk;
+      c.reserved = 0;
+      *chunks++ = c;
+    }
+  }
+  return QSG_OK;
+}
+
+int qsg_grad_sumsq(const qsg_grad* chunks_dev, int64_t n_chunks, double* sumsq_dev, void* workspace, void* stream) {
+  const char* fn = "qsg_grad_sumsq";
+  if (n_chunks < 0 || (n_chunks > 0 && !chunks_dev)) return fail(QSG_ERR_ARG, "%s: null table or negative length", fn);
+  if (!sumsq_dev || !workspace) return fail(QSG_ERR_ARG, "%s: null pointer", fn);
+  if (!aligned(sumsq_dev, 8) || !aligned(workspace, 8) || !aligned(chunks_dev, 8))
+    return fail(QSG_ERR_ALIGN, "%s: a pointer is not 8-byte aligned", fn);
+  qsg::launch_grad_sumsq(chunks_dev, n_chunks, sumsq_dev, reinterpret_cast<double*>(workspace), as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_grad_clip(const qsg_grad* chunks_dev, int64_t n_chunks, const double* sumsq_dev, float max_norm,
+                  float* norm_out_dev, void* stream) {
+  const char* fn = "qsg_grad_clip";
+  if (n_chunks < 0 || (n_chunks > 0 && !chunks_dev)) return fail(QSG_ERR_ARG, "%s: null table or negative length", fn);
+  if (!sumsq_dev) return fail(QSG_ERR_ARG, "%s: null sumsq", fn);
+  if (!(max_norm >= 0.0f)) return fail(QSG_ERR_ARG, "%s: max_norm must not be negative or NaN", fn);
+  if (!aligned(sumsq_dev, 8) || !aligned(chunks_dev, 8)) return fail(QSG_ERR_ALIGN, "%s: a pointer is not 8-byte aligned", fn);
+  if (norm_out_dev && !aligned(norm_out_dev, 4)) return fail(QSG_ERR_ALIGN, "%s: norm_out not aligned", fn);
+  qsg::launch_grad_clip(chunks_dev, n_chunks, sumsq_dev, max_norm, norm_out_dev, as_stream(stream));
   return check_launch(fn);
 }
 

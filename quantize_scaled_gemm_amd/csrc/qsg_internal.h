@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "qsg.h"
+
 namespace qsg {
 
 void launch_fill_u32(uint32_t* p, uint32_t v, int n, hipStream_t st);
@@ -79,5 +81,27 @@ bool launch_gemm_nvfp4_fast(const uint8_t* a, const uint8_t* sa, const float* ta
 void launch_scaled_gemm(const uint8_t* a, int fa, int ka, const void* sa, const uint8_t* b, int fb,
                         int kb, const void* sb, int64_t M, int64_t N, int64_t K, int64_t lda,
                         int64_t ldb, void* c, int c_dtype, int64_t ldc, bool accumulate, hipStream_t st);
+
+// Residual addition + RMS norm with an FP8 output (scaling < 0: none): one
+// pass, or two where a transposed copy or the current scaling is asked for.
+void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                             int64_t ldr, const void* gamma, int gamma_dtype, float eps, int scaling, int fmt,
+                             int margin, bool mx_ceil, const float* scale, void* h, int64_t ldh, float* rstd, void* y,
+                             uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out, hipStream_t st);
+void launch_quantize_normed(const void* h, int dtype, int64_t rows, int64_t cols, int64_t ld, const float* rstd,
+                            const void* gamma, int gamma_dtype, int scaling, int fmt, int margin, bool mx_ceil,
+                            const float* scale, uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out,
+                            hipStream_t st);
+// Backward of the norm; workspace of rmsnorm_bwd_workspace(rows, cols) bytes.
+int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
+                        int64_t lddy, int64_t ldh, int64_t lddres, const void* gamma, int gamma_dtype,
+                        const float* rstd, void* dx, int64_t lddx, float* dgamma, bool accumulate, void* workspace,
+                        hipStream_t st);
+// Sum of squares of the gradients of a table of chunks in device memory, and
+// out = g min(1, max_norm / (norm + 1e-6)).
+void launch_grad_sumsq(const qsg_grad* table, int64_t n, double* sumsq, double* partial, hipStream_t st);
+void launch_grad_clip(const qsg_grad* table, int64_t n, const double* sumsq, float max_norm, float* norm_out,
+                      hipStream_t st);
 
 }  // namespace qsg
