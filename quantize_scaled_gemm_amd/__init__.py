@@ -462,24 +462,41 @@ def _rows(t, name):
 
 
 def _same_matrix(t, name, like):
-    """(ld) of a matrix of the shape and type of ``like``."""
+    """(pointer, ld) of a matrix of the shape and type of ``like``."""
+    if t is None:
+        return None, 0
     rows, cols, ld = _rows(t, name)
     if t.shape != like.shape:
         raise QsgError(f"{name} is {rows}x{cols}, expected {like.shape[0]}x{like.shape[1]}")
     if t.dtype != like.dtype:
         raise QsgError(f"{name} must be {like.dtype} (got {t.dtype})")
-    return ld
+    return _ptr(t), ld
+
+
+def _dense(t, name, numel, dtype):
+    """Pointer of an optional buffer that _buffer accepts."""
+    if t is None or isinstance(t, int):
+        return t
+    _buffer(t, name, numel, dtype)
+    return t.data_ptr()
+
+
+def _weight(gamma, cols):
+    """(pointer, type) of a norm's weight."""
+    dt = _dtype_code(gamma)
+    return _dense(gamma, "gamma", cols, "bf16" if dt == BF16 else "f32"), dt
 
 
 def _workspace(t, nbytes):
-    if nbytes == 0 and t is None or isinstance(t, int):
-        return
+    if isinstance(t, int) or (t is None and nbytes == 0):
+        return t
     if t is None:
         raise QsgError("workspace is required")
     if not t.is_cuda or not t.is_contiguous():
         raise QsgError("workspace must be a contiguous GPU tensor")
     if t.numel() * t.element_size() < nbytes:
         raise QsgError(f"workspace must hold at least {nbytes} bytes")
+    return t.data_ptr()
 
 
 def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h=None, rstd=None, y=None, q=None,
@@ -490,28 +507,35 @@ def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h
     bf16, rstd (rows) fp32; DELAYED takes its scale and returns amax_out."""
     rows, cols, ld = _rows(x, "x")
     dt = _dtype_code(x)
-    ldr = _same_matrix(residual, "residual", x) if residual is not None else 0
-    ldh = _same_matrix(h, "h", x) if h is not None else 0
-    gt = _dtype_code(gamma)
-    _buffer(gamma, "gamma", cols, "bf16" if gt == BF16 else "f32")
-    _buffer(rstd, "rstd", rows, "f32", required=False)
-    _buffer(y, "y", rows * cols, "bf16" if dt == BF16 else "f32", required=False)
-    _buffer(q, "q", rows * cols, "u8", required=False)
-    _buffer(qt, "qt", rows * cols, "u8", required=False)
-    _buffer(scale, "scale", 1, "f32", required=scaling == DELAYED)
-    _buffer(amax_out, "amax_out", 1, "f32", required=False)
-    if scaling == TENSORWISE:
+    numel = rows * cols
+    pr, ldr = _same_matrix(residual, "residual", x)
+    ph, ldh = _same_matrix(h, "h", x)
+    pg, gt = _weight(gamma, cols)
+    prstd = _dense(rstd, "rstd", rows, "f32")
+    py = _dense(y, "y", numel, "bf16" if dt == BF16 else "f32")
+    pq, pqt = _dense(q, "q", numel, "u8"), _dense(qt, "qt", numel, "u8")
+    pa = _dense(amax_out, "amax_out", 1, "f32")
+    psc = ps = pst = None
+    if scaling == DELAYED:
+        _buffer(scale, "scale", 1, "f32")
+        psc = _ptr(scale)
+    elif scaling == TENSORWISE:
         _buffer(s, "s", 3, "f32")
+        ps = _ptr(s)
     elif scaling in (MXFP8, BLOCK_1X128):
+        # a shape that breaks the block rule is the library's to refuse
         row, col = _scale_layout(scaling, rows, cols), _scale_layout(scaling, cols, rows)
-        if row is not None and q is not None:
-            _buffer(s, "s", row[0], row[1])
-        if col is not None and qt is not None:
-            _buffer(st, "st", col[0], col[1])
+        if q is not None:
+            if row is not None:
+                _buffer(s, "s", row[0], row[1])
+            ps = _ptr(s)
+        if qt is not None:
+            if col is not None:
+                _buffer(st, "st", col[0], col[1])
+            pst = _ptr(st)
     rec = None if scaling is None else ctypes.byref(Recipe(scaling, fmt, margin, mx_rule))
-    _check(load_library().qsg_rmsnorm_quantize(_ptr(x), _ptr(residual), dt, rows, cols, ld, ldr, _ptr(gamma), gt, eps,
-                                               rec, _ptr(scale), _ptr(h), ldh, _ptr(rstd), _ptr(y), _ptr(q), _ptr(s),
-                                               _ptr(qt), _ptr(st), _ptr(amax_out), _stream(stream)))
+    _check(load_library().qsg_rmsnorm_quantize(_ptr(x), pr, dt, rows, cols, ld, ldr, pg, gt, eps, rec, psc, ph, ldh,
+                                               prstd, py, pq, ps, pqt, pst, pa, _stream(stream)))
 
 
 def qsg_rmsnorm_bwd_workspace(rows, cols):
@@ -528,17 +552,15 @@ def qsg_rmsnorm_bwd(dy, h, gamma, rstd, dx, dres=None, dgamma=None, accumulate=F
     accumulated.  workspace: qsg_rmsnorm_bwd_workspace(rows, cols) bytes."""
     rows, cols, lddy = _rows(dy, "dy")
     dt = _dtype_code(dy)
-    ldh = _same_matrix(h, "h", dy)
-    lddx = _same_matrix(dx, "dx", dy)
-    lddres = _same_matrix(dres, "dres", dy) if dres is not None else 0
-    gt = _dtype_code(gamma)
-    _buffer(gamma, "gamma", cols, "bf16" if gt == BF16 else "f32")
-    _buffer(rstd, "rstd", rows, "f32")
-    _buffer(dgamma, "dgamma", cols, "f32", required=False)
-    _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))
-    _check(load_library().qsg_rmsnorm_bwd(_ptr(dy), _ptr(h), _ptr(dres), dt, rows, cols, lddy, ldh, lddres, _ptr(gamma),
-                                          gt, _ptr(rstd), _ptr(dx), lddx, _ptr(dgamma), 1 if accumulate else 0,
-                                          _ptr(workspace), _stream(stream)))
+    ph, ldh = _same_matrix(h, "h", dy)
+    pdx, lddx = _same_matrix(dx, "dx", dy)
+    pdr, lddres = _same_matrix(dres, "dres", dy)
+    pg, gt = _weight(gamma, cols)
+    prstd = _dense(rstd, "rstd", rows, "f32")
+    pdg = _dense(dgamma, "dgamma", cols, "f32")
+    pw = _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))
+    _check(load_library().qsg_rmsnorm_bwd(_ptr(dy), ph, pdr, dt, rows, cols, lddy, ldh, lddres, pg, gt, prstd, pdx,
+                                          lddx, pdg, 1 if accumulate else 0, pw, _stream(stream)))
 
 
 GRAD_WORKSPACE_BYTES = 8192  # QSG_GRAD_WORKSPACE_BYTES of include/qsg.h
@@ -589,9 +611,8 @@ def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
     """sumsq (1 fp64 on the GPU) = sum of the squares of the plan's gradients.
     workspace: GRAD_WORKSPACE_BYTES bytes on the GPU."""
     _buffer(sumsq, "sumsq", 1, "f64")
-    _workspace(workspace, GRAD_WORKSPACE_BYTES)
-    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), _ptr(workspace),
-                                         _stream(stream)))
+    ws = _workspace(workspace, GRAD_WORKSPACE_BYTES)
+    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), ws, _stream(stream)))
 
 
 def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):

@@ -17,6 +17,7 @@
 // that ask only for the element's alignment (gfx950 takes global accesses at
 // any byte address), so odd leading dimensions and offsets use the same
 // instructions.
+#include <float.h>
 #include <hip/hip_runtime.h>
 
 #include "qsg_device.h"
@@ -28,11 +29,41 @@ namespace {
 
 // vector accesses at any element's address
 typedef u32x4 u32x4_e __attribute__((aligned(2)));
+typedef u32x4 u32x4_b __attribute__((aligned(1)));
 typedef u32x2 u32x2_e __attribute__((aligned(1)));
+typedef uint32_t u32_b __attribute__((aligned(1)));
 
 // ---------------------------------------------------------------------------
 // chunks of 8 elements, and single ones
 // ---------------------------------------------------------------------------
+// STREAM: a non-temporal store, for what the call does not read back.  What
+// the second pass reads (h, or q) is stored plainly and stays in the caches as
+// far as they reach.
+template <bool STREAM>
+__device__ __forceinline__ void keep_apart() {
+  // a comment before and after each store: the compiler otherwise merges a
+  // plain and a streaming store in two branches into one plain store
+  asm volatile("; streaming %0" : : "n"(STREAM));
+}
+template <bool STREAM>
+__device__ __forceinline__ void put16(void* p, u32x4 v) {
+  keep_apart<STREAM>();
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_b*>(p));
+  else
+    *reinterpret_cast<u32x4_b*>(p) = v;
+  keep_apart<STREAM>();
+}
+template <bool STREAM>
+__device__ __forceinline__ void put8(void* p, u32x2 v) {
+  keep_apart<STREAM>();
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x2_e*>(p));
+  else
+    *reinterpret_cast<u32x2_e*>(p) = v;
+  keep_apart<STREAM>();
+}
+
 template <typename In>
 struct Chunk;
 
@@ -44,14 +75,21 @@ struct Chunk<uint16_t> {  // bf16 bit patterns
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
   }
+  // the words become new values to the compiler, which would otherwise keep
+  // the 8 widened values of an earlier use in registers beside them
+  __device__ __forceinline__ void forget_wide() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) asm("" : "+v"(w[k]));
+  }
   __device__ __forceinline__ void load(const uint16_t* p, bool valid) {
     u32x4 u = {0, 0, 0, 0};
     if (valid) u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(p));
     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
   }
+  template <bool STREAM>
   __device__ __forceinline__ void store(uint16_t* p) const {
     const u32x4 u = {w[0], w[1], w[2], w[3]};
-    *reinterpret_cast<u32x4_e*>(p) = u;
+    put16<STREAM>(p, u);
   }
 };
 
@@ -63,6 +101,7 @@ struct Chunk<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
   }
+  __device__ __forceinline__ void forget_wide() {}
   __device__ __forceinline__ void load(const float* p, bool valid) {
     u32x4 u = {0, 0, 0, 0}, v = {0, 0, 0, 0};
     if (valid) {
@@ -72,10 +111,11 @@ struct Chunk<float> {
     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
     w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
   }
+  template <bool STREAM>
   __device__ __forceinline__ void store(float* p) const {
     const u32x4 u = {w[0], w[1], w[2], w[3]}, v = {w[4], w[5], w[6], w[7]};
-    *reinterpret_cast<u32x4_e*>(p) = u;
-    *reinterpret_cast<u32x4_e*>(p + 4) = v;
+    put16<STREAM>(p, u);
+    put16<STREAM>(p + 4, v);
   }
 };
 
@@ -134,10 +174,11 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
 }
 
-// Sum over the TPR threads that share a row.  For TPR > 64 they are a whole
-// workgroup, `red` is one of two LDS buffers used in turn, and one barrier
-// suffices: a wave writes a buffer again only after the barrier of the call
-// between, which every wave passes after its reads.
+// Sum over the TPR threads (consecutive ones of the workgroup) that share a
+// row.  For TPR > 64 every thread of the workgroup calls this together, `red`
+// is one of two LDS buffers used in turn, and one barrier suffices: a wave
+// writes a buffer again only after the barrier of the call between, which
+// every wave passes after its reads.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
   v = wave_sum(v);
@@ -145,6 +186,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     constexpr int W = TPR / 64;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
+    red += threadIdx.x / TPR * W;
     v = red[0];
 #pragma unroll
     for (int i = 1; i < W; ++i) v += red[i];
@@ -173,6 +215,7 @@ struct NormArgs {
   uint8_t* q;          // dense, or null
   void* s;
   uint32_t* amax_out;  // max |y| bits, or null
+  bool second, again;  // the second pass reads h, or q, back
 };
 
 template <int FMT>
@@ -182,16 +225,32 @@ __device__ __forceinline__ u32x2 enc8(const float (&y)[8], float s) {
   return v;
 }
 
-// Outputs of one chunk of normalised values at row `row`, column c.  A block
-// is made of whole chunks of neighbouring lanes, all of them inside the row
-// (valid) or all outside.
+// Where a row's outputs begin.  Uniform in a wave: the address of a chunk is a
+// scalar base and a 32-bit offset.
 template <typename In>
-__device__ __forceinline__ void emit(const NormArgs& a, int64_t row, int64_t c, bool valid, const float (&y)[8],
-                                     float tscale, uint32_t& amax) {
+struct RowOut {
+  In* y;
+  uint8_t* q;
+  void* s;
+  __device__ __forceinline__ RowOut(const NormArgs& a, int64_t row) {
+    y = reinterpret_cast<In*>(a.y) + (a.y ? row * a.cols : 0);
+    q = a.q + (a.q ? row * a.cols : 0);
+    s = nullptr;
+    if (a.quant == Q_MX) s = reinterpret_cast<uint8_t*>(a.s) + row * (a.cols / 32);
+    if (a.quant == Q_BLOCK) s = reinterpret_cast<float*>(a.s) + row * (a.cols / 128);
+  }
+};
+
+// Outputs of one chunk of normalised values at column c.  A block is made of
+// whole chunks of neighbouring lanes, all of them inside the row (valid) or
+// all outside.
+template <typename In>
+__device__ __forceinline__ void emit(const NormArgs& a, const RowOut<In>& out, uint32_t c, bool valid,
+                                     const float (&y)[8], float tscale, uint32_t& amax) {
   if (a.y && valid) {
     Chunk<In> o;
     o.set(y);
-    o.store(reinterpret_cast<In*>(a.y) + row * a.cols + c);
+    o.template store<true>(out.y + c);
   }
   uint32_t m = 0;
 #pragma unroll
@@ -205,78 +264,110 @@ __device__ __forceinline__ void emit(const NormArgs& a, int64_t row, int64_t c, 
     const int e = mx_exponent(m, a.fmt == kE4M3 ? Fp8Traits<kE4M3>::kEmaxElem : Fp8Traits<kE5M2>::kEmaxElem,
                               a.mx_ceil, a.margin);
     s = pow2_neg(e);
-    if ((threadIdx.x & 3) == 0 && valid)
-      reinterpret_cast<uint8_t*>(a.s)[row * (a.cols / 32) + (c >> 5)] = (uint8_t)(e + 127);
+    if ((threadIdx.x & 3) == 0 && valid) reinterpret_cast<uint8_t*>(out.s)[c >> 5] = (uint8_t)(e + 127);
   } else if (a.quant == Q_BLOCK) {
     m = group_max_u32<0xF>(m);
     m = m > 0x7F800000u ? 0x7FC00000u : m;
     s = scale_from_amax(__uint_as_float(m), fp8_max(a.fmt), a.margin);
-    if ((threadIdx.x & 15) == 0 && valid)
-      reinterpret_cast<float*>(a.s)[row * (a.cols / 128) + (c >> 7)] = __fdiv_rn(1.0f, s);
+    if ((threadIdx.x & 15) == 0 && valid) reinterpret_cast<float*>(out.s)[c >> 7] = __fdiv_rn(1.0f, s);
   }
   const u32x2 v = a.fmt == kE4M3 ? enc8<kE4M3>(y, s) : enc8<kE5M2>(y, s);
-  if (valid) __builtin_nontemporal_store(v, reinterpret_cast<u32x2_e*>(a.q + row * a.cols + c));
+  if (valid) {
+    if (a.again)
+      put8<false>(out.q + c, v);
+    else
+      put8<true>(out.q + c, v);
+  }
 }
 
 // Outputs of one element after the last whole chunk (never in a block).
 template <typename In>
-__device__ __forceinline__ void emit1(const NormArgs& a, int64_t row, int64_t c, float y, float tscale,
+__device__ __forceinline__ void emit1(const NormArgs& a, const RowOut<In>& out, uint32_t c, float y, float tscale,
                                       uint32_t& amax) {
-  if (a.y) store1(reinterpret_cast<In*>(a.y) + row * a.cols + c, y);
+  if (a.y) store1(out.y + c, y);
   amax = umax_u32(amax, __float_as_uint(y) & 0x7FFFFFFFu);
   if (a.quant == Q_NONE) return;
   const float v = y * tscale;
-  a.q[row * a.cols + c] = (uint8_t)(a.fmt == kE4M3 ? enc4<kE4M3>(v, 0, 0, 0) : enc4<kE5M2>(v, 0, 0, 0));
+  out.q[c] = (uint8_t)(a.fmt == kE4M3 ? enc4<kE4M3>(v, 0, 0, 0) : enc4<kE5M2>(v, 0, 0, 0));
 }
 
 __device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)cols) + eps));
 }
 
-// One pass: TPR threads hold a row in registers, NCH chunks each.
-template <typename In, int TPR, int NCH>
-__global__ __launch_bounds__(256) void norm_row_kernel(NormArgs a) {
-  constexpr int RPW = 256 / TPR;
-  __shared__ float red[2][4];
+// One pass: TPR threads hold a row in registers, NCH chunks each; a workgroup
+// of BLK threads takes BLK / TPR rows at a time.
+template <typename In, int TPR, int NCH, int BLK>
+__global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
+  constexpr int RPW = BLK / TPR;
+  constexpr bool EARLY = NCH <= 2;  // the weights fit beside the row: loaded once, before the first row arrives
+  __shared__ float red[2][16];
   const int t = threadIdx.x % TPR;
-  const int sub = TPR == 256 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);  // uniform in a wave
-  const int chunks = (int)(a.cols / 8), rest = (int)(a.cols % 8);
+  const int sub = RPW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);  // uniform in a wave
+  const int all_chunks = (int)(a.cols / 8), all_rest = (int)(a.cols % 8);
   const float tscale = a.quant == Q_TENSOR ? *a.scale : 1.0f;
   uint32_t amax = 0;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < a.rows; row += (int64_t)gridDim.x * RPW, turn ^= 1) {
+  const bool outputs = a.quant != Q_NONE || a.y || a.amax_out;
+  float ge[EARLY ? NCH : 1][8], g1 = 0.0f;
+  if (EARLY && outputs) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const uint32_t k = j * TPR + t;
+      load_gamma(ge[j], a.gamma, a.gamma_bf16, k * 8, k < (uint32_t)all_chunks);
+    }
+  }
+  if (t < all_rest && outputs) g1 = load_gamma1(a.gamma, a.gamma_bf16, all_chunks * 8 + t);
+  for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.rows; row0 += (int64_t)gridDim.x * RPW, turn ^= 1) {
+    // with barriers in the loop the last workgroup's spare threads stay in it, on a row that is not there
+    const int64_t row = row0 + sub;
+    const bool there = RPW == 1 || row < a.rows;
+    if (TPR == 64 && !there) break;
+    const int chunks = there ? all_chunks : 0, rest = there ? all_rest : 0;
     const In* x = reinterpret_cast<const In*>(a.x) + row * a.ldx;
     const In* r = reinterpret_cast<const In*>(a.r) + row * a.ldr;
     In* ho = reinterpret_cast<In*>(a.h) + row * a.ldh;
     Chunk<In> h[NCH];
     float h1 = 0.0f;  // the element after the last whole chunk
-#pragma unroll
-    for (int j = 0; j < NCH; ++j) {
-      const uint32_t k = j * TPR + t;
-      h[j].load(x + k * 8, k < (uint32_t)chunks);
-    }
     if (t < rest) h1 = load1(x + chunks * 8 + t);
-    if (a.r) {
-      Chunk<In> d[NCH];
+    if (!a.r) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const uint32_t k = j * TPR + t;
-        d[j].load(r + k * 8, k < (uint32_t)chunks);
+        h[j].load(x + k * 8, k < (uint32_t)chunks);
+      }
+    } else {
+      // at most 8 chunks of each at a time: 16 loads in flight in each lane
+      constexpr int PART = NCH < 8 ? NCH : 8;
+#pragma unroll
+      for (int j0 = 0; j0 < NCH; j0 += PART) {
+        Chunk<In> d[PART];
+#pragma unroll
+        for (int j = 0; j < PART; ++j) {
+          const uint32_t k = (j0 + j) * TPR + t;
+          h[j0 + j].load(x + k * 8, k < (uint32_t)chunks);
+          d[j].load(r + k * 8, k < (uint32_t)chunks);
+        }
+#pragma unroll
+        for (int j = 0; j < PART; ++j) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = h[j0 + j].at(i) + d[j].at(i);
+          h[j0 + j].set(v);
+        }
       }
       if (t < rest) h1 = round1(x, h1 + load1(r + chunks * 8 + t));
-#pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = h[j].at(i) + d[j].at(i);
-        h[j].set(v);
-      }
     }
     if (a.h) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const uint32_t k = j * TPR + t;
-        if (k < (uint32_t)chunks) h[j].store(ho + k * 8);
+        if (k < (uint32_t)chunks) {
+          if (a.second)
+            h[j].template store<false>(ho + k * 8);
+          else
+            h[j].template store<true>(ho + k * 8);
+        }
       }
       if (t < rest) store1(ho + chunks * 8 + t, h1);
     }
@@ -287,26 +378,31 @@ __global__ __launch_bounds__(256) void norm_row_kernel(NormArgs a) {
       for (int i = 0; i < 8; ++i) ss = fmaf(h[j].at(i), h[j].at(i), ss);
     ss = row_sum<TPR>(ss, red[turn]);
     const float rstd = rstd_of(ss, a.cols, a.eps);
-    if (a.rstd && t == 0) a.rstd[row] = rstd;
-    if (a.quant == Q_NONE && !a.y && !a.amax_out) continue;
+    if (a.rstd && t == 0 && there) a.rstd[row] = rstd;
+    if (!outputs || !there) continue;
+    const RowOut<In> out(a, row);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const uint32_t k = j * TPR + t;
       const bool valid = k < (uint32_t)chunks;
       float g[8], y[8];
-      load_gamma(g, a.gamma, a.gamma_bf16, k * 8, valid);
+      h[j].forget_wide();
+      if constexpr (EARLY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = ge[j][i];
+      } else {
+        load_gamma(g, a.gamma, a.gamma_bf16, k * 8, valid);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = h[j].at(i) * rstd * g[i];
-      emit<In>(a, row, k * 8, valid, y, tscale, amax);
+      emit<In>(a, out, k * 8, valid, y, tscale, amax);
+      __builtin_amdgcn_sched_barrier(0);  // one chunk's binary32 values at a time in registers
     }
-    if (t < rest) {
-      const int64_t c = chunks * 8 + t;
-      emit1<In>(a, row, c, h1 * rstd * load_gamma1(a.gamma, a.gamma_bf16, c), tscale, amax);
-    }
+    if (t < rest) emit1<In>(a, out, chunks * 8 + t, h1 * rstd * g1, tscale, amax);
   }
   if (a.amax_out) {
-    __shared__ uint32_t ured[4];
-    block_max_to_global<256>(amax, a.amax_out, ured);
+    __shared__ uint32_t ured[16];
+    block_max_to_global<BLK>(amax, a.amax_out, ured);
   }
 }
 
@@ -318,14 +414,14 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
   const float tscale = a.quant == Q_TENSOR ? *a.scale : 1.0f;
   uint32_t amax = 0;
   int turn = 0;
-  const int64_t chunks = a.cols / 8, padded = (chunks + 255) / 256 * 256;
-  const int64_t c1 = chunks * 8 + threadIdx.x;  // this thread's element after the last whole chunk
+  const int chunks = (int)(a.cols / 8), padded = (chunks + 255) / 256 * 256;
+  const int c1 = chunks * 8 + threadIdx.x;  // this thread's element after the last whole chunk
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const In* x = reinterpret_cast<const In*>(a.x) + row * a.ldx;
     const In* r = reinterpret_cast<const In*>(a.r) + row * a.ldr;
     In* ho = reinterpret_cast<In*>(a.h) + row * a.ldh;
     float ss = 0.0f, h1 = 0.0f;
-    for (int64_t k = threadIdx.x; k < chunks; k += 256) {
+    for (int k = threadIdx.x; k < chunks; k += 256) {
       Chunk<In> h;
       h.load(x + k * 8, true);
       if (a.r) {
@@ -336,7 +432,7 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = h.at(i) + d.at(i);
         h.set(v);
       }
-      if (a.h) h.store(ho + k * 8);
+      if (a.h) h.template store<false>(ho + k * 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = fmaf(h.at(i), h.at(i), ss);
     }
@@ -351,9 +447,10 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (a.quant == Q_NONE && !a.y && !a.amax_out) continue;
     const In* hi = a.h ? ho : x;
+    const RowOut<In> out(a, row);
     // every lane takes part in the block maxima, so the count is padded; each
     // thread reads back the chunks that it wrote itself
-    for (int64_t k = threadIdx.x; k < padded; k += 256) {
+    for (int k = threadIdx.x; k < padded; k += 256) {
       const bool valid = k < chunks;
       Chunk<In> h;
       float g[8], y[8];
@@ -361,9 +458,9 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
       load_gamma(g, a.gamma, a.gamma_bf16, k * 8, valid);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = h.at(i) * rstd * g[i];
-      emit<In>(a, row, k * 8, valid, y, tscale, amax);
+      emit<In>(a, out, k * 8, valid, y, tscale, amax);
     }
-    if (c1 < a.cols) emit1<In>(a, row, c1, h1 * rstd * load_gamma1(a.gamma, a.gamma_bf16, c1), tscale, amax);
+    if (c1 < a.cols) emit1<In>(a, out, c1, h1 * rstd * load_gamma1(a.gamma, a.gamma_bf16, c1), tscale, amax);
   }
   if (a.amax_out) {
     __shared__ uint32_t ured[4];
@@ -374,30 +471,329 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
 template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
-  // one wave per row where it holds the row and there are rows enough to fill
-  // the card with waves, else a workgroup per row
-  const bool wave = chunks <= 64 || (chunks <= 64 * 16 && a.rows >= 1024 && sizeof(In) == 2);
+  const bool wave = chunks <= 128;                               // a row is a wave's
+  const bool wide = !wave && chunks > 256 && a.rows <= 512;      // few rows: a row's own latency is all
+  // An amax output ends in one atomic per workgroup on one address, which the
+  // memory side performs one at a time: a persistent grid of large workgroups.
+  const bool large = a.amax_out && !wide && chunks <= (sizeof(In) == 2 ? 1024 : 512);
   int64_t grid = wave ? (a.rows + 3) / 4 : a.rows;
-  // an amax output ends in one atomic per workgroup on one address, which the
-  // memory side performs one at a time: a persistent grid then
-  const int64_t cap = a.amax_out ? 1024 : 1 << 20;
+  if (large) grid = wave ? (a.rows + 15) / 16 : (a.rows + 3) / 4;
+  const int64_t cap = !a.amax_out ? 1 << 20 : large ? 256 : 1024;
   if (grid > cap) grid = cap;
-  const dim3 g((unsigned)grid), b(256);
-#define QSG_ROW(TPR, NCH) hipLaunchKernelGGL((norm_row_kernel<In, TPR, NCH>), g, b, 0, st, a)
-  if (wave) {
-    if (chunks <= 64) QSG_ROW(64, 1);
-    else if constexpr (sizeof(In) == 2) {
-      if (chunks <= 64 * 2) QSG_ROW(64, 2);
-      else if (chunks <= 64 * 4) QSG_ROW(64, 4);
-      else if (chunks <= 64 * 8) QSG_ROW(64, 8);
-      else QSG_ROW(64, 16);
-    }
-  } else if (chunks <= 256) QSG_ROW(256, 1);
-  else if (chunks <= 256 * 2) QSG_ROW(256, 2);
-  else if (chunks <= 256 * 4) QSG_ROW(256, 4);
-  else if (chunks <= 256 * 8) QSG_ROW(256, 8);
-  else hipLaunchKernelGGL(norm_long_kernel<In>, g, b, 0, st, a);
+  const dim3 g((unsigned)grid);
+#define QSG_ROW(TPR, NCH, BLK) hipLaunchKernelGGL((norm_row_kernel<In, TPR, NCH, BLK>), g, dim3(BLK), 0, st, a)
+#define QSG_ROWS(TPR, NCH)             \
+  do {                                 \
+    if (large) QSG_ROW(TPR, NCH, 1024); \
+    else QSG_ROW(TPR, NCH, 256);       \
+  } while (0)
+  if (chunks <= 64) QSG_ROWS(64, 1);
+  else if (chunks <= 128) QSG_ROWS(64, 2);
+  else if (chunks <= 256) QSG_ROWS(256, 1);
+  else if (wide && chunks <= 1024) QSG_ROW(1024, 1, 1024);
+  else if (wide && chunks <= 2048) QSG_ROW(1024, 2, 1024);
+  else if (chunks <= 512) QSG_ROWS(256, 2);
+  else if (chunks <= 1024) {
+    if constexpr (sizeof(In) == 2) QSG_ROWS(256, 4);
+    else QSG_ROW(256, 4, 256);
+  } else if (chunks <= 2048) QSG_ROW(256, 8, 256);
+  else hipLaunchKernelGGL(norm_long_kernel<In>, g, dim3(256), 0, st, a);
+#undef QSG_ROWS
 #undef QSG_ROW
+}
+
+// ---------------------------------------------------------------------------
+// second pass: column-wise copies
+// ---------------------------------------------------------------------------
+// 4 x 4 byte transpose: a..d are four rows of four bytes (byte k = column
+// k); o0..o3 are the four columns (byte k = row k).
+__device__ __forceinline__ void transpose4x4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
+  // v_perm_b32(hi, lo, sel): selector byte values 0-3 pick bytes of lo, 4-7 of hi
+  const uint32_t ab01 = __builtin_amdgcn_perm(b, a, 0x05010400u);  // a0 b0 a1 b1
+  const uint32_t ab23 = __builtin_amdgcn_perm(b, a, 0x07030602u);  // a2 b2 a3 b3
+  const uint32_t cd01 = __builtin_amdgcn_perm(d, c, 0x05010400u);
+  const uint32_t cd23 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(cd01, ab01, 0x05040100u);           // a0 b0 c0 d0
+  o[1] = __builtin_amdgcn_perm(cd01, ab01, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(cd23, ab23, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(cd23, ab23, 0x07060302u);
+}
+
+// Where tile k of `tile` rows (or columns) begins: the last tile of a matrix
+// that is no multiple of it begins earlier and does some of its neighbour's
+// work again, with the same result, so that no tile has an edge inside (the
+// only tile of a smaller matrix has).
+__device__ __forceinline__ int64_t tile_start(int64_t k, int64_t tile, int64_t n) {
+  const int64_t at = k * tile;
+  return at + tile > n && n > tile ? n - tile : at;
+}
+
+constexpr int CT_ROWS = 128;  // rows of a tile: a column's run in qt is 128 bytes, a cache line
+
+// LDS tile of codes: [column][row / 4], one word holds 4 rows; the stride of 33
+// words puts the 64 words that a wave writes at once on 64 banks.
+constexpr int CT_STRIDE = CT_ROWS / 4 + 1;
+
+// Codes of COLS columns from LDS to qt: 16 rows (16 bytes) a lane, 8 lanes a run.
+template <int COLS>
+__device__ __forceinline__ void store_columns(const uint32_t* codes, uint8_t* qt, int64_t rows, int64_t cols,
+                                              int64_t r0, int64_t c0) {
+#pragma unroll
+  for (int k = 0; k < COLS * 8 / 256; ++k) {
+    const int id = k * 256 + threadIdx.x, col = id >> 3, r = (id & 7) * 16;
+    const uint32_t* w = codes + col * CT_STRIDE + (r >> 2);
+    const u32x4 v = {w[0], w[1], w[2], w[3]};
+    uint8_t* p = qt + (c0 + col) * rows + r0 + r;
+    if (c0 + col < cols) {
+      if (r0 + r + 16 <= rows) {
+        put16<true>(p, v);
+      } else {
+        for (int b = 0; b < 16; ++b)
+          if (r0 + r + b < rows) p[b] = (uint8_t)(codes[col * CT_STRIDE + ((r + b) >> 2)] >> (8 * (b & 3)));
+      }
+    }
+  }
+}
+
+struct ColArgs {
+  const void* h;
+  int64_t rows, cols, ld;
+  const float* rstd;
+  const void* gamma;
+  bool gamma_bf16;
+  int quant, fmt, margin;
+  bool mx_ceil;
+  float* three;        // Q_TENSOR, current scaling: {amax, scale, scale_inv}, or null
+  const float* scale;  // Q_TENSOR otherwise
+  uint8_t* q;          // Q_TENSOR: rows x cols, or null
+  uint8_t* qt;         // cols x rows, or null (Q_TENSOR only)
+  void* st;
+  int64_t tiles_c, tiles;
+};
+
+constexpr int CT_COLS = 64;
+
+// A workgroup makes the column-wise copy of a 128 x 64 tile of y (and, with a
+// per-tensor scale, the row-wise one): thread t holds rows 4 (t / 8) .. + 3 of
+// chunk t % 8, so that a wave is 32 rows, the rows of an MXFP8 column block.
+//
+// A column's maximum: each lane's of its 4 rows go through LDS to the lane of
+// that column (64 columns, 64 lanes), which alone makes the scale; no barrier
+// where the block is the wave's.  Ordinary values skip what only the others
+// need (the wave decides): a row whose rstd is positive and finite has finite
+// h, so with finite weights y has no NaN; a block whose maximum is finite is
+// scaled to at most the format's maximum, up to a rounding that the encode
+// takes back, so nothing is clamped; and an MXFP8 scale (a power of two) is
+// put into the weight, which changes no bit of a code: with |gamma| <= 2^60
+// and a block maximum of 2^-50 at least, gamma 2^-e is neither too large nor
+// subnormal (|h rstd| <= sqrt(cols) <= 2^15), and an element of y that is
+// subnormal has the code of zero.
+template <typename In, int QUANT>
+__global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
+  __shared__ uint32_t codes[CT_COLS * CT_STRIDE];
+  __shared__ __attribute__((aligned(16))) uint32_t lane_max[4][8][CT_COLS];
+  __shared__ uint32_t part[4][CT_COLS];  // MXFP8: scale bytes [column][wave]; 1 x 128: maxima of the waves
+  __shared__ __attribute__((aligned(16))) float cscale[4][CT_COLS];
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  // last rows first: they are the ones that the first pass has left in the caches
+  const int64_t tile = a.tiles - 1 - blockIdx.x;
+  const int64_t r0 = tile_start(tile / a.tiles_c, CT_ROWS, a.rows), c0 = tile_start(tile % a.tiles_c, CT_COLS, a.cols);
+  const int64_t r = r0 + ty * 4, c = c0 + tx * 8;
+  const bool full = a.rows >= CT_ROWS && a.cols >= CT_COLS;
+  const In* h = reinterpret_cast<const In*>(a.h);
+  Chunk<In> v[4];
+  float rs[4], g[8];
+  if (full) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j].load(h + (r + j) * a.ld + c, true);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rs[j] = a.rstd[r + j];
+    load_gamma(g, a.gamma, a.gamma_bf16, c, true);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = r + j < a.rows && c + i < a.cols ? load1(h + (r + j) * a.ld + c + i) : 0.0f;
+      v[j].set(e);
+      rs[j] = r + j < a.rows ? a.rstd[r + j] : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = c + i < a.cols ? load_gamma1(a.gamma, a.gamma_bf16, c + i) : 0.0f;
+  }
+  float smallest = fminf(fminf(rs[0], rs[1]), fminf(rs[2], rs[3])), largest = fmaxf(fmaxf(rs[0], rs[1]), fmaxf(rs[2], rs[3]));
+  bool nan = __builtin_isnan(rs[0]) | __builtin_isnan(rs[1]) | __builtin_isnan(rs[2]) | __builtin_isnan(rs[3]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) nan |= !(fabsf(g[i]) <= 0x1p60f);
+  const bool plain = __all(!nan && smallest > 0.0f && largest <= FLT_MAX);  // no NaN anywhere in the wave's y
+  float y[4][8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[j][i] = v[j].at(i) * rs[j] * g[i];
+
+  uint32_t cq[8];  // column i: the codes of rows r .. r + 3
+  if constexpr (QUANT == Q_TENSOR) {
+    float s;
+    if (a.three) {
+      s = scale_from_amax(a.three[0], fp8_max(a.fmt), a.margin);
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.three[1] = s;
+        a.three[2] = __fdiv_rn(1.0f, s);
+      }
+    } else {
+      s = *a.scale;
+    }
+    u32x2 rq[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      rq[j] = a.fmt == kE4M3 ? enc8<kE4M3>(y[j], s) : enc8<kE5M2>(y[j], s);
+      if (a.q) {
+        uint8_t* p = a.q + (r + j) * a.cols + c;
+        if (full) {
+          put8<true>(p, rq[j]);
+        } else if (r + j < a.rows) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < a.cols) p[i] = (uint8_t)(rq[j][i >> 2] >> (8 * (i & 3)));
+        }
+      }
+    }
+    if (!a.qt) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t o[4];
+      transpose4x4(rq[0][k], rq[1][k], rq[2][k], rq[3][k], o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cq[k * 4 + i] = o[i];
+    }
+  } else {
+    uint32_t cm[8];
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        cm[i] = __float_as_uint(fmaxf(fmaxf(fabsf(y[0][i]), fabsf(y[1][i])), fmaxf(fabsf(y[2][i]), fabsf(y[3][i]))));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cm[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[i] = umax_u32(cm[i], abs_bits_canon(__float_as_uint(y[j][i])));
+      }
+    }
+    *reinterpret_cast<u32x4*>(&lane_max[wave][ty & 7][tx * 8]) = u32x4{cm[0], cm[1], cm[2], cm[3]};
+    *reinterpret_cast<u32x4*>(&lane_max[wave][ty & 7][tx * 8 + 4]) = u32x4{cm[4], cm[5], cm[6], cm[7]};
+    __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses are performed in their order
+    uint32_t m = lane_max[wave][0][lane];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) m = umax_u32(m, lane_max[wave][k][lane]);
+    // m: the maximum of column c0 + lane over the wave's rows
+    bool easy;
+    if constexpr (QUANT == Q_MX) {
+      const int e = mx_exponent(m, a.fmt == kE4M3 ? Fp8Traits<kE4M3>::kEmaxElem : Fp8Traits<kE5M2>::kEmaxElem,
+                                a.mx_ceil, a.margin);
+      reinterpret_cast<uint8_t*>(&part[0][0])[lane * 4 + wave] = (uint8_t)(e + 127);
+      cscale[wave][lane] = pow2_neg(e);
+      easy = plain && __all(m >= 0x26800000u && m < 0x7F800000u) && a.mx_ceil;  // 2^-50 <= m < inf
+    } else {
+      part[wave][lane] = m;
+      __syncthreads();
+      m = umax_u32(umax_u32(part[0][lane], part[1][lane]), umax_u32(part[2][lane], part[3][lane]));
+      const float s = scale_from_amax(__uint_as_float(m), fp8_max(a.fmt), a.margin);
+      cscale[wave][lane] = s;
+      if (wave == 0 && c0 + lane < a.cols)
+        reinterpret_cast<float*>(a.st)[(c0 + lane) * (a.rows / 128) + r0 / 128] = __fdiv_rn(1.0f, s);
+      easy = plain && __all(m < 0x7F800000u);
+    }
+    __builtin_amdgcn_wave_barrier();
+    float cs[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = cscale[wave][tx * 8 + i];
+    if (easy) {
+      if constexpr (QUANT == Q_MX) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] *= g[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = (QUANT == Q_MX ? v[j].at(i) * rs[j] : y[j][i]) * cs[i];
+        cq[i] = a.fmt == kE4M3 ? enc4_inrange<kE4M3>(z[0], z[1], z[2], z[3]) : enc4_inrange<kE5M2>(z[0], z[1], z[2], z[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        cq[i] = a.fmt == kE4M3 ? enc4<kE4M3>(y[0][i] * cs[i], y[1][i] * cs[i], y[2][i] * cs[i], y[3][i] * cs[i])
+                               : enc4<kE5M2>(y[0][i] * cs[i], y[1][i] * cs[i], y[2][i] * cs[i], y[3][i] * cs[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) codes[(tx * 8 + i) * CT_STRIDE + ty] = cq[i];
+  __syncthreads();
+  if constexpr (QUANT == Q_MX) {
+    if (threadIdx.x < CT_COLS && c0 + threadIdx.x < a.cols) {
+      const uint32_t w = part[threadIdx.x >> 6][threadIdx.x & 63];
+      uint8_t* p = reinterpret_cast<uint8_t*>(a.st) + (c0 + threadIdx.x) * (a.rows / 32) + r0 / 32;
+      if (full) {
+        *reinterpret_cast<u32_b*>(p) = w;
+      } else {
+        for (int k = 0; k < 4; ++k)
+          if (r0 + k * 32 < a.rows) p[k] = (uint8_t)(w >> (8 * k));
+      }
+    }
+  }
+  store_columns<CT_COLS>(codes, a.qt, a.rows, a.cols, r0, c0);
+}
+
+constexpr int TT_COLS = 128;
+
+// qt = q transposed (bytes), 128 x 128 tiles: with a per-tensor scale the
+// column-wise copy has the row-wise one's codes, and reading those back costs
+// half of reading h.  Thread t holds rows 4 (t / 8) .. + 3 of 16 columns.
+__global__ __launch_bounds__(256) void transpose_bytes_kernel(const uint8_t* q, uint8_t* qt, int64_t rows, int64_t cols,
+                                                              int64_t tiles_c, int64_t tiles) {
+  __shared__ uint32_t codes[TT_COLS * CT_STRIDE];
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int64_t tile = tiles - 1 - blockIdx.x;  // last rows first, as above
+  const int64_t r0 = tile_start(tile / tiles_c, CT_ROWS, rows), c0 = tile_start(tile % tiles_c, TT_COLS, cols);
+  const int64_t r = r0 + ty * 4, c = c0 + tx * 16;
+  u32x4 v[4];
+  if (rows >= CT_ROWS && cols >= TT_COLS) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_b*>(q + (r + j) * cols + c));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w = 0;
+        for (int b = 0; b < 4; ++b)
+          if (r + j < rows && c + k * 4 + b < cols) w |= (uint32_t)q[(r + j) * cols + c + k * 4 + b] << (8 * b);
+        v[j][k] = w;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t o[4];
+    transpose4x4(v[0][k], v[1][k], v[2][k], v[3][k], o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) codes[(tx * 16 + k * 4 + i) * CT_STRIDE + ty] = o[i];
+  }
+  __syncthreads();
+  store_columns<TT_COLS>(codes, qt, rows, cols, r0, c0);
+}
+
+template <typename In>
+void launch_col(ColArgs a, hipStream_t st) {
+  a.tiles_c = (a.cols + CT_COLS - 1) / CT_COLS;
+  a.tiles = (a.rows + CT_ROWS - 1) / CT_ROWS * a.tiles_c;
+  const dim3 g((unsigned)a.tiles);
+  if (a.quant == Q_TENSOR) hipLaunchKernelGGL((norm_col_kernel<In, Q_TENSOR>), g, dim3(256), 0, st, a);
+  else if (a.quant == Q_MX) hipLaunchKernelGGL((norm_col_kernel<In, Q_MX>), g, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((norm_col_kernel<In, Q_BLOCK>), g, dim3(256), 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -482,6 +878,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
     for (int j = 0; j < NCH; ++j) {
       const uint32_t k = j * TPR + t;
       float v[8];
+      dy[j].forget_wide();
+      h[j].forget_wide();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = h[j].at(i) * rstd;
@@ -492,7 +890,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
       if (k < (uint32_t)chunks) {
         Chunk<In> o;
         o.set(v);
-        o.store(pdx + k * 8);
+        o.template store<true>(pdx + k * 8);
       }
     }
     if (t < rest) {
@@ -509,7 +907,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
       if (k < (uint32_t)chunks) {
         Chunk<float> o;
         o.set(acc[j]);
-        o.store(p + k * 8);
+        o.template store<false>(p + k * 8);
       }
     }
     if (t < rest) p[chunks * 8 + t] = acc1;
@@ -543,28 +941,41 @@ __global__ __launch_bounds__(256) void norm_bwd_dot_kernel(NormBwdArgs a) {
 }
 
 // dgamma[c] (+)= sum over groups of partial[group][c], in a fixed order: a
-// workgroup takes 32 columns, 8 lanes of 4 columns by 32 rows of groups.
+// workgroup takes 16 columns, 4 lanes of 4 columns by 64 parts of the groups.
 __global__ __launch_bounds__(256) void norm_dgamma_kernel(const float* partial, int64_t groups, int64_t cols,
                                                           float* dgamma, bool accumulate) {
-  __shared__ float sum[32][33];
-  const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane * 4;
+  __shared__ float sum[64][17];
+  const int lane = threadIdx.x & 3, part = threadIdx.x >> 2;
+  const int64_t c = (int64_t)blockIdx.x * 16 + lane * 4;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t k = part; k < groups; k += 32) {
-    const float* p = partial + k * cols + c;
+  if (c + 4 <= cols) {
+#pragma unroll 8
+    for (int64_t k = part; k < groups; k += 64) {
+      const u32x4 u = *reinterpret_cast<const u32x4_e*>(partial + k * cols + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < cols) v[i] += p[i];
+      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(u[i]);
+    }
+  } else {
+    for (int64_t k = part; k < groups; k += 64)
+      for (int i = 0; i < 4; ++i)
+        if (c + i < cols) v[i] += partial[k * cols + c + i];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[part][lane * 4 + i] = v[i];
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    if (col < cols) {
-      float s = sum[0][threadIdx.x];
-      for (int k = 1; k < 32; ++k) s += sum[k][threadIdx.x];
-      dgamma[col] = accumulate ? dgamma[col] + s : s;
+  // 16 threads a column, 4 parts each, then 16 partial sums
+  const int col = threadIdx.x & 15, p = threadIdx.x >> 4;
+  float s = ((sum[p][col] + sum[p + 16][col]) + sum[p + 32][col]) + sum[p + 48][col];
+  __syncthreads();
+  sum[p][col] = s;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    if (at < cols) {
+      s = sum[0][threadIdx.x];
+#pragma unroll
+      for (int k = 1; k < 16; ++k) s += sum[k][threadIdx.x];
+      dgamma[at] = accumulate ? dgamma[at] + s : s;
     }
   }
 }
@@ -607,7 +1018,7 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
                              int64_t ldr, const void* gamma, int gamma_dtype, float eps, int scaling, int fmt,
                              int margin, bool mx_ceil, const float* scale, void* h, int64_t ldh, float* rstd, void* y,
                              uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out, hipStream_t st) {
-  const bool tensorwise = scaling == 0, quantized = q || qt;
+  const bool tensorwise = scaling == 0;
   float* three = reinterpret_cast<float*>(s);
   float* amax = tensorwise ? three : amax_out;
   if (amax) launch_fill_u32(reinterpret_cast<uint32_t*>(amax), 0u, 1, st);
@@ -615,10 +1026,11 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
     if (tensorwise) launch_compute_scale(three, fmt, margin, three + 1, three + 2, st);
     return;
   }
-  // The transposed copy takes tiles of 128 rows, and the current scaling the
-  // whole tensor's amax, before the first code can be written: a second
-  // kernel reads h (or x) back then.
-  const bool two = quantized && (tensorwise || qt);
+  // The first pass has whole rows: h, rstd, y, and the row-wise copy except
+  // under the current scaling, whose scale needs the whole tensor's amax.  The
+  // second has tiles: the column-wise copy from h, or from q where both copies
+  // share one given scale.
+  const int quant = scaling < 0 ? Q_NONE : scaling < 2 ? Q_TENSOR : scaling == 2 ? Q_MX : Q_BLOCK;
   NormArgs a{};
   a.x = x; a.r = r;
   a.rows = rows; a.cols = cols; a.ldx = ldx; a.ldr = ldr; a.ldh = ldh;
@@ -626,20 +1038,36 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
   a.eps = eps;
   a.h = h; a.rstd = rstd; a.y = y;
   a.fmt = fmt; a.margin = margin; a.mx_ceil = mx_ceil;
-  if (!two && q) {
-    a.quant = scaling == 1 ? Q_TENSOR : scaling == 2 ? Q_MX : Q_BLOCK;
-    a.scale = scale;
-    a.q = q; a.s = s;
+  a.scale = scale; a.s = s;
+  if (q && !tensorwise) {
+    a.quant = quant;
+    a.q = q;
   }
-  if (tensorwise || !two) a.amax_out = reinterpret_cast<uint32_t*>(amax);
+  a.amax_out = reinterpret_cast<uint32_t*>(amax);
+  a.again = scaling == 1 && q && qt;
+  a.second = (qt || tensorwise) && !a.again;
   if (dtype == 1)
     launch_row<uint16_t>(a, st);
   else
     launch_row<float>(a, st);
-  if (!two) return;
-  if (tensorwise) launch_compute_scale(three, fmt, margin, three + 1, three + 2, st);
-  launch_quantize_normed(h ? h : x, dtype, rows, cols, h ? ldh : ldx, rstd, gamma, gamma_dtype, scaling, fmt, margin,
-                         mx_ceil, tensorwise ? three + 1 : scale, q, s, qt, st_, tensorwise ? nullptr : amax_out, st);
+  if (!qt && !tensorwise) return;
+  if (a.again) {
+    const int64_t tc = (cols + TT_COLS - 1) / TT_COLS, tiles = (rows + CT_ROWS - 1) / CT_ROWS * tc;
+    hipLaunchKernelGGL(transpose_bytes_kernel, dim3((unsigned)tiles), dim3(256), 0, st, q, qt, rows, cols, tc, tiles);
+    return;
+  }
+  ColArgs k{};
+  k.h = h ? h : x; k.ld = h ? ldh : ldx;
+  k.rows = rows; k.cols = cols;
+  k.rstd = rstd; k.gamma = gamma; k.gamma_bf16 = a.gamma_bf16;
+  k.quant = quant; k.fmt = fmt; k.margin = margin; k.mx_ceil = mx_ceil;
+  k.three = tensorwise ? three : nullptr; k.scale = scale;
+  k.q = tensorwise ? q : nullptr;
+  k.qt = qt; k.st = st_;
+  if (dtype == 1)
+    launch_col<uint16_t>(k, st);
+  else
+    launch_col<float>(k, st);
 }
 
 int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
@@ -672,7 +1100,7 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
   else
     launch_bwd<float>(a, groups, st);
   if (dgamma)
-    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, st, ws, groups, cols,
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, st, ws, groups, cols,
                        dgamma, accumulate);
 }
 

@@ -88,10 +88,6 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
                              int64_t ldr, const void* gamma, int gamma_dtype, float eps, int scaling, int fmt,
                              int margin, bool mx_ceil, const float* scale, void* h, int64_t ldh, float* rstd, void* y,
                              uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out, hipStream_t st);
-void launch_quantize_normed(const void* h, int dtype, int64_t rows, int64_t cols, int64_t ld, const float* rstd,
-                            const void* gamma, int gamma_dtype, int scaling, int fmt, int margin, bool mx_ceil,
-                            const float* scale, uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out,
-                            hipStream_t st);
 // Backward of the norm; workspace of rmsnorm_bwd_workspace(rows, cols) bytes.
 int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
 void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,

@@ -190,10 +190,6 @@ struct TileArgs {
   // per column (st) when those runs are 4-byte aligned
   bool s_vec, st_vec;
   int64_t tiles_c, ntiles;
-  // normalised input only (Normed below): 1 / rms of each row, the weight
-  const float* rstd;
-  const void* gamma;
-  bool gamma_bf16;
 };
 
 // Thread-private 8x8 sub-block in its input type.
@@ -259,33 +255,6 @@ struct Block8<float> {
         for (int i = 0; i < 8; ++i)
           v[j][i] = (r + j < a.rows && c + i < a.cols) ? x[(r + j) * a.ld + c + i] : 0.0f;
       }
-    }
-  }
-};
-
-// Sub-block of y = fp32(fp32(h rstd) gamma), computed from h (type In) where
-// it is used: the tile kernel then quantizes the RMS norm's output without a
-// copy of it in memory.
-template <typename In>
-struct Normed {};
-
-template <typename In>
-struct Block8<Normed<In>> {
-  Block8<In> h;
-  float rstd[8], gamma[8];
-  __device__ __forceinline__ float at(int j, int i) const { return h.at(j, i) * rstd[j] * gamma[i]; }
-  __device__ __forceinline__ uint32_t absbits(int j, int i) const { return __float_as_uint(at(j, i)) & 0x7FFFFFFFu; }
-  template <bool FULL>
-  __device__ __forceinline__ void load(const TileArgs& a, int64_t r, int64_t c) {
-    h.template load<FULL>(a, r, c);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) rstd[j] = (FULL || r + j < a.rows) ? a.rstd[r + j] : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gamma[i] = 0.0f;
-      if (FULL || c + i < a.cols)
-        gamma[i] = a.gamma_bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.gamma)[c + i] << 16)
-                                : reinterpret_cast<const float*>(a.gamma)[c + i];
     }
   }
 };
@@ -806,37 +775,6 @@ void launch_quantize_blocked(const void* x, int dtype, int64_t rows, int64_t col
     launch_tile_dtype<MODE_B1X128>(a, dtype, fmt, st);
   else
     launch_tile_dtype<MODE_B128X128>(a, dtype, fmt, st);
-}
-
-// Second pass of qsg_rmsnorm_quantize: the copies of y = h rstd gamma under a
-// recipe (scaling 0 and 1: with *scale).
-void launch_quantize_normed(const void* h, int dtype, int64_t rows, int64_t cols, int64_t ld, const float* rstd,
-                            const void* gamma, int gamma_dtype, int scaling, int fmt, int margin, bool mx_ceil,
-                            const float* scale, uint8_t* q, void* s, uint8_t* qt, void* st_, float* amax_out,
-                            hipStream_t st) {
-  TileArgs a{};
-  a.x = h; a.rows = rows; a.cols = cols; a.ld = ld;
-  a.vec_ok = tile_vec_ok(h, dtype == 1 ? 2 : 4, rows, cols, ld, q, qt);
-  a.q = q; a.qt = qt;
-  a.margin = margin; a.mx_ceil = mx_ceil;
-  a.rstd = rstd; a.gamma = gamma; a.gamma_bf16 = gamma_dtype == 1;
-  a.tiles_c = (cols + TILE - 1) / TILE;
-  a.ntiles = ((rows + TILE - 1) / TILE) * a.tiles_c;
-  const bool bf16 = dtype == 1;
-  if (scaling == 0 || scaling == 1) {
-    a.scale = scale;
-    a.amax_out = reinterpret_cast<uint32_t*>(amax_out);
-    bf16 ? launch_tile<Normed<uint16_t>, MODE_TENSOR>(a, fmt, st) : launch_tile<Normed<float>, MODE_TENSOR>(a, fmt, st);
-    return;
-  }
-  a.s = q ? s : nullptr;
-  a.st = qt ? st_ : nullptr;
-  a.s_vec = a.s && ((uintptr_t)a.s % 4 == 0) && (cols % 128 == 0);
-  a.st_vec = a.st && ((uintptr_t)a.st % 4 == 0) && (rows % 128 == 0);
-  if (scaling == 2)
-    bf16 ? launch_tile<Normed<uint16_t>, MODE_MX>(a, fmt, st) : launch_tile<Normed<float>, MODE_MX>(a, fmt, st);
-  else
-    bf16 ? launch_tile<Normed<uint16_t>, MODE_B1X128>(a, fmt, st) : launch_tile<Normed<float>, MODE_B1X128>(a, fmt, st);
 }
 
 }  // namespace qsg

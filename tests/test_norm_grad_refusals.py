@@ -53,6 +53,7 @@ TW, DL, B1 = (q.TENSORWISE, q.E4M3, 0, 0), (q.DELAYED, q.E4M3, 0, 0), (q.BLOCK_1
     (dict(recipe=B1, cols=192), -2), (dict(recipe=B1, s=66), -3),
     (dict(recipe=TW, s=None), -1), (dict(recipe=TW, s=66), -3), (dict(recipe=TW, qt=None, rstd=None), -1),
     (dict(recipe=TW, amax=64), -1), (dict(amax=64), -1), (dict(recipe=DL), -1), (dict(recipe=DL, scale=66), -3),
+    (dict(cols=(1 << 30) + 32, ldx=1 << 31, ldr=1 << 31, ldh=1 << 31), -4),
     (dict(recipe=DL, scale=64, amax=66), -3), (dict(y=33, recipe=DL, scale=64), -3),
 ])
 def test_forward_refuses(lib, kw, status):
