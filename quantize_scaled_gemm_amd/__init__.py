@@ -203,7 +203,8 @@ def _stream(stream):
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
 
-    return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle without the Stream object around it, which costs more than a launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(rc):
@@ -453,38 +454,61 @@ def qsg_gemm_nvfp4(a, sa, ts_a, b, sb, ts_b, c, stream=None):
                                          _ptr(c), _dtype_code(c), ldc, _stream(stream)))
 
 
+# The calls below take many tensors and are made for single tokens too, so
+# their checks ask each tensor for as little as they can and leave the wording
+# of a refusal to the checks above.
+_DTYPES = {}  # torch dtype -> (code, name); filled on first use
+
+
+def _dtype_entry(dtype):
+    if not _DTYPES:
+        import torch
+
+        _DTYPES.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32"), torch.uint8: (None, "u8"),
+                        torch.float64: (None, "f64")})
+    return _DTYPES.get(dtype, (None, None))
+
+
 def _rows(t, name):
-    """_matrix of a view whose rows do not overlap."""
+    """(pointer, rows, cols, ld) of a view whose rows do not overlap."""
+    if not t.is_cuda:
+        raise QsgError(f"{name} must live on the GPU")
+    if t.dim() == 2 and t.is_contiguous():
+        rows, cols = t.shape
+        return t.data_ptr(), rows, cols, cols or 1
     rows, cols, ld = _matrix(t)
     if rows > 1 and cols > 0 and t.stride(0) < cols:
         raise QsgError(f"{name}: the rows overlap (stride {t.stride(0)} for {cols} columns)")
-    return rows, cols, ld
+    return t.data_ptr(), rows, cols, ld
 
 
 def _same_matrix(t, name, like):
-    """(pointer, ld) of a matrix of the shape and type of ``like``."""
+    """(pointer, ld) of a matrix of the shape and type of ``like``, or of none."""
     if t is None:
         return None, 0
-    rows, cols, ld = _rows(t, name)
+    p, rows, cols, ld = _rows(t, name)
     if t.shape != like.shape:
         raise QsgError(f"{name} is {rows}x{cols}, expected {like.shape[0]}x{like.shape[1]}")
-    if t.dtype != like.dtype:
+    if t.dtype is not like.dtype:
         raise QsgError(f"{name} must be {like.dtype} (got {t.dtype})")
-    return _ptr(t), ld
+    return p, ld
 
 
-def _dense(t, name, numel, dtype):
-    """Pointer of an optional buffer that _buffer accepts."""
-    if t is None or isinstance(t, int):
+def _dense(t, name, numel, dtype, required=False):
+    """Pointer of a buffer that _buffer accepts."""
+    if t is None and not required or isinstance(t, int):
         return t
-    _buffer(t, name, numel, dtype)
+    if t is None or _dtype_entry(t.dtype)[1] != dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+        _buffer(t, name, numel, dtype)
     return t.data_ptr()
 
 
 def _weight(gamma, cols):
     """(pointer, type) of a norm's weight."""
-    dt = _dtype_code(gamma)
-    return _dense(gamma, "gamma", cols, "bf16" if dt == BF16 else "f32"), dt
+    code, name = _dtype_entry(gamma.dtype)
+    if code is None:
+        raise QsgError(f"unsupported input dtype {gamma.dtype}")
+    return _dense(gamma, "gamma", cols, name), code
 
 
 def _workspace(t, nbytes):
@@ -505,37 +529,34 @@ def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h
     recipe (scaling None: y only).  x, residual and h are 2-D with a unit
     column stride; h may be x or residual itself.  gamma (cols) is fp32 or
     bf16, rstd (rows) fp32; DELAYED takes its scale and returns amax_out."""
-    rows, cols, ld = _rows(x, "x")
-    dt = _dtype_code(x)
+    px, rows, cols, ld = _rows(x, "x")
+    dt, dname = _dtype_entry(x.dtype)
+    if dt is None:
+        raise QsgError(f"unsupported input dtype {x.dtype}")
     numel = rows * cols
     pr, ldr = _same_matrix(residual, "residual", x)
     ph, ldh = _same_matrix(h, "h", x)
     pg, gt = _weight(gamma, cols)
     prstd = _dense(rstd, "rstd", rows, "f32")
-    py = _dense(y, "y", numel, "bf16" if dt == BF16 else "f32")
+    py = _dense(y, "y", numel, dname)
     pq, pqt = _dense(q, "q", numel, "u8"), _dense(qt, "qt", numel, "u8")
     pa = _dense(amax_out, "amax_out", 1, "f32")
     psc = ps = pst = None
     if scaling == DELAYED:
-        _buffer(scale, "scale", 1, "f32")
-        psc = _ptr(scale)
+        psc = _dense(scale, "scale", 1, "f32", True)
     elif scaling == TENSORWISE:
-        _buffer(s, "s", 3, "f32")
-        ps = _ptr(s)
+        ps = _dense(s, "s", 3, "f32", True)
     elif scaling in (MXFP8, BLOCK_1X128):
-        # a shape that breaks the block rule is the library's to refuse
-        row, col = _scale_layout(scaling, rows, cols), _scale_layout(scaling, cols, rows)
+        # a shape that breaks the block rule has no layout, and the library refuses it
         if q is not None:
-            if row is not None:
-                _buffer(s, "s", row[0], row[1])
-            ps = _ptr(s)
+            row = _scale_layout(scaling, rows, cols)
+            ps = _dense(s, "s", row[0], row[1], True) if row else _ptr(s)
         if qt is not None:
-            if col is not None:
-                _buffer(st, "st", col[0], col[1])
-            pst = _ptr(st)
-    rec = None if scaling is None else ctypes.byref(Recipe(scaling, fmt, margin, mx_rule))
-    _check(load_library().qsg_rmsnorm_quantize(_ptr(x), pr, dt, rows, cols, ld, ldr, pg, gt, eps, rec, psc, ph, ldh,
-                                               prstd, py, pq, ps, pqt, pst, pa, _stream(stream)))
+            col = _scale_layout(scaling, cols, rows)
+            pst = _dense(st, "st", col[0], col[1], True) if col else _ptr(st)
+    rec = None if scaling is None else Recipe(scaling, fmt, margin, mx_rule)
+    _check(load_library().qsg_rmsnorm_quantize(px, pr, dt, rows, cols, ld, ldr, pg, gt, eps, rec, psc, ph, ldh, prstd,
+                                               py, pq, ps, pqt, pst, pa, _stream(stream)))
 
 
 def qsg_rmsnorm_bwd_workspace(rows, cols):
@@ -550,17 +571,19 @@ def qsg_rmsnorm_bwd(dy, h, gamma, rstd, dx, dres=None, dgamma=None, accumulate=F
     """dx = gradient of x (and of the residual) from dy, the gradient of y, plus
     dres, the gradient that reaches h directly; dgamma (cols fp32) written or
     accumulated.  workspace: qsg_rmsnorm_bwd_workspace(rows, cols) bytes."""
-    rows, cols, lddy = _rows(dy, "dy")
-    dt = _dtype_code(dy)
+    pdy, rows, cols, lddy = _rows(dy, "dy")
+    dt = _dtype_entry(dy.dtype)[0]
+    if dt is None:
+        raise QsgError(f"unsupported input dtype {dy.dtype}")
     ph, ldh = _same_matrix(h, "h", dy)
     pdx, lddx = _same_matrix(dx, "dx", dy)
     pdr, lddres = _same_matrix(dres, "dres", dy)
     pg, gt = _weight(gamma, cols)
-    prstd = _dense(rstd, "rstd", rows, "f32")
+    prstd = _dense(rstd, "rstd", rows, "f32", True)
     pdg = _dense(dgamma, "dgamma", cols, "f32")
     pw = _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))
-    _check(load_library().qsg_rmsnorm_bwd(_ptr(dy), ph, pdr, dt, rows, cols, lddy, ldh, lddres, pg, gt, prstd, pdx,
-                                          lddx, pdg, 1 if accumulate else 0, pw, _stream(stream)))
+    _check(load_library().qsg_rmsnorm_bwd(pdy, ph, pdr, dt, rows, cols, lddy, ldh, lddres, pg, gt, prstd, pdx, lddx,
+                                          pdg, 1 if accumulate else 0, pw, _stream(stream)))
 
 
 GRAD_WORKSPACE_BYTES = 8192  # QSG_GRAD_WORKSPACE_BYTES of include/qsg.h
@@ -610,15 +633,12 @@ def qsg_grad_plan(grads, outs=None):
 def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
     """sumsq (1 fp64 on the GPU) = sum of the squares of the plan's gradients.
     workspace: GRAD_WORKSPACE_BYTES bytes on the GPU."""
-    _buffer(sumsq, "sumsq", 1, "f64")
-    ws = _workspace(workspace, GRAD_WORKSPACE_BYTES)
-    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), ws, _stream(stream)))
+    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64", True),
+                                         _workspace(workspace, GRAD_WORKSPACE_BYTES), _stream(stream)))
 
 
 def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
     """The plan's outputs = gradients * min(1, max_norm / (norm + 1e-6)) with
     norm = sqrt(sumsq), written to norm_out (1 fp32) if given."""
-    _buffer(sumsq, "sumsq", 1, "f64")
-    _buffer(norm_out, "norm_out", 1, "f32", required=False)
-    _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _ptr(sumsq), max_norm, _ptr(norm_out),
-                                        _stream(stream)))
+    _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64", True),
+                                        max_norm, _dense(norm_out, "norm_out", 1, "f32"), _stream(stream)))

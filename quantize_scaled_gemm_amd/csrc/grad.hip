@@ -35,23 +35,60 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red) {
   return ((red[0] + red[1]) + red[2]) + red[3];
 }
 
-__device__ __forceinline__ void add_squares_bf16(double& s, u32x4 u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const double lo = bf16lo(w[k]), hi = bf16hi(w[k]);
-    s = fma(lo, lo, s);
-    s = fma(hi, hi, s);
+// 16 bytes of a tensor: 8 bf16 or 4 fp32 values
+template <typename T>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ float at(u32x4 u, int i) { return (i & 1) ? bf16hi(u[i >> 1]) : bf16lo(u[i >> 1]); }
+  static __device__ __forceinline__ u32x4 scaled(u32x4 u, float k) {
+    return u32x4{pack_bf16x2(bf16lo(u.x) * k, bf16hi(u.x) * k), pack_bf16x2(bf16lo(u.y) * k, bf16hi(u.y) * k),
+                 pack_bf16x2(bf16lo(u.z) * k, bf16hi(u.z) * k), pack_bf16x2(bf16lo(u.w) * k, bf16hi(u.w) * k)};
   }
-}
+  static __device__ __forceinline__ float one(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+  static __device__ __forceinline__ uint16_t rounded(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ float at(u32x4 u, int i) { return __uint_as_float(u[i]); }
+  static __device__ __forceinline__ u32x4 scaled(u32x4 u, float k) {
+    return u32x4{__float_as_uint(__uint_as_float(u.x) * k), __float_as_uint(__uint_as_float(u.y) * k),
+                 __float_as_uint(__uint_as_float(u.z) * k), __float_as_uint(__uint_as_float(u.w) * k)};
+  }
+  static __device__ __forceinline__ float one(float v) { return v; }
+  static __device__ __forceinline__ float rounded(float v) { return v; }
+};
 
-__device__ __forceinline__ void add_squares_f32(double& s, u32x4 u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+constexpr int kFlight = 8;  // 16-byte loads of a thread in flight
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T* g, int n) {
+  typedef Vec<T> V;
+  double s = 0.0;
+  const int whole = n / V::N;  // 16-byte pieces
+  for (int i0 = threadIdx.x; i0 < whole; i0 += 256 * kFlight) {
+    u32x4 u[kFlight];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const double v = __uint_as_float(w[k]);
+    for (int k = 0; k < kFlight; ++k) {
+      u[k] = u32x4{0, 0, 0, 0};
+      if (i0 + k * 256 < whole)
+        u[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + (i0 + k * 256) * V::N));
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) {
+        const double v = V::at(u[k], i);
+        s = fma(v, v, s);
+      }
+  }
+  for (int i = whole * V::N + threadIdx.x; i < n; i += 256) {
+    const double v = V::one(g[i]);
     s = fma(v, v, s);
   }
+  return s;
 }
 
 __global__ __launch_bounds__(256) void grad_sumsq_kernel(const qsg_grad* table, int64_t n, double* partial) {
@@ -59,25 +96,8 @@ __global__ __launch_bounds__(256) void grad_sumsq_kernel(const qsg_grad* table, 
   double s = 0.0;
   for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
     const qsg_grad t = table[k];
-    if (t.dtype == QSG_BF16) {
-      const uint16_t* g = reinterpret_cast<const uint16_t*>(t.g);
-      const int whole = (int)(t.n / 8) * 8;
-      for (int i = threadIdx.x * 8; i < whole; i += 256 * 8)
-        add_squares_bf16(s, __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + i)));
-      for (int i = whole + threadIdx.x; i < (int)t.n; i += 256) {
-        const double v = __uint_as_float((uint32_t)g[i] << 16);
-        s = fma(v, v, s);
-      }
-    } else {
-      const float* g = reinterpret_cast<const float*>(t.g);
-      const int whole = (int)(t.n / 4) * 4;
-      for (int i = threadIdx.x * 4; i < whole; i += 256 * 4)
-        add_squares_f32(s, __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + i)));
-      for (int i = whole + threadIdx.x; i < (int)t.n; i += 256) {
-        const double v = g[i];
-        s = fma(v, v, s);
-      }
-    }
+    s += t.dtype == QSG_BF16 ? chunk_squares(reinterpret_cast<const uint16_t*>(t.g), (int)t.n)
+                             : chunk_squares(reinterpret_cast<const float*>(t.g), (int)t.n);
   }
   s = block_sum_f64(s, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
@@ -91,6 +111,24 @@ __global__ __launch_bounds__(256) void grad_sum_kernel(const double* partial, in
   if (threadIdx.x == 0) *sumsq = s;
 }
 
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* g, T* o, int n, float c) {
+  typedef Vec<T> V;
+  const int whole = n / V::N;
+  for (int i0 = threadIdx.x; i0 < whole; i0 += 256 * kFlight) {
+    u32x4 u[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (i0 + k * 256 < whole)
+        u[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + (i0 + k * 256) * V::N));
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (i0 + k * 256 < whole)
+        __builtin_nontemporal_store(V::scaled(u[k], c), reinterpret_cast<u32x4_e*>(o + (i0 + k * 256) * V::N));
+  }
+  for (int i = whole * V::N + threadIdx.x; i < n; i += 256) o[i] = V::rounded(V::one(g[i]) * c);
+}
+
 __global__ __launch_bounds__(256) void grad_clip_kernel(const qsg_grad* table, int64_t n, const double* sumsq,
                                                         float max_norm, float* norm_out) {
   const float norm = (float)sqrt(*sumsq);
@@ -98,32 +136,12 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(const qsg_grad* table, i
   if (k > 1.0f) k = 1.0f;  // a NaN stays
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = norm;
   for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
-    const qsg_grad t = table[c];
+    const qsg_grad t = table[n - 1 - c];
     if (k == 1.0f && t.out == t.g) continue;  // every product is the value itself
-    if (t.dtype == QSG_BF16) {
-      const uint16_t* g = reinterpret_cast<const uint16_t*>(t.g);
-      uint16_t* o = reinterpret_cast<uint16_t*>(t.out);
-      const int whole = (int)(t.n / 8) * 8;
-      for (int i = threadIdx.x * 8; i < whole; i += 256 * 8) {
-        const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + i));
-        const u32x4 v = {pack_bf16x2(bf16lo(u.x) * k, bf16hi(u.x) * k), pack_bf16x2(bf16lo(u.y) * k, bf16hi(u.y) * k),
-                         pack_bf16x2(bf16lo(u.z) * k, bf16hi(u.z) * k), pack_bf16x2(bf16lo(u.w) * k, bf16hi(u.w) * k)};
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e*>(o + i));
-      }
-      for (int i = whole + threadIdx.x; i < (int)t.n; i += 256)
-        o[i] = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)g[i] << 16) * k, 0.0f);
-    } else {
-      const float* g = reinterpret_cast<const float*>(t.g);
-      float* o = reinterpret_cast<float*>(t.out);
-      const int whole = (int)(t.n / 4) * 4;
-      for (int i = threadIdx.x * 4; i < whole; i += 256 * 4) {
-        const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(g + i));
-        const u32x4 v = {__float_as_uint(__uint_as_float(u.x) * k), __float_as_uint(__uint_as_float(u.y) * k),
-                         __float_as_uint(__uint_as_float(u.z) * k), __float_as_uint(__uint_as_float(u.w) * k)};
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e*>(o + i));
-      }
-      for (int i = whole + threadIdx.x; i < (int)t.n; i += 256) o[i] = g[i] * k;
-    }
+    if (t.dtype == QSG_BF16)
+      chunk_scale(reinterpret_cast<const uint16_t*>(t.g), reinterpret_cast<uint16_t*>(t.out), (int)t.n, k);
+    else
+      chunk_scale(reinterpret_cast<const float*>(t.g), reinterpret_cast<float*>(t.out), (int)t.n, k);
   }
 }
 

@@ -941,48 +941,59 @@ __global__ __launch_bounds__(256) void norm_bwd_dot_kernel(NormBwdArgs a) {
 }
 
 // dgamma[c] (+)= sum over groups of partial[group][c], in a fixed order: a
-// workgroup takes 16 columns, 4 lanes of 4 columns by 64 parts of the groups.
-__global__ __launch_bounds__(256) void norm_dgamma_kernel(const float* partial, int64_t groups, int64_t cols,
+// workgroup takes 32 columns, 8 lanes of 4 columns by 128 parts of the groups.
+__global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* partial, int64_t groups, int64_t cols,
                                                           float* dgamma, bool accumulate) {
-  __shared__ float sum[64][17];
-  const int lane = threadIdx.x & 3, part = threadIdx.x >> 2;
-  const int64_t c = (int64_t)blockIdx.x * 16 + lane * 4;
+  constexpr int PARTS = 128;
+  __shared__ float sum[PARTS][33];
+  const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane * 4;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c + 4 <= cols) {
 #pragma unroll 8
-    for (int64_t k = part; k < groups; k += 64) {
+    for (int64_t k = part; k < groups; k += PARTS) {
       const u32x4 u = *reinterpret_cast<const u32x4_e*>(partial + k * cols + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(u[i]);
     }
   } else {
-    for (int64_t k = part; k < groups; k += 64)
+    for (int64_t k = part; k < groups; k += PARTS)
       for (int i = 0; i < 4; ++i)
         if (c + i < cols) v[i] += partial[k * cols + c + i];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[part][lane * 4 + i] = v[i];
   __syncthreads();
-  // 16 threads a column, 4 parts each, then 16 partial sums
-  const int col = threadIdx.x & 15, p = threadIdx.x >> 4;
-  float s = ((sum[p][col] + sum[p + 16][col]) + sum[p + 32][col]) + sum[p + 48][col];
+  const int col = threadIdx.x & 31, p = threadIdx.x >> 5;
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s += sum[p + k * (PARTS / 4)][col];
   __syncthreads();
   sum[p][col] = s;
   __syncthreads();
-  if (threadIdx.x < 16) {
-    const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x;
+  if (threadIdx.x < 32) {
+    const int64_t at = (int64_t)blockIdx.x * 32 + threadIdx.x;
     if (at < cols) {
       s = sum[0][threadIdx.x];
 #pragma unroll
-      for (int k = 1; k < 16; ++k) s += sum[k][threadIdx.x];
+      for (int k = 1; k < PARTS / 4; ++k) s += sum[k][threadIdx.x];
       dgamma[at] = accumulate ? dgamma[at] + s : s;
     }
   }
 }
 
-constexpr int64_t kBwdGroups = 1024;     // groups that share the rows of a backward pass, at most
-constexpr int64_t kBwdMostCols = 16391; // of a row held in registers: 2048 chunks and 7 elements
+constexpr int64_t kBwdMostCols = 16391;  // of a row held in registers: 2048 chunks and 7 elements
 constexpr int64_t kBwdPiece = 2048;      // columns of a workgroup beyond that
+
+// Groups that share the rows: about what the card holds at once, since each
+// leaves a partial dgamma (4 bytes a column, written and read again).
+int64_t bwd_groups(int64_t rows, int64_t cols) {
+  const int64_t chunks = cols / 8;
+  const int64_t most = chunks <= 64 ? 4096 : chunks <= 512 ? 1024 : chunks <= 1024 ? 512 : chunks <= 2048 ? 256 : 128;
+  int64_t g = rows < most ? rows : most;
+  if (chunks <= 64) g = (g + 3) / 4 * 4;  // a workgroup is 4 groups there
+  return g;
+}
 
 template <typename In>
 void launch_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
@@ -1003,13 +1014,6 @@ void launch_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
                        a);
   }
 #undef QSG_BWD
-}
-
-// groups of a backward pass: a multiple of 4 where a workgroup holds 4 rows
-int64_t bwd_groups(int64_t rows, int64_t cols) {
-  int64_t g = rows < kBwdGroups ? rows : kBwdGroups;
-  if (cols < 65 * 8) g = (g + 3) / 4 * 4;
-  return g;
 }
 
 }  // namespace
@@ -1100,7 +1104,7 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
   else
     launch_bwd<float>(a, groups, st);
   if (dgamma)
-    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, st, ws, groups, cols,
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, ws, groups, cols,
                        dgamma, accumulate);
 }
 

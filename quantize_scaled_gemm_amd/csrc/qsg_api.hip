@@ -462,7 +462,7 @@ int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, 
 
 int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t* n_chunks) {
   const char* fn = "qsg_grad_plan";
-  constexpr int64_t kChunk = 32768;  // elements
+  constexpr int64_t kChunk = 8192;  // elements: 8 16-byte loads a thread of fp32, all in flight at once
   if (!n_chunks || count < 0 || (count > 0 && !list)) return fail(QSG_ERR_ARG, "%s: null list or negative count", fn);
   int64_t total = 0;
   for (int64_t k = 0; k < count; ++k) {

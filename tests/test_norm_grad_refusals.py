@@ -8,7 +8,8 @@ import torch
 
 import quantize_scaled_gemm_amd as q
 from helpers import build_library, lib_is_stale
-from test_binding_cpu import BF, F32, U8, Dev, raises
+from test_binding_cpu import BF, F32, U8, raises
+from test_binding_cpu import Dev as Stand
 
 NAN, INF = float("nan"), float("inf")
 F64 = torch.float64
@@ -150,7 +151,32 @@ def test_clipping_refuses(lib):
     assert lib.qsg_grad_clip(64, 1, 64, 1.0, 66, None) == -3
 
 
-def test_binding_checks_the_forward():
+class Dev(Stand):
+    """A stand-in for a GPU tensor whose address may be asked for."""
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.fixture
+def no_call(lib, monkeypatch):
+    """A library whose calls that launch must not be reached."""
+
+    class Lib:
+        qsg_rmsnorm_bwd_workspace = lib.qsg_rmsnorm_bwd_workspace
+        qsg_grad_plan = lib.qsg_grad_plan
+
+        def __getattr__(self, name):
+            def reached(*args):
+                raise AssertionError(f"the binding must reject this call before it reaches {name}")
+
+            return reached
+
+    monkeypatch.setattr(q, "load_library", Lib)
+    monkeypatch.setattr(q, "_stream", lambda stream: None)
+
+
+def test_binding_checks_the_forward(no_call):
     x, g, r = Dev((64, 256), BF), Dev((256,), BF), Dev((64,), F32)
     qq, s = Dev((64, 256), U8), Dev((64, 8), U8)
     M = q.MXFP8
@@ -169,7 +195,7 @@ def test_binding_checks_the_forward():
     raises(lambda: q.qsg_rmsnorm_quantize(Dev((64, 256), BF, strides=(1, 64)), g, 1e-5, M, q=qq, s=s), "contiguous")
 
 
-def test_binding_checks_the_backward(lib):
+def test_binding_checks_the_backward(no_call):
     x, g, r = Dev((64, 256), BF), Dev((256,), BF), Dev((64,), F32)
     ws = Dev((q.qsg_rmsnorm_bwd_workspace(64, 256),), U8)
     ws.element_size = lambda: 1
@@ -184,7 +210,7 @@ def test_binding_checks_the_backward(lib):
     raises(lambda: q.qsg_rmsnorm_bwd(x, x, g, r, x, workspace=small), "workspace must hold at least")
 
 
-def test_binding_checks_the_gradients():
+def test_binding_checks_the_gradients(no_call):
     a = Dev((4, 4), F32)
     a.device = "cuda:0"
     b = Dev((4, 4), BF)
