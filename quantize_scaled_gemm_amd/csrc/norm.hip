@@ -119,8 +119,19 @@ struct Chunk<float> {
   }
 };
 
-__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+// The same for an element that was loaded under a branch.  The compiler moves
+// a plain widen() into that branch, and so waits for the element there,
+// before it issues the loads that follow (backward 32768 x 1001: 85 us).
+__device__ __forceinline__ float widen_here(uint16_t v) {
+  uint32_t u = v;
+  asm("" : "+v"(u));
+  return __uint_as_float(u << 16);
+}
+__device__ __forceinline__ float widen_here(float v) { return v; }
+template <typename In>
+__device__ __forceinline__ float load1(const In* p) { return widen(*p); }
 // v rounded to the type, as binary32
 __device__ __forceinline__ float round1(const uint16_t*, float v) { return bf16lo(pack_bf16x2(v, 0.0f)); }
 __device__ __forceinline__ float round1(const float*, float v) { return v; }
@@ -158,20 +169,25 @@ __device__ __forceinline__ float dpp_add(float v) {
   return v + __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
 }
 
-// Sum of a wavefront's 64 values, the same in every lane (the rotates add in
-// another order in each lane, so one lane's sum is taken for all).
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over groups of 16 or 64 lanes, the same in every lane of a group: each
+// step adds two values that its two lanes hold in either order (quads by
+// exchanges, 16 lanes by mirrors, rows by swaps).
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float v) {
+  constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i gets 7 - i of its 8, 15 - i of its 16
   v = dpp_add<kDppXor1>(v);
   v = dpp_add<kDppXor2>(v);
-  v = dpp_add<kDppRor4>(v);
-  v = dpp_add<kDppRor8>(v);
-  const uint32_t u = __float_as_uint(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const uint32_t t = __float_as_uint(v);
-  const auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
-  v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane((int)__float_as_uint(v)));
+  v = dpp_add<kHalfMirror>(v);
+  v = dpp_add<kMirror>(v);
+  if constexpr (LANES == 64) {
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const uint32_t t = __float_as_uint(v);
+    const auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
 }
 
 // Sum over the TPR threads (consecutive ones of the workgroup) that share a
@@ -181,7 +197,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 // every wave passes after its reads.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
+  v = lane_sum<TPR < 64 ? TPR : 64>(v);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -303,7 +319,8 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
   constexpr bool EARLY = NCH <= 2;  // the weights fit beside the row: loaded once, before the first row arrives
   __shared__ float red[2][16];
   const int t = threadIdx.x % TPR;
-  const int sub = RPW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);  // uniform in a wave
+  int sub = threadIdx.x / TPR;
+  if constexpr (TPR >= 64) sub = __builtin_amdgcn_readfirstlane(sub);  // uniform in a wave
   const int all_chunks = (int)(a.cols / 8), all_rest = (int)(a.cols % 8);
   const float tscale = a.quant == Q_TENSOR ? *a.scale : 1.0f;
   uint32_t amax = 0;
@@ -322,14 +339,15 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
     // with barriers in the loop the last workgroup's spare threads stay in it, on a row that is not there
     const int64_t row = row0 + sub;
     const bool there = RPW == 1 || row < a.rows;
-    if (TPR == 64 && !there) break;
+    if (TPR <= 64 && !there) break;
     const int chunks = there ? all_chunks : 0, rest = there ? all_rest : 0;
     const In* x = reinterpret_cast<const In*>(a.x) + row * a.ldx;
     const In* r = reinterpret_cast<const In*>(a.r) + row * a.ldr;
     In* ho = reinterpret_cast<In*>(a.h) + row * a.ldh;
     Chunk<In> h[NCH];
-    float h1 = 0.0f;  // the element after the last whole chunk
-    if (t < rest) h1 = load1(x + chunks * 8 + t);
+    In x1 = 0, r1 = 0;  // the element after the last whole chunk
+    if (t < rest) x1 = x[chunks * 8 + t];
+    if (t < rest && a.r) r1 = r[chunks * 8 + t];
     if (!a.r) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
@@ -356,8 +374,9 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
           h[j0 + j].set(v);
         }
       }
-      if (t < rest) h1 = round1(x, h1 + load1(r + chunks * 8 + t));
     }
+    float h1 = widen_here(x1);
+    if (a.r) h1 = round1(x, h1 + widen_here(r1));
     if (a.h) {
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
@@ -471,13 +490,13 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
 template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
-  const bool wave = chunks <= 128;                               // a row is a wave's
-  const bool wide = !wave && chunks > 256 && a.rows <= 512;      // few rows: a row's own latency is all
+  const int tpr = chunks <= 32 ? 16 : chunks <= 128 ? 64 : chunks <= 1024 ? 256 : 512;  // threads a row
+  const bool wide = chunks > 256 && a.rows <= 512;  // few rows: a row's own latency is all
   // An amax output ends in one atomic per workgroup on one address, which the
   // memory side performs one at a time: a persistent grid of large workgroups.
   const bool large = a.amax_out && !wide && chunks <= (sizeof(In) == 2 ? 1024 : 512);
-  int64_t grid = wave ? (a.rows + 3) / 4 : a.rows;
-  if (large) grid = wave ? (a.rows + 15) / 16 : (a.rows + 3) / 4;
+  const int64_t rpw = wide || tpr == 512 ? 1 : (large ? 1024 : 256) / tpr;
+  int64_t grid = (a.rows + rpw - 1) / rpw;
   const int64_t cap = !a.amax_out ? 1 << 20 : large ? 256 : 1024;
   if (grid > cap) grid = cap;
   const dim3 g((unsigned)grid);
@@ -487,7 +506,9 @@ void launch_row(const NormArgs& a, hipStream_t st) {
     if (large) QSG_ROW(TPR, NCH, 1024); \
     else QSG_ROW(TPR, NCH, 256);       \
   } while (0)
-  if (chunks <= 64) QSG_ROWS(64, 1);
+  if (chunks <= 16) QSG_ROWS(16, 1);
+  else if (chunks <= 32) QSG_ROWS(16, 2);
+  else if (chunks <= 64) QSG_ROWS(64, 1);
   else if (chunks <= 128) QSG_ROWS(64, 2);
   else if (chunks <= 256) QSG_ROWS(256, 1);
   else if (wide && chunks <= 1024) QSG_ROW(1024, 1, 1024);
@@ -496,8 +517,8 @@ void launch_row(const NormArgs& a, hipStream_t st) {
   else if (chunks <= 1024) {
     if constexpr (sizeof(In) == 2) QSG_ROWS(256, 4);
     else QSG_ROW(256, 4, 256);
-  } else if (chunks <= 2048) QSG_ROW(256, 8, 256);
-  else hipLaunchKernelGGL(norm_long_kernel<In>, g, dim3(256), 0, st, a);
+  } else if (chunks <= 2048) QSG_ROW(512, 4, 512);
+  else hipLaunchKernelGGL(norm_long_kernel<In>, g, dim3(256), 0, st, a);  // one row a workgroup, as counted above
 #undef QSG_ROWS
 #undef QSG_ROW
 }
@@ -534,10 +555,14 @@ constexpr int CT_ROWS = 128;  // rows of a tile: a column's run in qt is 128 byt
 // words puts the 64 words that a wave writes at once on 64 banks.
 constexpr int CT_STRIDE = CT_ROWS / 4 + 1;
 
-// Codes of COLS columns from LDS to qt: 16 rows (16 bytes) a lane, 8 lanes a run.
+// Codes of COLS columns from LDS to qt: 16 rows (16 bytes) a lane, 8 lanes a
+// run.  Runs that are whole cache lines stream out; others stay in L2, where
+// the run of the tile below completes their lines (rows = 10000: 44 -> 26 us
+// for 10000 x 5008; whole lines: streaming is 3-5 % faster).
 template <int COLS>
 __device__ __forceinline__ void store_columns(const uint32_t* codes, uint8_t* qt, int64_t rows, int64_t cols,
                                               int64_t r0, int64_t c0) {
+  const bool lines = rows % 128 == 0 && (uintptr_t)qt % 128 == 0;
 #pragma unroll
   for (int k = 0; k < COLS * 8 / 256; ++k) {
     const int id = k * 256 + threadIdx.x, col = id >> 3, r = (id & 7) * 16;
@@ -546,7 +571,10 @@ __device__ __forceinline__ void store_columns(const uint32_t* codes, uint8_t* qt
     uint8_t* p = qt + (c0 + col) * rows + r0 + r;
     if (c0 + col < cols) {
       if (r0 + r + 16 <= rows) {
-        put16<true>(p, v);
+        if (lines)
+          put16<true>(p, v);
+        else
+          put16<false>(p, v);
       } else {
         for (int b = 0; b < 16; ++b)
           if (r0 + r + b < rows) p[b] = (uint8_t)(codes[col * CT_STRIDE + ((r + b) >> 2)] >> (8 * (b & 3)));
@@ -652,7 +680,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
       if (a.q) {
         uint8_t* p = a.q + (r + j) * a.cols + c;
         if (full) {
-          put8<true>(p, rq[j]);
+          put8<false>(p, rq[j]);  // half a line: the next tile completes it in L2
         } else if (r + j < a.rows) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -812,6 +840,16 @@ struct NormBwdArgs {
   float* dots;       // rows: sum(dn h), wide rows only
 };
 
+// Sum over the 4 rows of 16 lanes of a wave, lane by lane.
+__device__ __forceinline__ float add_groups(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const uint32_t t = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane32_swap(t, t, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // A group of TPR threads takes rows group, group + groups, ... and holds a
 // row in registers, NCH chunks per thread; its share of dgamma stays in
 // registers until the end.  WIDE: the rows' dots are read from a.dots, and
@@ -821,7 +859,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
   constexpr int THREADS = TPR < 256 ? 256 : TPR, RPW = THREADS / TPR;
   __shared__ float red[2][16];
   const int t = threadIdx.x % TPR;
-  const int sub = RPW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
+  int sub = threadIdx.x / TPR;
+  if constexpr (TPR >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
   const int64_t group = (int64_t)blockIdx.x * RPW + sub, groups = (int64_t)gridDim.x * RPW;
   const int64_t c0 = WIDE ? (int64_t)blockIdx.y * (8 * TPR * NCH) : 0;
   const int64_t here = WIDE && a.cols - c0 > 8 * TPR * NCH ? 8 * TPR * NCH : a.cols - c0;  // columns of this piece
@@ -842,7 +881,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
     const In* pdr = reinterpret_cast<const In*>(a.dres) + row * a.lddres + c0;
     In* pdx = reinterpret_cast<In*>(a.dx) + row * a.lddx + c0;
     Chunk<In> dy[NCH], h[NCH], dr[NCH];
-    float dy1 = 0.0f, h1 = 0.0f, dr1 = 0.0f;
+    In dy1r = 0, h1r = 0, dr1r = 0;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const uint32_t k = j * TPR + t;
@@ -850,8 +889,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
       h[j].load(ph + k * 8, k < (uint32_t)chunks);
     }
     if (t < rest) {
-      dy1 = load1(pdy + chunks * 8 + t);
-      h1 = load1(ph + chunks * 8 + t);
+      dy1r = pdy[chunks * 8 + t];
+      h1r = ph[chunks * 8 + t];
     }
     if (a.dres) {
 #pragma unroll
@@ -859,9 +898,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
         const uint32_t k = j * TPR + t;
         dr[j].load(pdr + k * 8, k < (uint32_t)chunks);
       }
-      if (t < rest) dr1 = load1(pdr + chunks * 8 + t);
+      if (t < rest) dr1r = pdr[chunks * 8 + t];
     }
     const float rstd = a.rstd[row];
+    const float dy1 = widen_here(dy1r), h1 = widen_here(h1r), dr1 = widen_here(dr1r);
     float dot;
     if constexpr (WIDE) {
       dot = a.dots[row];
@@ -900,7 +940,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
     }
   }
   if (a.partial) {
-    float* p = a.partial + group * a.cols + c0;
+    int64_t slot = group;
+    if constexpr (TPR == 16) {
+      // the 4 groups of a wave leave one partial
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j][i] = add_groups(acc[j][i]);
+      acc1 = add_groups(acc1);
+      if ((threadIdx.x & 63) >= 16) return;
+      slot = group / 4;
+    }
+    float* p = a.partial + slot * a.cols + c0;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const uint32_t k = j * TPR + t;
@@ -985,23 +1036,33 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* partial,
 constexpr int64_t kBwdMostCols = 16391;  // of a row held in registers: 2048 chunks and 7 elements
 constexpr int64_t kBwdPiece = 2048;      // columns of a workgroup beyond that
 
-// Groups that share the rows: about what the card holds at once, since each
-// leaves a partial dgamma (4 bytes a column, written and read again).
-int64_t bwd_groups(int64_t rows, int64_t cols) {
+// Partial sums of dgamma that a backward pass leaves (4 bytes a column each,
+// written and read again): one per group of threads that shares the rows, or
+// per wave of 4 groups; about as many groups as the card holds at once.  A
+// multiple of 4 where a workgroup leaves 4.
+int64_t bwd_partials(int64_t rows, int64_t cols) {
   const int64_t chunks = cols / 8;
-  const int64_t most = chunks <= 64 ? 4096 : chunks <= 512 ? 1024 : chunks <= 1024 ? 512 : chunks <= 2048 ? 256 : 128;
-  int64_t g = rows < most ? rows : most;
-  if (chunks <= 64) g = (g + 3) / 4 * 4;  // a workgroup is 4 groups there
+  const int64_t most = chunks <= 32   ? 2048
+                       : chunks <= 64 ? 4096
+                       : chunks <= 512 ? 1024
+                       : chunks <= 1024 ? 512
+                       : chunks <= 2048 ? 256
+                                        : 128;
+  int64_t g = chunks <= 32 ? (rows + 3) / 4 : rows;
+  if (g > most) g = most;
+  if (chunks <= 64) g = (g + 3) / 4 * 4;
   return g;
 }
 
 template <typename In>
-void launch_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
+void launch_bwd(const NormBwdArgs& a, int64_t partials, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
-#define QSG_BWD(TPR, NCH)                                                                          \
-  hipLaunchKernelGGL((norm_bwd_kernel<In, TPR, NCH, false>),                                       \
-                     dim3((unsigned)(groups / (TPR < 256 ? 256 / TPR : 1))), dim3(TPR < 256 ? 256 : TPR), 0, st, a)
-  if (chunks <= 64) QSG_BWD(64, 1);
+#define QSG_BWD(TPR, NCH)                                                                        \
+  hipLaunchKernelGGL((norm_bwd_kernel<In, TPR, NCH, false>),                                     \
+                     dim3((unsigned)(partials / (TPR <= 64 ? 4 : 1))), dim3(TPR < 256 ? 256 : TPR), 0, st, a)
+  if (chunks <= 16) QSG_BWD(16, 1);
+  else if (chunks <= 32) QSG_BWD(16, 2);
+  else if (chunks <= 64) QSG_BWD(64, 1);
   else if (chunks <= 256) QSG_BWD(256, 1);
   else if (chunks <= 512) QSG_BWD(256, 2);
   else if (chunks <= 1024) QSG_BWD(256, 4);
@@ -1010,7 +1071,7 @@ void launch_bwd(const NormBwdArgs& a, int64_t groups, hipStream_t st) {
     int64_t g = a.rows < 4096 ? a.rows : 4096;
     hipLaunchKernelGGL(norm_bwd_dot_kernel<In>, dim3((unsigned)g), dim3(256), 0, st, a);
     const int64_t pieces = (a.cols + kBwdPiece - 1) / kBwdPiece;
-    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, true>), dim3((unsigned)groups, (unsigned)pieces), dim3(256), 0, st,
+    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, true>), dim3((unsigned)partials, (unsigned)pieces), dim3(256), 0, st,
                        a);
   }
 #undef QSG_BWD
@@ -1076,7 +1137,7 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
 
 int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return 0;
-  return (bwd_groups(rows, cols) * cols + (cols > kBwdMostCols ? rows : 0)) * 4;
+  return (bwd_partials(rows, cols) * cols + (cols > kBwdMostCols ? rows : 0)) * 4;
 }
 
 void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
@@ -1090,7 +1151,7 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
     }
     return;
   }
-  const int64_t groups = bwd_groups(rows, cols);
+  const int64_t partials = bwd_partials(rows, cols);
   float* ws = reinterpret_cast<float*>(workspace);
   NormBwdArgs a{};
   a.dy = dy; a.h = h; a.dres = dres;
@@ -1098,13 +1159,13 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
   a.gamma = gamma; a.gamma_bf16 = gamma_dtype == 1;
   a.rstd = rstd; a.dx = dx;
   a.partial = dgamma ? ws : nullptr;
-  a.dots = ws + groups * cols;
+  a.dots = ws + partials * cols;
   if (dtype == 1)
-    launch_bwd<uint16_t>(a, groups, st);
+    launch_bwd<uint16_t>(a, partials, st);
   else
-    launch_bwd<float>(a, groups, st);
+    launch_bwd<float>(a, partials, st);
   if (dgamma)
-    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, ws, groups, cols,
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, ws, partials, cols,
                        dgamma, accumulate);
 }
 
