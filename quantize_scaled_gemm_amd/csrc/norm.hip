@@ -854,28 +854,34 @@ __device__ __forceinline__ float add_groups(float v) {
 // row in registers, NCH chunks per thread; its share of dgamma stays in
 // registers until the end.  WIDE: the rows' dots are read from a.dots, and
 // blockIdx.y is the piece of 8 TPR NCH columns.
-template <typename In, int TPR, int NCH, bool WIDE>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdArgs a) {
-  constexpr int THREADS = TPR < 256 ? 256 : TPR, RPW = THREADS / TPR;
+template <typename In, int TPR, int NCH, int BLK, bool WIDE>
+__global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int RPW = BLK / TPR;
+  constexpr bool JOIN = TPR > 64 && RPW > 1;  // the groups of a workgroup leave one partial
   __shared__ float red[2][16];
+  __shared__ float joined[JOIN ? (RPW - 1) * TPR * 8 : 1];
   const int t = threadIdx.x % TPR;
   int sub = threadIdx.x / TPR;
   if constexpr (TPR >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
   const int64_t group = (int64_t)blockIdx.x * RPW + sub, groups = (int64_t)gridDim.x * RPW;
   const int64_t c0 = WIDE ? (int64_t)blockIdx.y * (8 * TPR * NCH) : 0;
   const int64_t here = WIDE && a.cols - c0 > 8 * TPR * NCH ? 8 * TPR * NCH : a.cols - c0;  // columns of this piece
-  const int chunks = (int)(here / 8), rest = (int)(here % 8);
+  const int all_chunks = (int)(here / 8), all_rest = (int)(here % 8);
   float g[NCH][8], acc[NCH][8], g1 = 0.0f, acc1 = 0.0f;
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     const uint32_t k = j * TPR + t;
-    load_gamma(g[j], a.gamma, a.gamma_bf16, c0 + k * 8, k < (uint32_t)chunks);
+    load_gamma(g[j], a.gamma, a.gamma_bf16, c0 + k * 8, k < (uint32_t)all_chunks);
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
   }
-  if (t < rest) g1 = load_gamma1(a.gamma, a.gamma_bf16, c0 + chunks * 8 + t);
+  if (t < all_rest) g1 = load_gamma1(a.gamma, a.gamma_bf16, c0 + all_chunks * 8 + t);
   int turn = 0;
-  for (int64_t row = group; row < a.rows; row += groups, turn ^= 1) {
+  for (int64_t row = group; row - sub < a.rows; row += groups, turn ^= 1) {
+    // with barriers in the loop spare threads stay in it, on a row that is not there
+    const bool there = RPW == 1 || row < a.rows;
+    if (TPR <= 64 && !there) break;
+    const int chunks = there ? all_chunks : 0, rest = there ? all_rest : 0;
     const In* pdy = reinterpret_cast<const In*>(a.dy) + row * a.lddy + c0;
     const In* ph = reinterpret_cast<const In*>(a.h) + row * a.ldh + c0;
     const In* pdr = reinterpret_cast<const In*>(a.dres) + row * a.lddres + c0;
@@ -900,7 +906,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
       }
       if (t < rest) dr1r = pdr[chunks * 8 + t];
     }
-    const float rstd = a.rstd[row];
+    const float rstd = there ? a.rstd[row] : 0.0f;
     const float dy1 = widen_here(dy1r), h1 = widen_here(h1r), dr1 = widen_here(dr1r);
     float dot;
     if constexpr (WIDE) {
@@ -951,6 +957,30 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
       if ((threadIdx.x & 63) >= 16) return;
       slot = group / 4;
     }
+    if constexpr (JOIN) {
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        if (sub > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) joined[((sub - 1) * 8 + i) * TPR + t] = acc[j][i];
+        }
+        __syncthreads();
+        if (sub == 0) {
+#pragma unroll
+          for (int k = 0; k < RPW - 1; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j][i] += joined[(k * 8 + i) * TPR + t];
+        }
+        __syncthreads();
+      }
+      if (sub > 0) joined[(sub - 1) * TPR + t] = acc1;
+      __syncthreads();
+      if (sub > 0) return;
+#pragma unroll
+      for (int k = 0; k < RPW - 1; ++k) acc1 += joined[k * TPR + t];
+      slot = blockIdx.x;
+    }
+    const int chunks = all_chunks, rest = all_rest;
     float* p = a.partial + slot * a.cols + c0;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
@@ -1036,43 +1066,58 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* partial,
 constexpr int64_t kBwdMostCols = 16391;  // of a row held in registers: 2048 chunks and 7 elements
 constexpr int64_t kBwdPiece = 2048;      // columns of a workgroup beyond that
 
-// Partial sums of dgamma that a backward pass leaves (4 bytes a column each,
-// written and read again): one per group of threads that shares the rows, or
-// per wave of 4 groups; about as many groups as the card holds at once.  A
-// multiple of 4 where a workgroup leaves 4.
-int64_t bwd_partials(int64_t rows, int64_t cols) {
+// How a backward pass shares its rows: a workgroup of `blk` threads takes
+// blk / tpr rows at a time, and `partials` sums of dgamma are left (4 bytes a
+// column each, written and read again): one per workgroup, or per wave where
+// rows are a wave's or less.
+struct BwdPlan {
+  int tpr, blk;
+  int64_t grid, partials;
+};
+
+BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   const int64_t chunks = cols / 8;
-  const int64_t most = chunks <= 32   ? 2048
-                       : chunks <= 64 ? 4096
-                       : chunks <= 512 ? 1024
-                       : chunks <= 1024 ? 512
-                       : chunks <= 2048 ? 256
-                                        : 128;
-  int64_t g = chunks <= 32 ? (rows + 3) / 4 : rows;
-  if (g > most) g = most;
-  if (chunks <= 64) g = (g + 3) / 4 * 4;
-  return g;
+  BwdPlan p;
+  p.tpr = chunks <= 32 ? 16 : chunks <= 64 ? 64 : chunks <= 1024 ? 256 : chunks <= 2048 ? 1024 : 256;
+  p.blk = p.tpr == 1024 ? 1024 : 256;
+  // about as many workgroups as the card holds at once
+  int64_t most = chunks <= 32 ? 512 : chunks <= 512 ? 1024 : chunks <= 1024 ? 512 : chunks <= 2048 ? 256 : 128;
+  // Four rows to a workgroup, which adds their shares of dgamma in LDS: less
+  // to write and read again, for a barrier that four rows share.  [measured,
+  // joined against separate, us] 1024 x 4096 14.6 / 18.8, 1024 x 1024 9.5 /
+  // 11.5, 32768 x 4096 184 / 202; but 256 x 1024 8.3 / 7.5, 8192 x 1024
+  // 24.9 / 22.5, 4096 x 2048 23.0 / 21.2.
+  if (p.tpr == 256 && chunks <= 512 && rows >= 384 && (rows <= 1280 || chunks > 320)) {
+    p.blk = 1024;
+    most = 512;
+  }
+  const int64_t rpw = p.blk / p.tpr;
+  p.grid = (rows + rpw - 1) / rpw;
+  if (p.grid > most) p.grid = most;
+  p.partials = p.tpr <= 64 ? p.grid * 4 : p.grid;
+  return p;
 }
 
 template <typename In>
-void launch_bwd(const NormBwdArgs& a, int64_t partials, hipStream_t st) {
+void launch_bwd(const NormBwdArgs& a, const BwdPlan& p, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
-#define QSG_BWD(TPR, NCH)                                                                        \
-  hipLaunchKernelGGL((norm_bwd_kernel<In, TPR, NCH, false>),                                     \
-                     dim3((unsigned)(partials / (TPR <= 64 ? 4 : 1))), dim3(TPR < 256 ? 256 : TPR), 0, st, a)
-  if (chunks <= 16) QSG_BWD(16, 1);
-  else if (chunks <= 32) QSG_BWD(16, 2);
-  else if (chunks <= 64) QSG_BWD(64, 1);
-  else if (chunks <= 256) QSG_BWD(256, 1);
-  else if (chunks <= 512) QSG_BWD(256, 2);
-  else if (chunks <= 1024) QSG_BWD(256, 4);
-  else if (chunks <= 2048) QSG_BWD(1024, 2);
+  const dim3 g((unsigned)p.grid);
+#define QSG_BWD(TPR, NCH, BLK) hipLaunchKernelGGL((norm_bwd_kernel<In, TPR, NCH, BLK, false>), g, dim3(BLK), 0, st, a)
+  if (chunks <= 16) QSG_BWD(16, 1, 256);
+  else if (chunks <= 32) QSG_BWD(16, 2, 256);
+  else if (chunks <= 64) QSG_BWD(64, 1, 256);
+  else if (chunks <= 256 && p.blk == 1024) QSG_BWD(256, 1, 1024);
+  else if (chunks <= 256) QSG_BWD(256, 1, 256);
+  else if (chunks <= 512 && p.blk == 1024) QSG_BWD(256, 2, 1024);
+  else if (chunks <= 512) QSG_BWD(256, 2, 256);
+  else if (chunks <= 1024) QSG_BWD(256, 4, 256);
+  else if (chunks <= 2048) QSG_BWD(1024, 2, 1024);
   else {
-    int64_t g = a.rows < 4096 ? a.rows : 4096;
-    hipLaunchKernelGGL(norm_bwd_dot_kernel<In>, dim3((unsigned)g), dim3(256), 0, st, a);
+    const int64_t n = a.rows < 4096 ? a.rows : 4096;
+    hipLaunchKernelGGL(norm_bwd_dot_kernel<In>, dim3((unsigned)n), dim3(256), 0, st, a);
     const int64_t pieces = (a.cols + kBwdPiece - 1) / kBwdPiece;
-    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, true>), dim3((unsigned)partials, (unsigned)pieces), dim3(256), 0, st,
-                       a);
+    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, 256, true>), dim3((unsigned)p.grid, (unsigned)pieces), dim3(256), 0,
+                       st, a);
   }
 #undef QSG_BWD
 }
@@ -1137,7 +1182,7 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
 
 int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return 0;
-  return (bwd_partials(rows, cols) * cols + (cols > kBwdMostCols ? rows : 0)) * 4;
+  return (bwd_plan(rows, cols).partials * cols + (cols > kBwdMostCols ? rows : 0)) * 4;
 }
 
 void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
@@ -1151,7 +1196,7 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
     }
     return;
   }
-  const int64_t partials = bwd_partials(rows, cols);
+  const BwdPlan p = bwd_plan(rows, cols);
   float* ws = reinterpret_cast<float*>(workspace);
   NormBwdArgs a{};
   a.dy = dy; a.h = h; a.dres = dres;
@@ -1159,13 +1204,13 @@ void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dty
   a.gamma = gamma; a.gamma_bf16 = gamma_dtype == 1;
   a.rstd = rstd; a.dx = dx;
   a.partial = dgamma ? ws : nullptr;
-  a.dots = ws + partials * cols;
+  a.dots = ws + p.partials * cols;
   if (dtype == 1)
-    launch_bwd<uint16_t>(a, partials, st);
+    launch_bwd<uint16_t>(a, p, st);
   else
-    launch_bwd<float>(a, partials, st);
+    launch_bwd<float>(a, p, st);
   if (dgamma)
-    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, ws, partials, cols,
+    hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, st, ws, p.partials, cols,
                        dgamma, accumulate);
 }
 
