@@ -417,7 +417,7 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
  *   amax_out_dev  out, DELAYED only: 1 float, max |y| (for qsg_amax_update),
  *              or NULL.
  * One of y, q and qt is needed.  Pointers are aligned to their elements;
- * cols <= 2^30 (QSG_ERR_UNSUPPORTED beyond).
+ * cols <= 2^24 (QSG_ERR_UNSUPPORTED beyond).
  * One pass over the data row-wise; with qt or TENSORWISE a second kernel
  * reads h (x without a residual) back.  rows == 0 or cols == 0 writes only
  * TENSORWISE's s (amax 0) and DELAYED's amax (0).  A row of zeros with
@@ -453,7 +453,7 @@ int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
  *              4-byte aligned; nothing has to be in it before, and calls that
  *              overlap in time need one each.
  * Sums are binary32 in an order that depends on the shape alone, so equal
- * calls give equal bits.  rows == 0 writes dgamma = 0 unless accumulate. */
+ * calls give equal bits.  cols <= 2^24 (QSG_ERR_UNSUPPORTED).  rows == 0 writes dgamma = 0 unless accumulate. */
 int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
                     int64_t lddy, int64_t ldh, int64_t lddres, const void* gamma, int gamma_dtype, const float* rstd,
                     void* dx, int64_t lddx, float* dgamma, int accumulate, void* workspace, void* stream);

@@ -596,7 +596,7 @@ struct ColArgs {
   uint8_t* q;          // Q_TENSOR: rows x cols, or null
   uint8_t* qt;         // cols x rows, or null (Q_TENSOR only)
   void* st;
-  int64_t tiles_c, tiles;
+  int64_t tiles_c, tiles, tile0;
 };
 
 constexpr int CT_COLS = 64;
@@ -625,7 +625,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   // last rows first: they are the ones that the first pass has left in the caches
-  const int64_t tile = a.tiles - 1 - blockIdx.x;
+  const int64_t tile = a.tiles - 1 - (a.tile0 + blockIdx.x);
   const int64_t r0 = tile_start(tile / a.tiles_c, CT_ROWS, a.rows), c0 = tile_start(tile % a.tiles_c, CT_COLS, a.cols);
   const int64_t r = r0 + ty * 4, c = c0 + tx * 8;
   const bool full = a.rows >= CT_ROWS && a.cols >= CT_COLS;
@@ -666,7 +666,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
     float s;
     if (a.three) {
       s = scale_from_amax(a.three[0], fp8_max(a.fmt), a.margin);
-      if (blockIdx.x == 0 && threadIdx.x == 0) {
+      if (a.tile0 + blockIdx.x == 0 && threadIdx.x == 0) {
         a.three[1] = s;
         a.three[2] = __fdiv_rn(1.0f, s);
       }
@@ -781,10 +781,10 @@ constexpr int TT_COLS = 128;
 // column-wise copy has the row-wise one's codes, and reading those back costs
 // half of reading h.  Thread t holds rows 4 (t / 8) .. + 3 of 16 columns.
 __global__ __launch_bounds__(256) void transpose_bytes_kernel(const uint8_t* q, uint8_t* qt, int64_t rows, int64_t cols,
-                                                              int64_t tiles_c, int64_t tiles) {
+                                                              int64_t tiles_c, int64_t tiles, int64_t tile0) {
   __shared__ uint32_t codes[TT_COLS * CT_STRIDE];
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-  const int64_t tile = tiles - 1 - blockIdx.x;  // last rows first, as above
+  const int64_t tile = tiles - 1 - (tile0 + blockIdx.x);  // last rows first, as above
   const int64_t r0 = tile_start(tile / tiles_c, CT_ROWS, rows), c0 = tile_start(tile % tiles_c, TT_COLS, cols);
   const int64_t r = r0 + ty * 4, c = c0 + tx * 16;
   u32x4 v[4];
@@ -814,14 +814,18 @@ __global__ __launch_bounds__(256) void transpose_bytes_kernel(const uint8_t* q, 
   store_columns<TT_COLS>(codes, qt, rows, cols, r0, c0);
 }
 
+constexpr int64_t kMostTiles = 1 << 23;  // of a launch, whose threads are counted in 32 bits
+
 template <typename In>
 void launch_col(ColArgs a, hipStream_t st) {
   a.tiles_c = (a.cols + CT_COLS - 1) / CT_COLS;
   a.tiles = (a.rows + CT_ROWS - 1) / CT_ROWS * a.tiles_c;
-  const dim3 g((unsigned)a.tiles);
-  if (a.quant == Q_TENSOR) hipLaunchKernelGGL((norm_col_kernel<In, Q_TENSOR>), g, dim3(256), 0, st, a);
-  else if (a.quant == Q_MX) hipLaunchKernelGGL((norm_col_kernel<In, Q_MX>), g, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((norm_col_kernel<In, Q_BLOCK>), g, dim3(256), 0, st, a);
+  for (a.tile0 = 0; a.tile0 < a.tiles; a.tile0 += kMostTiles) {
+    const dim3 g((unsigned)(a.tiles - a.tile0 < kMostTiles ? a.tiles - a.tile0 : kMostTiles));
+    if (a.quant == Q_TENSOR) hipLaunchKernelGGL((norm_col_kernel<In, Q_TENSOR>), g, dim3(256), 0, st, a);
+    else if (a.quant == Q_MX) hipLaunchKernelGGL((norm_col_kernel<In, Q_MX>), g, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((norm_col_kernel<In, Q_BLOCK>), g, dim3(256), 0, st, a);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -853,7 +857,7 @@ __device__ __forceinline__ float add_groups(float v) {
 // A group of TPR threads takes rows group, group + groups, ... and holds a
 // row in registers, NCH chunks per thread; its share of dgamma stays in
 // registers until the end.  WIDE: the rows' dots are read from a.dots, and
-// blockIdx.y is the piece of 8 TPR NCH columns.
+// blockIdx.x is the piece of 8 TPR NCH columns (blockIdx.y the group).
 template <typename In, int TPR, int NCH, int BLK, bool WIDE>
 __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPW = BLK / TPR;
@@ -863,8 +867,9 @@ __global__ __launch_bounds__(BLK) void norm_bwd_kernel(NormBwdArgs a) {
   const int t = threadIdx.x % TPR;
   int sub = threadIdx.x / TPR;
   if constexpr (TPR >= 64) sub = __builtin_amdgcn_readfirstlane(sub);
-  const int64_t group = (int64_t)blockIdx.x * RPW + sub, groups = (int64_t)gridDim.x * RPW;
-  const int64_t c0 = WIDE ? (int64_t)blockIdx.y * (8 * TPR * NCH) : 0;
+  const int64_t group = (int64_t)(WIDE ? blockIdx.y : blockIdx.x) * RPW + sub;
+  const int64_t groups = (int64_t)(WIDE ? gridDim.y : gridDim.x) * RPW;
+  const int64_t c0 = WIDE ? (int64_t)blockIdx.x * (8 * TPR * NCH) : 0;
   const int64_t here = WIDE && a.cols - c0 > 8 * TPR * NCH ? 8 * TPR * NCH : a.cols - c0;  // columns of this piece
   const int all_chunks = (int)(here / 8), all_rest = (int)(here % 8);
   float g[NCH][8], acc[NCH][8], g1 = 0.0f, acc1 = 0.0f;
@@ -1116,7 +1121,7 @@ void launch_bwd(const NormBwdArgs& a, const BwdPlan& p, hipStream_t st) {
     const int64_t n = a.rows < 4096 ? a.rows : 4096;
     hipLaunchKernelGGL(norm_bwd_dot_kernel<In>, dim3((unsigned)n), dim3(256), 0, st, a);
     const int64_t pieces = (a.cols + kBwdPiece - 1) / kBwdPiece;
-    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, 256, true>), dim3((unsigned)p.grid, (unsigned)pieces), dim3(256), 0,
+    hipLaunchKernelGGL((norm_bwd_kernel<In, 256, 1, 256, true>), dim3((unsigned)pieces, (unsigned)p.grid), dim3(256), 0,
                        st, a);
   }
 #undef QSG_BWD
@@ -1163,7 +1168,9 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
   if (!qt && !tensorwise) return;
   if (a.again) {
     const int64_t tc = (cols + TT_COLS - 1) / TT_COLS, tiles = (rows + CT_ROWS - 1) / CT_ROWS * tc;
-    hipLaunchKernelGGL(transpose_bytes_kernel, dim3((unsigned)tiles), dim3(256), 0, st, q, qt, rows, cols, tc, tiles);
+    for (int64_t at = 0; at < tiles; at += kMostTiles)
+      hipLaunchKernelGGL(transpose_bytes_kernel, dim3((unsigned)(tiles - at < kMostTiles ? tiles - at : kMostTiles)),
+                         dim3(256), 0, st, q, qt, rows, cols, tc, tiles, at);
     return;
   }
   ColArgs k{};

@@ -345,7 +345,7 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
   return check_launch(fn);
 }
 
-static constexpr int64_t kMostNormCols = 1 << 30;  // a column's index is 32 bits wide
+static constexpr int64_t kMostNormCols = 1 << 24;  // a column's index and a launch's threads are 32 bits wide
 
 int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                          int64_t ldr, const void* gamma, int gamma_dtype, float eps, const qsg_recipe* recipe,
@@ -356,7 +356,7 @@ int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t
   if (rc) return rc;
   if (!valid_dtype(gamma_dtype)) return fail(QSG_ERR_ARG, "%s: bad gamma dtype %d", fn, gamma_dtype);
   if (!(eps >= 0.0f && eps <= FLT_MAX)) return fail(QSG_ERR_ARG, "%s: eps must be finite and not negative", fn);
-  if (cols > kMostNormCols) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 2^30 cols", fn);
+  if (cols > kMostNormCols) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 2^24 cols", fn);
   const bool empty = rows == 0 || cols == 0;
   const int esz = esize(dtype);
   if (!empty) {
@@ -436,7 +436,7 @@ int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, 
   if (rc) return rc;
   rc = check_matrix(fn, h, dtype, rows, cols, ldh);
   if (rc) return rc;
-  if (cols > kMostNormCols) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 2^30 cols", fn);
+  if (cols > kMostNormCols) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 2^24 cols", fn);
   if (!valid_dtype(gamma_dtype)) return fail(QSG_ERR_ARG, "%s: bad gamma dtype %d", fn, gamma_dtype);
   if (dgamma && !aligned(dgamma, 4)) return fail(QSG_ERR_ALIGN, "%s: dgamma not aligned", fn);
   if (rows > 0 && cols > 0) {

@@ -87,7 +87,7 @@ def same(got, want, what):
 
 
 def forward(q, rng, rows, cols, dtype, recipe, fmt="e4m3", residual=True, t=True, y=False, gamma="bf16", margin=0,
-            rule="ceil", ld=None, offset=0, inplace=None, x=None, r=None, eps=EPS, check=True):
+            rule="ceil", ld=None, offset=0, inplace=None, x=None, r=None, w=None, eps=EPS, check=True):
     """One call, checked against the oracle; returns its outputs."""
     import torch
 
@@ -95,7 +95,7 @@ def forward(q, rng, rows, cols, dtype, recipe, fmt="e4m3", residual=True, t=True
     x = make(rng, rows, cols, dtype, 1.0, ld, offset) if x is None else x
     if residual and r is None:
         r = make(rng, rows, cols, dtype, 2.0, ld, offset)
-    w = weights(rng, cols, gamma)
+    w = weights(rng, cols, gamma) if w is None else w
     x0, r0 = to_np(x).copy(), to_np(r).copy() if residual else None
     h = {"x": x, "r": r}.get(inplace)
     if h is None and residual:
@@ -235,6 +235,43 @@ def test_forward_special_rows(q, recipe, t):
     assert (qq[9, 200] & 0x7F) == 0x7F and ((np.delete(qq[9], 200) & 0x7F) == 0).all()
     if recipe in ("mx", "1x128"):
         assert ((np.delete(qq, [5, 9], axis=0) & 0x7F) != 0x7F).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("recipe, fmt, margin, rule", [("mx", "e4m3", 0, "ceil"), ("mx", "e5m2", 0, "ceil"),
+                                                       ("mx", "e4m3", 40, "ceil"), ("mx", "e4m3", 0, "ocp"),
+                                                       ("1x128", "e4m3", 0, "ceil"), ("tensorwise", "e4m3", 0, "ceil")])
+def test_forward_extreme_weights_and_rows(q, dtype, recipe, fmt, margin, rule):
+    """Weights from the smallest subnormal to near the largest number, zeros
+    among them, on rows from 1e-15 to 1e15: blocks whose values are subnormal,
+    overflow to infinity, or are scaled by the outermost powers of two."""
+    rng = np.random.default_rng(13)
+    rows, cols = 256, 256
+    x = make(rng, rows, cols, dtype)
+    x *= to_dev((10.0 ** rng.integers(-15, 16, (rows, 1))).astype(np.float32)).to(x.dtype)
+    x[64:96] = 0
+    w = np.float32(2.0) ** rng.integers(-149, 127, cols).astype(np.float32) * rng.choice([-1, 1], cols)
+    w[:64] = np.float32(2.0) ** rng.integers(-70, 70, 64).astype(np.float32)
+    w[64:128] *= np.float32(2.0) ** rng.integers(-60, 0, 64).astype(np.float32)
+    w[5], w[70], w[130] = 0.0, -0.0, 0.0
+    w = to_dev(w.astype(np.float32))
+    for t in (False, True):
+        forward(q, rng, rows, cols, dtype, recipe, fmt=fmt, margin=margin, rule=rule, x=x, w=w, residual=False, t=t,
+                eps=1e-30)
+
+
+def test_forward_weights_that_are_not_finite(q):
+    """An infinite and a NaN weight spoil their own columns and the blocks that
+    hold them, and nothing else."""
+    rng = np.random.default_rng(17)
+    w = weights(rng, 256, "f32")
+    w[40], w[200] = float("inf"), float("nan")
+    for recipe in ("mx", "1x128"):
+        o = forward(q, rng, 128, 256, "f32", recipe, w=w, check=False)
+        qt = to_np(o["qt"])
+        assert ((qt[200] & 0x7F) == 0x7F).all()
+        assert ((qt[40] & 0x7F) == 0x7E).all()
+        assert ((np.delete(qt, [40, 200], axis=0) & 0x7F) != 0x7F).all()
 
 
 def test_forward_zero_row_without_eps_is_nan(q):

@@ -54,7 +54,7 @@ TW, DL, B1 = (q.TENSORWISE, q.E4M3, 0, 0), (q.DELAYED, q.E4M3, 0, 0), (q.BLOCK_1
     (dict(recipe=B1, cols=192), -2), (dict(recipe=B1, s=66), -3),
     (dict(recipe=TW, s=None), -1), (dict(recipe=TW, s=66), -3), (dict(recipe=TW, qt=None, rstd=None), -1),
     (dict(recipe=TW, amax=64), -1), (dict(amax=64), -1), (dict(recipe=DL), -1), (dict(recipe=DL, scale=66), -3),
-    (dict(cols=(1 << 30) + 32, ldx=1 << 31, ldr=1 << 31, ldh=1 << 31), -4),
+    (dict(cols=(1 << 24) + 32, ldx=1 << 25, ldr=1 << 25, ldh=1 << 25), -4),
     (dict(recipe=DL, scale=64, amax=66), -3), (dict(y=33, recipe=DL, scale=64), -3),
 ])
 def test_forward_refuses(lib, kw, status):
@@ -80,6 +80,7 @@ B = dict(dy=4096, h=8192, dres=12288, dtype=1, rows=8, cols=256, lddy=256, ldh=2
     (dict(h=8193), -3), (dict(dres=12289), -3), (dict(dx=16385), -3), (dict(gamma=66), -3), (dict(rstd=66), -3),
     (dict(dgamma=130), -3), (dict(ws=258), -3), (dict(dx=8192), -1),        # dx may not be h
     (dict(dx=4096, lddy=512), -1), (dict(dx=12288, lddres=512), -1),
+    (dict(cols=(1 << 24) + 8, lddy=1 << 25, ldh=1 << 25, lddres=1 << 25, lddx=1 << 25), -4),
 ])
 def test_backward_refuses(lib, kw, status):
     a = dict(B, **kw)
