@@ -455,25 +455,25 @@ def qsg_gemm_nvfp4(a, sa, ts_a, b, sb, ts_b, c, stream=None):
 
 
 # The calls below take many tensors and are made for single tokens too, so
-# their checks ask each tensor for as little as they can and leave the wording
-# of a refusal to the checks above.
-_DTYPES = {}  # torch dtype -> (code, name); filled on first use
+# each tensor is asked for as little as accepts it; what is not accepted goes
+# to the checks above for the words of its refusal.
+_CODES = {}  # torch dtype -> (code of the ABI or None, name); filled on first use
 
 
-def _dtype_entry(dtype):
-    if not _DTYPES:
+def _codes():
+    if not _CODES:
         import torch
 
-        _DTYPES.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32"), torch.uint8: (None, "u8"),
-                        torch.float64: (None, "f64")})
-    return _DTYPES.get(dtype, (None, None))
+        _CODES.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32"), torch.uint8: (None, "u8"),
+                       torch.float64: (None, "f64")})
+    return _CODES
 
 
 def _rows(t, name):
     """(pointer, rows, cols, ld) of a view whose rows do not overlap."""
     if not t.is_cuda:
         raise QsgError(f"{name} must live on the GPU")
-    if t.dim() == 2 and t.is_contiguous():
+    if t.is_contiguous() and t.dim() == 2:
         rows, cols = t.shape
         return t.data_ptr(), rows, cols, cols or 1
     rows, cols, ld = _matrix(t)
@@ -482,15 +482,17 @@ def _rows(t, name):
     return t.data_ptr(), rows, cols, ld
 
 
-def _same_matrix(t, name, like):
-    """(pointer, ld) of a matrix of the shape and type of ``like``, or of none."""
+def _same_matrix(t, name, shape, dtype):
+    """(pointer, ld) of a matrix of this shape and type, or of none."""
     if t is None:
         return None, 0
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr(), shape[1] or 1
     p, rows, cols, ld = _rows(t, name)
-    if t.shape != like.shape:
-        raise QsgError(f"{name} is {rows}x{cols}, expected {like.shape[0]}x{like.shape[1]}")
-    if t.dtype is not like.dtype:
-        raise QsgError(f"{name} must be {like.dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise QsgError(f"{name} is {rows}x{cols}, expected {shape[0]}x{shape[1]}")
+    if t.dtype is not dtype:
+        raise QsgError(f"{name} must be {dtype} (got {t.dtype})")
     return p, ld
 
 
@@ -498,17 +500,18 @@ def _dense(t, name, numel, dtype, required=False):
     """Pointer of a buffer that _buffer accepts."""
     if t is None and not required or isinstance(t, int):
         return t
-    if t is None or _dtype_entry(t.dtype)[1] != dtype or t.numel() != numel or not t.is_cuda or not t.is_contiguous():
+    if t is None or _codes().get(t.dtype, (None, None))[1] != dtype or t.numel() != numel or not (
+            t.is_contiguous() and t.is_cuda):
         _buffer(t, name, numel, dtype)
     return t.data_ptr()
 
 
-def _weight(gamma, cols):
-    """(pointer, type) of a norm's weight."""
-    code, name = _dtype_entry(gamma.dtype)
-    if code is None:
-        raise QsgError(f"unsupported input dtype {gamma.dtype}")
-    return _dense(gamma, "gamma", cols, name), code
+def _float_code(t):
+    """(code, name) of a float type of the ABI."""
+    e = _codes().get(t.dtype)
+    if e is None or e[0] is None:
+        raise QsgError(f"unsupported input dtype {t.dtype}")
+    return e
 
 
 def _workspace(t, nbytes):
@@ -530,13 +533,12 @@ def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h
     column stride; h may be x or residual itself.  gamma (cols) is fp32 or
     bf16, rstd (rows) fp32; DELAYED takes its scale and returns amax_out."""
     px, rows, cols, ld = _rows(x, "x")
-    dt, dname = _dtype_entry(x.dtype)
-    if dt is None:
-        raise QsgError(f"unsupported input dtype {x.dtype}")
-    numel = rows * cols
-    pr, ldr = _same_matrix(residual, "residual", x)
-    ph, ldh = _same_matrix(h, "h", x)
-    pg, gt = _weight(gamma, cols)
+    dt, dname = _float_code(x)
+    gt, gname = _float_code(gamma)
+    numel, like = rows * cols, (x.shape, x.dtype)
+    pr, ldr = _same_matrix(residual, "residual", *like)
+    ph, ldh = _same_matrix(h, "h", *like)
+    pg = _dense(gamma, "gamma", cols, gname)
     prstd = _dense(rstd, "rstd", rows, "f32")
     py = _dense(y, "y", numel, dname)
     pq, pqt = _dense(q, "q", numel, "u8"), _dense(qt, "qt", numel, "u8")
@@ -572,13 +574,13 @@ def qsg_rmsnorm_bwd(dy, h, gamma, rstd, dx, dres=None, dgamma=None, accumulate=F
     dres, the gradient that reaches h directly; dgamma (cols fp32) written or
     accumulated.  workspace: qsg_rmsnorm_bwd_workspace(rows, cols) bytes."""
     pdy, rows, cols, lddy = _rows(dy, "dy")
-    dt = _dtype_entry(dy.dtype)[0]
-    if dt is None:
-        raise QsgError(f"unsupported input dtype {dy.dtype}")
-    ph, ldh = _same_matrix(h, "h", dy)
-    pdx, lddx = _same_matrix(dx, "dx", dy)
-    pdr, lddres = _same_matrix(dres, "dres", dy)
-    pg, gt = _weight(gamma, cols)
+    dt = _float_code(dy)[0]
+    gt, gname = _float_code(gamma)
+    like = (dy.shape, dy.dtype)
+    ph, ldh = _same_matrix(h, "h", *like)
+    pdx, lddx = _same_matrix(dx, "dx", *like)
+    pdr, lddres = _same_matrix(dres, "dres", *like)
+    pg = _dense(gamma, "gamma", cols, gname)
     prstd = _dense(rstd, "rstd", rows, "f32", True)
     pdg = _dense(dgamma, "dgamma", cols, "f32")
     pw = _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))

@@ -491,7 +491,7 @@ template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
   const int tpr = chunks <= 32 ? 16 : chunks <= 128 ? 64 : chunks <= 1024 ? 256 : 512;  // threads a row
-  const bool wide = chunks > 256 && a.rows <= 512;  // few rows: a row's own latency is all
+  const bool wide = chunks > 256 && a.rows <= 256;  // at most a workgroup a CU: a row's own latency is all
   // An amax output ends in one atomic per workgroup on one address, which the
   // memory side performs one at a time: a persistent grid of large workgroups.
   const bool large = a.amax_out && !wide && chunks <= (sizeof(In) == 2 ? 1024 : 512);
