@@ -6,7 +6,15 @@
 // The tensors are cut into chunks on the host (qsg_grad_plan) and the table
 // of chunks lies in device memory, so one launch covers any number of
 // tensors.  Squares and sums are binary64: a binary32 square loses gradients
-// below 2^-75 and overflows above 2^64.
+// below 2^-75 and overflows above 2^64, and the conversion and the fma are a
+// small part of the time that an element takes to arrive.
+//
+// Both passes are bound by HBM.  [measured, MI355X, 302 M fp32 gradients] the
+// sum reads 1.21 GB in 177 us (6.8 TB/s), the clip reads and writes 2.42 GB in
+// 412 us (5.9 TB/s); a 2 GiB device copy moves 4.9-5.1 TB/s.  Chunks of 8192
+// elements: 16384 435 us and 32768 439 us for the clip (the last round of
+// workgroups is shorter).  Plain instead of non-temporal loads in the sum: 203
+// us, and 418 for the clip after them.
 #include <hip/hip_runtime.h>
 
 #include "qsg.h"
@@ -136,7 +144,7 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(const qsg_grad* table, i
   if (k > 1.0f) k = 1.0f;  // a NaN stays
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = norm;
   for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
-    const qsg_grad t = table[n - 1 - c];
+    const qsg_grad t = table[n - 1 - c];  // last chunks first: the sum has read them last
     if (k == 1.0f && t.out == t.g) continue;  // every product is the value itself
     if (t.dtype == QSG_BF16)
       chunk_scale(reinterpret_cast<const uint16_t*>(t.g), reinterpret_cast<uint16_t*>(t.out), (int)t.n, k);

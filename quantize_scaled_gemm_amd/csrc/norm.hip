@@ -17,6 +17,16 @@
 // that ask only for the element's alignment (gfx950 takes global accesses at
 // any byte address), so odd leading dimensions and offsets use the same
 // instructions.
+//
+// Every kernel here is bound by HBM (a few rows by latency).  [measured,
+// MI355X] A 2 GiB device copy moves 4.9-5.1 TB/s; the row kernel moves 6.2
+// (32768 x 4096, MXFP8 row-wise: 939 MB in 150 us), the column kernel 6.1
+// counting what it reads from the caches (268 MB of h and 134 MB of codes in
+// 66 us), the backward kernel 5.8 (16384 x 7168 with a residual gradient: 940
+// MB in 160 us).  One launch that kept 128 rows of h on the chip for both
+// copies would save the second reading of h (2 of 10 bytes an element), but
+// 128 rows of 4096 columns are 1 MB, twice a CU's registers and LDS, and
+// fewer rows write runs of qt shorter than a cache line.
 #include <float.h>
 #include <hip/hip_runtime.h>
 
@@ -271,7 +281,7 @@ __device__ __forceinline__ void emit(const NormArgs& a, const RowOut<In>& out, u
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = umax_u32(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-  amax = umax_u32(amax, m);
+  if (valid) amax = umax_u32(amax, m);
   if (a.quant == Q_NONE) return;
   float s = tscale;
   if (a.quant == Q_MX) {
@@ -355,24 +365,19 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
         h[j].load(x + k * 8, k < (uint32_t)chunks);
       }
     } else {
-      // at most 8 chunks of each at a time: 16 loads in flight in each lane
-      constexpr int PART = NCH < 8 ? NCH : 8;
+      Chunk<In> d[NCH];
 #pragma unroll
-      for (int j0 = 0; j0 < NCH; j0 += PART) {
-        Chunk<In> d[PART];
+      for (int j = 0; j < NCH; ++j) {
+        const uint32_t k = j * TPR + t;
+        h[j].load(x + k * 8, k < (uint32_t)chunks);
+        d[j].load(r + k * 8, k < (uint32_t)chunks);
+      }
 #pragma unroll
-        for (int j = 0; j < PART; ++j) {
-          const uint32_t k = (j0 + j) * TPR + t;
-          h[j0 + j].load(x + k * 8, k < (uint32_t)chunks);
-          d[j].load(r + k * 8, k < (uint32_t)chunks);
-        }
+      for (int j = 0; j < NCH; ++j) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < PART; ++j) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = h[j0 + j].at(i) + d[j].at(i);
-          h[j0 + j].set(v);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = h[j].at(i) + d[j].at(i);
+        h[j].set(v);
       }
     }
     float h1 = widen_here(x1);
@@ -487,14 +492,25 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
   }
 }
 
+// How a row is held, by its length [measured, us per call, MXFP8 row-wise with a
+// residual unless said otherwise]:
+//   16 lanes up to 263 columns      32768 x 128 10.2, a wave a row 23.6
+//   a wave up to 1031               32768 x 1024 42, a workgroup of 256 78
+//   256 threads up to 8199          32768 x 4096 150 (6.2 TB/s), a wave 187, 1024 threads 368
+//   512 threads up to 16391         8192 x 12288 133, 256 threads 139
+// and longer rows are read twice.  With at most one row a CU a row's own
+// latency is all, and 1024 threads take it (64 x 7168: 6.0, 256 threads 7.6;
+// at 512 x 4096 256 threads are ahead, 7.1 to 9.0).
+// An amax output ends in one atomic per workgroup on one address, which the
+// memory side performs one at a time, so its grid is persistent, with 1024
+// threads a workgroup up to 4103 columns (32768 x 512 with a given scale: 25.9,
+// 256 threads 32.2; 4096 x 8192: 49.7 and 47.3).
 template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
   const int tpr = chunks <= 32 ? 16 : chunks <= 128 ? 64 : chunks <= 1024 ? 256 : 512;  // threads a row
-  const bool wide = chunks > 256 && a.rows <= 256;  // at most a workgroup a CU: a row's own latency is all
-  // An amax output ends in one atomic per workgroup on one address, which the
-  // memory side performs one at a time: a persistent grid of large workgroups.
-  const bool large = a.amax_out && !wide && chunks <= (sizeof(In) == 2 ? 1024 : 512);
+  const bool wide = chunks > 256 && a.rows <= 256;
+  const bool large = a.amax_out && !wide && chunks <= 512;
   const int64_t rpw = wide || tpr == 512 ? 1 : (large ? 1024 : 256) / tpr;
   int64_t grid = (a.rows + rpw - 1) / rpw;
   const int64_t cap = !a.amax_out ? 1 << 20 : large ? 256 : 1024;
@@ -514,10 +530,8 @@ void launch_row(const NormArgs& a, hipStream_t st) {
   else if (wide && chunks <= 1024) QSG_ROW(1024, 1, 1024);
   else if (wide && chunks <= 2048) QSG_ROW(1024, 2, 1024);
   else if (chunks <= 512) QSG_ROWS(256, 2);
-  else if (chunks <= 1024) {
-    if constexpr (sizeof(In) == 2) QSG_ROWS(256, 4);
-    else QSG_ROW(256, 4, 256);
-  } else if (chunks <= 2048) QSG_ROW(512, 4, 512);
+  else if (chunks <= 1024) QSG_ROW(256, 4, 256);
+  else if (chunks <= 2048) QSG_ROW(512, 4, 512);
   else hipLaunchKernelGGL(norm_long_kernel<In>, g, dim3(256), 0, st, a);  // one row a workgroup, as counted above
 #undef QSG_ROWS
 #undef QSG_ROW
@@ -854,6 +868,9 @@ __device__ __forceinline__ float add_groups(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// [measured, us per call with dgamma] 16384 x 7168 with a residual gradient 165,
+// 8192 x 4096 without 45; the sum of the partials takes 4-5 of them.
+//
 // A group of TPR threads takes rows group, group + groups, ... and holds a
 // row in registers, NCH chunks per thread; its share of dgamma stays in
 // registers until the end.  WIDE: the rows' dots are read from a.dots, and
