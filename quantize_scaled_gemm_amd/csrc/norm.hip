@@ -615,21 +615,38 @@ struct ColArgs {
 
 constexpr int CT_COLS = 64;
 
+// max(|a|, |b|, |c|, |d|) of values that are not NaN (written out: the compiler
+// puts an instruction before each operand to quiet a NaN)
+__device__ __forceinline__ float max4_abs(float a, float b, float c, float d) {
+  float m;
+  asm("v_max3_f32 %0, |%1|, |%2|, |%3|" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+  asm("v_max_f32 %0, %1, |%2|" : "=v"(m) : "v"(m), "v"(d));
+  return m;
+}
+
 // A workgroup makes the column-wise copy of a 128 x 64 tile of y (and, with a
 // per-tensor scale, the row-wise one): thread t holds rows 4 (t / 8) .. + 3 of
 // chunk t % 8, so that a wave is 32 rows, the rows of an MXFP8 column block.
 //
 // A column's maximum: each lane's of its 4 rows go through LDS to the lane of
 // that column (64 columns, 64 lanes), which alone makes the scale; no barrier
-// where the block is the wave's.  Ordinary values skip what only the others
+// where the block is the wave's.  The largest |h rstd| is found first and
+// multiplied by |gamma| then: rounding keeps order.  Ordinary values skip what only the others
 // need (the wave decides): a row whose rstd is positive and finite has finite
 // h, so with finite weights y has no NaN; a block whose maximum is finite is
 // scaled to at most the format's maximum, up to a rounding that the encode
 // takes back, so nothing is clamped; and an MXFP8 scale (a power of two) is
 // put into the weight, which changes no bit of a code: with |gamma| <= 2^60
 // and a block maximum of 2^-50 at least, gamma 2^-e is neither too large nor
-// subnormal (|h rstd| <= sqrt(cols) <= 2^15), and an element of y that is
+// subnormal (|h rstd| <= sqrt(cols) <= 2^12), and an element of y that is
 // subnormal has the code of zero.
+//
+// What bounds it: the order of its accesses.  It reads 128-byte pieces of rows
+// and writes 128-byte pieces of columns; without its stores 32768 x 4096 takes
+// 52 us of 66, without its loads 56, and the vector instructions of the waves
+// are 47 % of the time.  Tried without gain: 256 or 512 rows a tile (81 and 87
+// us), 2-16 tiles a workgroup with the next one's loads in flight (66-76), a
+// tile order by XCD (the whole call 217 -> 221-225), 6-8 waves a SIMD.
 template <typename In, int QUANT>
 __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
   __shared__ uint32_t codes[CT_COLS * CT_STRIDE];
@@ -669,11 +686,11 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) nan |= !(fabsf(g[i]) <= 0x1p60f);
   const bool plain = __all(!nan && smallest > 0.0f && largest <= FLT_MAX);  // no NaN anywhere in the wave's y
-  float y[4][8];
+  float n[4][8];  // h rstd
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[j][i] = v[j].at(i) * rs[j] * g[i];
+    for (int i = 0; i < 8; ++i) n[j][i] = v[j].at(i) * rs[j];
 
   uint32_t cq[8];  // column i: the codes of rows r .. r + 3
   if constexpr (QUANT == Q_TENSOR) {
@@ -690,7 +707,10 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
     u32x2 rq[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      rq[j] = a.fmt == kE4M3 ? enc8<kE4M3>(y[j], s) : enc8<kE5M2>(y[j], s);
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = n[j][i] * g[i];
+      rq[j] = a.fmt == kE4M3 ? enc8<kE4M3>(y, s) : enc8<kE5M2>(y, s);
       if (a.q) {
         uint8_t* p = a.q + (r + j) * a.cols + c;
         if (full) {
@@ -713,15 +733,16 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
   } else {
     uint32_t cm[8];
     if (plain) {
+      // rounding keeps order: the largest product is the product of the largest
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        cm[i] = __float_as_uint(fmaxf(fmaxf(fabsf(y[0][i]), fabsf(y[1][i])), fmaxf(fabsf(y[2][i]), fabsf(y[3][i]))));
+        cm[i] = __float_as_uint(max4_abs(n[0][i], n[1][i], n[2][i], n[3][i]) * fabsf(g[i]));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         cm[i] = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) cm[i] = umax_u32(cm[i], abs_bits_canon(__float_as_uint(y[j][i])));
+        for (int j = 0; j < 4; ++j) cm[i] = umax_u32(cm[i], abs_bits_canon(__float_as_uint(n[j][i] * g[i])));
       }
     }
     *reinterpret_cast<u32x4*>(&lane_max[wave][ty & 7][tx * 8]) = u32x4{cm[0], cm[1], cm[2], cm[3]};
@@ -753,22 +774,21 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = cscale[wave][tx * 8 + i];
     if (easy) {
-      if constexpr (QUANT == Q_MX) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] *= g[i];
-      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float z[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = (QUANT == Q_MX ? v[j].at(i) * rs[j] : y[j][i]) * cs[i];
+        for (int j = 0; j < 4; ++j) z[j] = QUANT == Q_MX ? n[j][i] * (g[i] * cs[i]) : n[j][i] * g[i] * cs[i];
         cq[i] = a.fmt == kE4M3 ? enc4_inrange<kE4M3>(z[0], z[1], z[2], z[3]) : enc4_inrange<kE5M2>(z[0], z[1], z[2], z[3]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        cq[i] = a.fmt == kE4M3 ? enc4<kE4M3>(y[0][i] * cs[i], y[1][i] * cs[i], y[2][i] * cs[i], y[3][i] * cs[i])
-                               : enc4<kE5M2>(y[0][i] * cs[i], y[1][i] * cs[i], y[2][i] * cs[i], y[3][i] * cs[i]);
+      for (int i = 0; i < 8; ++i) {
+        float z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = n[j][i] * g[i] * cs[i];
+        cq[i] = a.fmt == kE4M3 ? enc4<kE4M3>(z[0], z[1], z[2], z[3]) : enc4<kE5M2>(z[0], z[1], z[2], z[3]);
+      }
     }
   }
 #pragma unroll
