@@ -317,6 +317,18 @@ __device__ __forceinline__ void emit1(const NormArgs& a, const RowOut<In>& out, 
   out.q[c] = (uint8_t)(a.fmt == kE4M3 ? enc4<kE4M3>(v, 0, 0, 0) : enc4<kE5M2>(v, 0, 0, 0));
 }
 
+// The maximum of a launch of one workgroup, stored: nothing is cleared before.
+template <int NTHREADS>
+__device__ __forceinline__ void block_max_alone(uint32_t m, uint32_t* out, uint32_t* lds) {
+  m = wave_max_u32(m);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < NTHREADS / 64; ++i) m = umax_u32(m, lds[i]);
+    *out = m > 0x7F800000u ? 0x7FC00000u : m;
+  }
+}
+
 __device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)cols) + eps));
 }
@@ -426,7 +438,10 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
   }
   if (a.amax_out) {
     __shared__ uint32_t ured[16];
-    block_max_to_global<BLK>(amax, a.amax_out, ured);
+    if (gridDim.x == 1)
+      block_max_alone<BLK>(amax, a.amax_out, ured);
+    else
+      block_max_to_global<BLK>(amax, a.amax_out, ured);
   }
 }
 
@@ -488,7 +503,10 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
   }
   if (a.amax_out) {
     __shared__ uint32_t ured[4];
-    block_max_to_global<256>(amax, a.amax_out, ured);
+    if (gridDim.x == 1)
+      block_max_alone<256>(amax, a.amax_out, ured);
+    else
+      block_max_to_global<256>(amax, a.amax_out, ured);
   }
 }
 
@@ -504,18 +522,20 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
 // An amax output ends in one atomic per workgroup on one address, which the
 // memory side performs one at a time, so its grid is persistent, with 1024
 // threads a workgroup up to 4103 columns (32768 x 512 with a given scale: 25.9,
-// 256 threads 32.2; 4096 x 8192: 49.7 and 47.3).
+// 256 threads 32.2; 4096 x 8192: 49.7 and 47.3); a single workgroup needs no
+// launch that clears it first.
 template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
   const int tpr = chunks <= 32 ? 16 : chunks <= 128 ? 64 : chunks <= 1024 ? 256 : 512;  // threads a row
-  const bool wide = chunks > 256 && a.rows <= 256;
+  const bool wide = chunks > 256 && a.rows <= 256 && !(a.amax_out && chunks <= 512 && a.rows <= 4);
   const bool large = a.amax_out && !wide && chunks <= 512;
   const int64_t rpw = wide || tpr == 512 ? 1 : (large ? 1024 : 256) / tpr;
   int64_t grid = (a.rows + rpw - 1) / rpw;
   const int64_t cap = !a.amax_out ? 1 << 20 : large ? 256 : 1024;
   if (grid > cap) grid = cap;
   const dim3 g((unsigned)grid);
+  if (a.amax_out && grid > 1) launch_fill_u32(a.amax_out, 0u, 1, st);  // one workgroup stores its maximum
 #define QSG_ROW(TPR, NCH, BLK) hipLaunchKernelGGL((norm_row_kernel<In, TPR, NCH, BLK>), g, dim3(BLK), 0, st, a)
 #define QSG_ROWS(TPR, NCH)             \
   do {                                 \
@@ -659,7 +679,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
   const int64_t tile = a.tiles - 1 - (a.tile0 + blockIdx.x);
   const int64_t r0 = tile_start(tile / a.tiles_c, CT_ROWS, a.rows), c0 = tile_start(tile % a.tiles_c, CT_COLS, a.cols);
   const int64_t r = r0 + ty * 4, c = c0 + tx * 8;
-  const bool full = a.rows >= CT_ROWS && a.cols >= CT_COLS;
+  const bool whole = a.cols >= CT_COLS, full = whole && a.rows >= CT_ROWS;  // no edge in the columns; none at all
   const In* h = reinterpret_cast<const In*>(a.h);
   Chunk<In> v[4];
   float rs[4], g[8];
@@ -668,16 +688,28 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
     for (int j = 0; j < 4; ++j) v[j].load(h + (r + j) * a.ld + c, true);
 #pragma unroll
     for (int j = 0; j < 4; ++j) rs[j] = a.rstd[r + j];
-    load_gamma(g, a.gamma, a.gamma_bf16, c, true);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = r + j < a.rows && c + i < a.cols ? load1(h + (r + j) * a.ld + c + i) : 0.0f;
-      v[j].set(e);
-      rs[j] = r + j < a.rows ? a.rstd[r + j] : 1.0f;
+      rs[j] = 1.0f;
+      if (r + j < a.rows) rs[j] = a.rstd[r + j];
     }
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j].load(h + (r + j) * a.ld + c, r + j < a.rows);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = r + j < a.rows && c + i < a.cols ? load1(h + (r + j) * a.ld + c + i) : 0.0f;
+        v[j].set(e);
+      }
+    }
+  }
+  if (whole) {
+    load_gamma(g, a.gamma, a.gamma_bf16, c, true);
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = c + i < a.cols ? load_gamma1(a.gamma, a.gamma_bf16, c + i) : 0.0f;
   }
@@ -713,8 +745,8 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
       rq[j] = a.fmt == kE4M3 ? enc8<kE4M3>(y, s) : enc8<kE5M2>(y, s);
       if (a.q) {
         uint8_t* p = a.q + (r + j) * a.cols + c;
-        if (full) {
-          put8<false>(p, rq[j]);  // half a line: the next tile completes it in L2
+        if (whole) {
+          if (r + j < a.rows) put8<false>(p, rq[j]);  // half a line: the next tile completes it in L2
         } else if (r + j < a.rows) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -822,9 +854,12 @@ __global__ __launch_bounds__(256) void transpose_bytes_kernel(const uint8_t* q, 
   const int64_t r0 = tile_start(tile / tiles_c, CT_ROWS, rows), c0 = tile_start(tile % tiles_c, TT_COLS, cols);
   const int64_t r = r0 + ty * 4, c = c0 + tx * 16;
   u32x4 v[4];
-  if (rows >= CT_ROWS && cols >= TT_COLS) {
+  if (cols >= TT_COLS) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_b*>(q + (r + j) * cols + c));
+    for (int j = 0; j < 4; ++j) {
+      v[j] = u32x4{0, 0, 0, 0};
+      if (r + j < rows) v[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_b*>(q + (r + j) * cols + c));
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -1173,8 +1208,8 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
   const bool tensorwise = scaling == 0;
   float* three = reinterpret_cast<float*>(s);
   float* amax = tensorwise ? three : amax_out;
-  if (amax) launch_fill_u32(reinterpret_cast<uint32_t*>(amax), 0u, 1, st);
   if (rows == 0 || cols == 0) {
+    if (amax) launch_fill_u32(reinterpret_cast<uint32_t*>(amax), 0u, 1, st);
     if (tensorwise) launch_compute_scale(three, fmt, margin, three + 1, three + 2, st);
     return;
   }
