@@ -320,15 +320,24 @@ __device__ __forceinline__ void emit1(const NormArgs& a, const RowOut<In>& out, 
   out.q[c] = (uint8_t)(a.fmt == kE4M3 ? enc4<kE4M3>(v, 0, 0, 0) : enc4<kE5M2>(v, 0, 0, 0));
 }
 
-// The maximum of a launch of one workgroup, stored: nothing is cleared before.
+// The launch's maximum: stored by a launch's only workgroup (nothing is
+// cleared before); by one atomic of each of up to 256, which wait for nothing;
+// of more only by those that read a smaller one there, since all of this is
+// done one at a time on the memory side (1021 x 4096, 256 workgroups: 12.4 us a
+// call, with a read first 14.4; 4096 x 8192, 1024 workgroups: 49.1 and 48.1).
 template <int NTHREADS>
-__device__ __forceinline__ void block_max_alone(uint32_t m, uint32_t* out, uint32_t* lds) {
+__device__ __forceinline__ void finish_amax(uint32_t m, uint32_t* out, uint32_t* lds) {
+  if (gridDim.x > 256) return block_max_to_global<NTHREADS>(m, out, lds);
   m = wave_max_u32(m);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < NTHREADS / 64; ++i) m = umax_u32(m, lds[i]);
-    *out = m > 0x7F800000u ? 0x7FC00000u : m;
+    if (m > 0x7F800000u) m = 0x7FC00000u;
+    if (gridDim.x == 1)
+      *out = m;
+    else
+      atomicMax(out, m);
   }
 }
 
@@ -441,10 +450,7 @@ __global__ __launch_bounds__(BLK) void norm_row_kernel(NormArgs a) {
   }
   if (a.amax_out) {
     __shared__ uint32_t ured[16];
-    if (gridDim.x == 1)
-      block_max_alone<BLK>(amax, a.amax_out, ured);
-    else
-      block_max_to_global<BLK>(amax, a.amax_out, ured);
+    finish_amax<BLK>(amax, a.amax_out, ured);
   }
 }
 
@@ -506,10 +512,7 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
   }
   if (a.amax_out) {
     __shared__ uint32_t ured[4];
-    if (gridDim.x == 1)
-      block_max_alone<256>(amax, a.amax_out, ured);
-    else
-      block_max_to_global<256>(amax, a.amax_out, ured);
+    finish_amax<256>(amax, a.amax_out, ured);
   }
 }
 
