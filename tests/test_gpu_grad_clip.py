@@ -148,6 +148,18 @@ def test_ranks_add_their_sums(q):
     assert (np.abs(to_np(b) - want[1]) <= np.abs(want[1]) * (2.0 ** -8 + 5 * U)).all()
 
 
+def test_a_tensor_of_more_than_2_31_elements(q):
+    import torch
+
+    n = (1 << 31) + 5
+    t = torch.full((n,), 2.0, dtype=torch.bfloat16, device="cuda")
+    s, norm = call(q, q.qsg_grad_plan([t]), 2.0 ** 9)
+    assert s == 4.0 * n and norm == np.float32(math.sqrt(4.0 * n))
+    k = np.float32(512.0) / (np.float32(norm) + np.float32(1e-6))
+    want = torch.tensor(2.0 * float(k)).to(torch.bfloat16)
+    assert t[0].item() == want.item() and torch.equal(t[-9:].cpu(), want.expand(9)) and t.min() == t.max()
+
+
 def test_same_bits_twice(q):
     rng = np.random.default_rng(6)
     grads = [tensor(rng, n, "bf16")[0] for n in (300000, 5, 1234567)]

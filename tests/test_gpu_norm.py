@@ -318,6 +318,42 @@ def test_forward_offsets_past_32_bits(q):
     close_dx(dx, to_np(x), to_np(x), np.ones(3), np.ones(cols), None, "bf16")
 
 
+def test_more_than_2_32_elements(q):
+    """Dense outputs past 2^32 bytes and elements: the last rows of a large call
+    are those of a call on them alone."""
+    import torch
+
+    rows, cols, tail = (1 << 21) + 128, 2080, 512
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    for part in x.split(1 << 18):
+        part.normal_(generator=g)
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+
+    def call(x):
+        r = x.shape[0]
+        u8 = dict(dtype=torch.uint8, device="cuda")
+        o = dict(rstd=torch.empty(r, device="cuda"), q=torch.empty((r, cols), **u8), s=torch.empty((r, cols // 32), **u8),
+                 qt=torch.empty((cols, r), **u8), st=torch.empty((cols, r // 32), **u8))
+        q.qsg_rmsnorm_quantize(x, w, EPS, q.MXFP8, **o)
+        return o
+
+    big, small = call(x), call(x[-tail:])
+    for name in ("rstd", "q", "s"):
+        assert torch.equal(big[name][-tail:], small[name]), name
+    assert torch.equal(big["qt"][:, -tail:], small["qt"]) and torch.equal(big["st"][:, -tail // 32:], small["st"])
+    # the byte transpose, and the backward pass in place of dy
+    scale = torch.full((1,), 30.0, device="cuda")
+    q.qsg_rmsnorm_quantize(x, w, EPS, q.DELAYED, rstd=big["rstd"], q=big["q"], qt=big["qt"], scale=scale)
+    assert torch.equal(big["q"][-tail:].t(), big["qt"][:, -tail:])
+    h, dy = x[-tail:].clone(), x[-tail:].clone()
+    ws = torch.empty(q.qsg_rmsnorm_bwd_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    q.qsg_rmsnorm_bwd(dy, h, w, small["rstd"], dy, workspace=ws)
+    out = torch.empty_like(x)
+    q.qsg_rmsnorm_bwd(x, x, w, big["rstd"], out, workspace=ws)
+    assert torch.equal(out[-tail:], dy)
+
+
 # ---------------------------------------------------------------------------
 # backward
 # ---------------------------------------------------------------------------
