@@ -321,13 +321,13 @@ __device__ __forceinline__ void emit1(const NormArgs& a, const RowOut<In>& out, 
 }
 
 // The launch's maximum: stored by a launch's only workgroup (nothing is
-// cleared before); by one atomic of each of up to 256, which wait for nothing;
+// cleared before); by one atomic of each of up to 512, which wait for nothing;
 // of more only by those that read a smaller one there, since all of this is
 // done one at a time on the memory side (1021 x 4096, 256 workgroups: 12.4 us a
 // call, with a read first 14.4; 4096 x 8192, 1024 workgroups: 49.1 and 48.1).
 template <int NTHREADS>
 __device__ __forceinline__ void finish_amax(uint32_t m, uint32_t* out, uint32_t* lds) {
-  if (gridDim.x > 256) return block_max_to_global<NTHREADS>(m, out, lds);
+  if (gridDim.x > 512) return block_max_to_global<NTHREADS>(m, out, lds);
   m = wave_max_u32(m);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
   __syncthreads();
@@ -528,33 +528,38 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormArgs a) {
 // An amax output ends in one atomic per workgroup on one address, which the
 // memory side performs one at a time, so its grid is persistent, with 1024
 // threads a workgroup up to 4103 columns (32768 x 512 with a given scale: 25.9,
-// 256 threads 32.2; 4096 x 8192: 49.7 and 47.3); a single workgroup needs no
-// launch that clears it first.
+// 256 threads 32.2; 4096 x 8192: 49.7 and 47.3), or twice as many of 512 where
+// many long rows keep both busy (16384 x 4096 with both copies: 104, 1024
+// threads 109; 1021 x 4096: 14.5 and 12.4); a single workgroup needs no launch
+// that clears it first.
 template <typename In>
 void launch_row(const NormArgs& a, hipStream_t st) {
   const int64_t chunks = a.cols / 8;
   const int tpr = chunks <= 32 ? 16 : chunks <= 128 ? 64 : chunks <= 1024 ? 256 : 512;  // threads a row
   const bool wide = chunks > 256 && a.rows <= 256 && !(a.amax_out && chunks <= 512 && a.rows <= 4);
   const bool large = a.amax_out && !wide && chunks <= 512;
-  const int64_t rpw = wide || tpr == 512 ? 1 : (large ? 1024 : 256) / tpr;
+  const int blk = !large ? 256 : tpr == 256 && a.rows > 2048 ? 512 : 1024;
+  const int64_t rpw = wide || tpr == 512 ? 1 : blk / tpr;
   int64_t grid = (a.rows + rpw - 1) / rpw;
-  const int64_t cap = !a.amax_out ? 1 << 20 : large ? 256 : 1024;
+  const int64_t cap = !a.amax_out ? 1 << 20 : !large ? 1024 : blk == 512 ? 512 : 256;
   if (grid > cap) grid = cap;
   const dim3 g((unsigned)grid);
   if (a.amax_out && grid > 1) launch_fill_u32(a.amax_out, 0u, 1, st);  // one workgroup stores its maximum
 #define QSG_ROW(TPR, NCH, BLK) hipLaunchKernelGGL((norm_row_kernel<In, TPR, NCH, BLK>), g, dim3(BLK), 0, st, a)
-#define QSG_ROWS(TPR, NCH)             \
-  do {                                 \
-    if (large) QSG_ROW(TPR, NCH, 1024); \
-    else QSG_ROW(TPR, NCH, 256);       \
+#define QSG_ROWS(TPR, NCH)                   \
+  do {                                       \
+    if (blk == 1024) QSG_ROW(TPR, NCH, 1024); \
+    else QSG_ROW(TPR, NCH, 256);             \
   } while (0)
   if (chunks <= 16) QSG_ROWS(16, 1);
   else if (chunks <= 32) QSG_ROWS(16, 2);
   else if (chunks <= 64) QSG_ROWS(64, 1);
   else if (chunks <= 128) QSG_ROWS(64, 2);
+  else if (chunks <= 256 && blk == 512) QSG_ROW(256, 1, 512);
   else if (chunks <= 256) QSG_ROWS(256, 1);
   else if (wide && chunks <= 1024) QSG_ROW(1024, 1, 1024);
   else if (wide && chunks <= 2048) QSG_ROW(1024, 2, 1024);
+  else if (chunks <= 512 && blk == 512) QSG_ROW(256, 2, 512);
   else if (chunks <= 512) QSG_ROWS(256, 2);
   else if (chunks <= 1024) QSG_ROW(256, 4, 256);
   else if (chunks <= 2048) QSG_ROW(512, 4, 512);

@@ -177,7 +177,7 @@ def test_forward(q, dtype, recipe, rows, cols, t):
 
 @pytest.mark.parametrize("dtype, rows, cols", [
     ("bf16", 1500, 520), ("bf16", 1100, 1040), ("bf16", 1030, 2056), ("bf16", 1027, 4104), ("bf16", 2100, 264),
-    ("bf16", 1025, 8199), ("f32", 1030, 2056), ("f32", 1100, 520), ("bf16", 100, 520), ("bf16", 100, 2056),
+    ("bf16", 1025, 8199), ("bf16", 2100, 1040), ("bf16", 2051, 4103), ("f32", 2049, 1111), ("f32", 1030, 2056), ("f32", 1100, 520), ("bf16", 100, 520), ("bf16", 100, 2056),
     ("bf16", 40, 4104), ("bf16", 30, 8200), ("f32", 30, 4104), ("f32", 20, 8200)])
 def test_forward_row_variants(q, dtype, rows, cols):
     """Every way that a row is held: a wave or a workgroup, 1 to 16 chunks a
@@ -408,7 +408,8 @@ def backward(q, rng, rows, cols, dtype, dres=True, dgamma=True, accumulate=False
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows, cols", [
     (1, 1), (1, 8), (3, 7), (5, 64), (130, 500), (1300, 519), (7, 520), (64, 2048), (33, 2055), (40, 4096), (9, 4103),
-    (20, 8192), (6, 8195), (5, 16384), (4, 16391), (3, 16392), (2, 20005), (2500, 264), (1100, 1040)])
+    (20, 8192), (6, 8195), (5, 16384), (4, 16391), (3, 16392), (2, 20005), (2500, 264), (1100, 1040),
+    (400, 3001), (1290, 2600)])
 def test_backward(q, dtype, rows, cols):
     rng = np.random.default_rng([rows, cols])
     backward(q, rng, rows, cols, dtype)
