@@ -935,7 +935,7 @@ __device__ __forceinline__ float add_groups(float v) {
 }
 
 // [measured, us per call with dgamma] 16384 x 7168 with a residual gradient 165,
-// 8192 x 4096 without 45; the sum of the partials takes 4-5 of them.
+// 8192 x 4096 without 41; the sum of the partials takes 4-5 of them.
 //
 // A group of TPR threads takes rows group, group + groups, ... and holds a
 // row in registers, NCH chunks per thread; its share of dgamma stays in
@@ -1170,14 +1170,24 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   p.blk = p.tpr == 1024 ? 1024 : 256;
   // about as many workgroups as the card holds at once
   int64_t most = chunks <= 32 ? 512 : chunks <= 512 ? 1024 : chunks <= 1024 ? 512 : chunks <= 2048 ? 256 : 128;
-  // Four rows to a workgroup, which adds their shares of dgamma in LDS: less
-  // to write and read again, for a barrier that four rows share.  [measured,
-  // joined against separate, us] 1024 x 4096 14.6 / 18.8, 1024 x 1024 9.5 /
-  // 11.5, 32768 x 4096 184 / 202; but 256 x 1024 8.3 / 7.5, 8192 x 1024
-  // 24.9 / 22.5, 4096 x 2048 23.0 / 21.2.
-  if (p.tpr == 256 && chunks <= 512 && rows >= 384 && (rows <= 1280 || chunks > 320)) {
-    p.blk = 1024;
-    most = 512;
+  // Two or four rows to a workgroup, which adds their shares of dgamma in LDS:
+  // less to write and read again, for a barrier that the rows share.
+  // [measured, us per call, one / two / four rows] 1024 x 4096 18.8 / 15.3 /
+  // 14.7, 1024 x 1024 11.5 / 9.6 / 9.2, 8192 x 4096 58.6 / 52.6 / 56.5 (without
+  // a residual gradient 43.8 / 41.1 / 46.9), 2048 x 2048 15.6 / 14.6 / 16.8, but
+  // 256 x 1024 7.5 / - / 8.3 and 32768 x 1024 57.8 / 60.6 / 69; 512 x 7168
+  // 17.2 / 15.7, 8192 x 7168 88 / 92.
+  if (p.tpr == 256 && rows >= 384) {
+    if (chunks <= 512 && rows <= 1280) {
+      p.blk = 1024;
+      most = 512;
+    } else if (chunks <= 512 && (chunks > 160 || rows <= 16384)) {
+      p.blk = 512;
+      most = 512;
+    } else if (chunks > 512 && chunks <= 1024 && rows <= 1280) {
+      p.blk = 512;
+      most = 256;
+    }
   }
   const int64_t rpw = p.blk / p.tpr;
   p.grid = (rows + rpw - 1) / rpw;
@@ -1195,9 +1205,12 @@ void launch_bwd(const NormBwdArgs& a, const BwdPlan& p, hipStream_t st) {
   else if (chunks <= 32) QSG_BWD(16, 2, 256);
   else if (chunks <= 64) QSG_BWD(64, 1, 256);
   else if (chunks <= 256 && p.blk == 1024) QSG_BWD(256, 1, 1024);
+  else if (chunks <= 256 && p.blk == 512) QSG_BWD(256, 1, 512);
   else if (chunks <= 256) QSG_BWD(256, 1, 256);
   else if (chunks <= 512 && p.blk == 1024) QSG_BWD(256, 2, 1024);
+  else if (chunks <= 512 && p.blk == 512) QSG_BWD(256, 2, 512);
   else if (chunks <= 512) QSG_BWD(256, 2, 256);
+  else if (chunks <= 1024 && p.blk == 512) QSG_BWD(256, 4, 512);
   else if (chunks <= 1024) QSG_BWD(256, 4, 256);
   else if (chunks <= 2048) QSG_BWD(1024, 2, 1024);
   else {

@@ -409,7 +409,7 @@ def backward(q, rng, rows, cols, dtype, dres=True, dgamma=True, accumulate=False
 @pytest.mark.parametrize("rows, cols", [
     (1, 1), (1, 8), (3, 7), (5, 64), (130, 500), (1300, 519), (7, 520), (64, 2048), (33, 2055), (40, 4096), (9, 4103),
     (20, 8192), (6, 8195), (5, 16384), (4, 16391), (3, 16392), (2, 20005), (2500, 264), (1100, 1040),
-    (400, 3001), (1290, 2600)])
+    (400, 3001), (1290, 2600), (1301, 1100), (1311, 4100), (390, 5003)])
 def test_backward(q, dtype, rows, cols):
     rng = np.random.default_rng([rows, cols])
     backward(q, rng, rows, cols, dtype)
