@@ -25,8 +25,10 @@
 // 66 us), the backward kernel 5.8 (16384 x 7168 with a residual gradient: 940
 // MB in 160 us).  One launch that kept 128 rows of h on the chip for both
 // copies would save the second reading of h (2 of 10 bytes an element), but
-// 128 rows of 4096 columns are 1 MB, twice a CU's registers and LDS, and
-// fewer rows write runs of qt shorter than a cache line.
+// 128 rows of 4096 columns are 1 MB, twice a CU's registers and LDS.  32 rows
+// fit, and write qt in runs of 32 bytes: a kernel that only moved those bytes
+// (32768 x 4096, neighbouring rows on one XCD, no arithmetic) took 206 us, the
+// two passes with all of theirs 209.
 #include <float.h>
 #include <hip/hip_runtime.h>
 
