@@ -457,16 +457,21 @@ def qsg_gemm_nvfp4(a, sa, ts_a, b, sb, ts_b, c, stream=None):
 # The calls below take many tensors and are made for single tokens too, so
 # each tensor is asked for as little as accepts it; what is not accepted goes
 # to the checks above for the words of its refusal.
-_CODES = {}  # torch dtype -> (code of the ABI or None, name); filled on first use
+_FLOATS = {}  # torch dtype -> (code of the ABI, name); both filled on first use
+_NAMES = {}   # torch dtype -> name of any type that a buffer may have
 
 
-def _codes():
-    if not _CODES:
+def _float_code(t):
+    """(code, name) of a float type of the ABI."""
+    e = _FLOATS.get(t.dtype)
+    if e is None:
+        _dtype_code(t)  # refuses other types
         import torch
 
-        _CODES.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32"), torch.uint8: (None, "u8"),
-                       torch.float64: (None, "f64")})
-    return _CODES
+        _FLOATS.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32")})
+        _NAMES.update({torch.bfloat16: "bf16", torch.float32: "f32", torch.uint8: "u8", torch.float64: "f64"})
+        e = _FLOATS[t.dtype]
+    return e
 
 
 def _rows(t, name):
@@ -496,22 +501,13 @@ def _same_matrix(t, name, shape, dtype):
     return p, ld
 
 
-def _dense(t, name, numel, dtype, required=False):
-    """Pointer of a buffer that _buffer accepts."""
-    if t is None and not required or isinstance(t, int):
+def _dense(t, name, numel, dtype):
+    """Pointer of a required buffer that _buffer accepts."""
+    if isinstance(t, int):
         return t
-    if t is None or _codes().get(t.dtype, (None, None))[1] != dtype or t.numel() != numel or not (
-            t.is_contiguous() and t.is_cuda):
+    if t is None or _NAMES.get(t.dtype) != dtype or t.numel() != numel or not (t.is_contiguous() and t.is_cuda):
         _buffer(t, name, numel, dtype)
     return t.data_ptr()
-
-
-def _float_code(t):
-    """(code, name) of a float type of the ABI."""
-    e = _codes().get(t.dtype)
-    if e is None or e[0] is None:
-        raise QsgError(f"unsupported input dtype {t.dtype}")
-    return e
 
 
 def _workspace(t, nbytes):
@@ -535,28 +531,30 @@ def qsg_rmsnorm_quantize(x, gamma, eps, scaling=None, fmt=E4M3, residual=None, h
     px, rows, cols, ld = _rows(x, "x")
     dt, dname = _float_code(x)
     gt, gname = _float_code(gamma)
-    numel, like = rows * cols, (x.shape, x.dtype)
-    pr, ldr = _same_matrix(residual, "residual", *like)
-    ph, ldh = _same_matrix(h, "h", *like)
+    numel, shape, dtype = rows * cols, x.shape, x.dtype
+    pr, ldr = _same_matrix(residual, "residual", shape, dtype)
+    ph, ldh = _same_matrix(h, "h", shape, dtype)
     pg = _dense(gamma, "gamma", cols, gname)
-    prstd = _dense(rstd, "rstd", rows, "f32")
-    py = _dense(y, "y", numel, dname)
-    pq, pqt = _dense(q, "q", numel, "u8"), _dense(qt, "qt", numel, "u8")
-    pa = _dense(amax_out, "amax_out", 1, "f32")
-    psc = ps = pst = None
-    if scaling == DELAYED:
-        psc = _dense(scale, "scale", 1, "f32", True)
-    elif scaling == TENSORWISE:
-        ps = _dense(s, "s", 3, "f32", True)
-    elif scaling in (MXFP8, BLOCK_1X128):
-        # a shape that breaks the block rule has no layout, and the library refuses it
-        if q is not None:
-            row = _scale_layout(scaling, rows, cols)
-            ps = _dense(s, "s", row[0], row[1], True) if row else _ptr(s)
-        if qt is not None:
-            col = _scale_layout(scaling, cols, rows)
-            pst = _dense(st, "st", col[0], col[1], True) if col else _ptr(st)
-    rec = None if scaling is None else Recipe(scaling, fmt, margin, mx_rule)
+    prstd = None if rstd is None else _dense(rstd, "rstd", rows, "f32")
+    py = None if y is None else _dense(y, "y", numel, dname)
+    pq = None if q is None else _dense(q, "q", numel, "u8")
+    pqt = None if qt is None else _dense(qt, "qt", numel, "u8")
+    pa = None if amax_out is None else _dense(amax_out, "amax_out", 1, "f32")
+    psc = ps = pst = rec = None
+    if scaling is not None:
+        rec = Recipe(scaling, fmt, margin, mx_rule)
+        if scaling == DELAYED:
+            psc = _dense(scale, "scale", 1, "f32")
+        elif scaling == TENSORWISE:
+            ps = _dense(s, "s", 3, "f32")
+        elif scaling == MXFP8 or scaling == BLOCK_1X128:
+            # a shape that breaks the block rule has no layout, and the library refuses it
+            if q is not None:
+                row = _scale_layout(scaling, rows, cols)
+                ps = _dense(s, "s", row[0], row[1]) if row else _ptr(s)
+            if qt is not None:
+                col = _scale_layout(scaling, cols, rows)
+                pst = _dense(st, "st", col[0], col[1]) if col else _ptr(st)
     _check(load_library().qsg_rmsnorm_quantize(px, pr, dt, rows, cols, ld, ldr, pg, gt, eps, rec, psc, ph, ldh, prstd,
                                                py, pq, ps, pqt, pst, pa, _stream(stream)))
 
@@ -576,13 +574,13 @@ def qsg_rmsnorm_bwd(dy, h, gamma, rstd, dx, dres=None, dgamma=None, accumulate=F
     pdy, rows, cols, lddy = _rows(dy, "dy")
     dt = _float_code(dy)[0]
     gt, gname = _float_code(gamma)
-    like = (dy.shape, dy.dtype)
-    ph, ldh = _same_matrix(h, "h", *like)
-    pdx, lddx = _same_matrix(dx, "dx", *like)
-    pdr, lddres = _same_matrix(dres, "dres", *like)
+    shape, dtype = dy.shape, dy.dtype
+    ph, ldh = _same_matrix(h, "h", shape, dtype)
+    pdx, lddx = _same_matrix(dx, "dx", shape, dtype)
+    pdr, lddres = _same_matrix(dres, "dres", shape, dtype)
     pg = _dense(gamma, "gamma", cols, gname)
-    prstd = _dense(rstd, "rstd", rows, "f32", True)
-    pdg = _dense(dgamma, "dgamma", cols, "f32")
+    prstd = _dense(rstd, "rstd", rows, "f32")
+    pdg = None if dgamma is None else _dense(dgamma, "dgamma", cols, "f32")
     pw = _workspace(workspace, qsg_rmsnorm_bwd_workspace(rows, cols))
     _check(load_library().qsg_rmsnorm_bwd(pdy, ph, pdr, dt, rows, cols, lddy, ldh, lddres, pg, gt, prstd, pdx, lddx,
                                           pdg, 1 if accumulate else 0, pw, _stream(stream)))
@@ -635,12 +633,13 @@ def qsg_grad_plan(grads, outs=None):
 def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
     """sumsq (1 fp64 on the GPU) = sum of the squares of the plan's gradients.
     workspace: GRAD_WORKSPACE_BYTES bytes on the GPU."""
-    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64", True),
+    _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
                                          _workspace(workspace, GRAD_WORKSPACE_BYTES), _stream(stream)))
 
 
 def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
     """The plan's outputs = gradients * min(1, max_norm / (norm + 1e-6)) with
     norm = sqrt(sumsq), written to norm_out (1 fp32) if given."""
-    _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64", True),
-                                        max_norm, _dense(norm_out, "norm_out", 1, "f32"), _stream(stream)))
+    _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
+                                        max_norm, None if norm_out is None else _dense(norm_out, "norm_out", 1, "f32"),
+                                        _stream(stream)))
