@@ -428,8 +428,9 @@ int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t
                          const float* scale_dev, void* h, int64_t ldh, float* rstd, void* y, uint8_t* q, void* s,
                          uint8_t* qt, void* st, float* amax_out_dev, void* stream);
 
-/* Bytes of the workspace that qsg_rmsnorm_bwd needs for this shape (0 for an
- * empty one), or a negative qsg_status. */
+/* Bytes of the workspace that qsg_rmsnorm_bwd needs for this shape and for
+ * every shape with no more rows and no more columns (0 for an empty one), or a
+ * negative qsg_status. */
 int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
 
 /* Backward of qsg_rmsnorm_quantize, through y (the quantization passes the

@@ -1165,6 +1165,7 @@ struct BwdPlan {
   int64_t grid, partials;
 };
 
+// The last shapes of each kind stand in rmsnorm_bwd_workspace too.
 BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   const int64_t chunks = cols / 8;
   BwdPlan p;
@@ -1285,9 +1286,24 @@ void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t ro
     launch_col<float>(k, st);
 }
 
+// A workspace serves every shape with no more rows and no more columns, while a
+// plan may leave fewer partials of a larger shape (rows joined, fewer groups of
+// longer rows): the most that any such shape needs.  The need grows within each
+// kind of plan, so its value at the kinds' last shapes and at this one is all.
 int64_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows == 0 || cols == 0) return 0;
-  return (bwd_plan(rows, cols).partials * cols + (cols > kBwdMostCols ? rows : 0)) * 4;
+  const int64_t row_ends[] = {383, 1280, 16384, rows};
+  const int64_t col_ends[] = {263, 519, 1287, 4103, 8199, kBwdMostCols, cols};
+  int64_t most = 0;
+  for (const int64_t c : col_ends) {
+    if (c > cols) continue;
+    for (const int64_t r : row_ends) {
+      if (r > rows) continue;
+      const int64_t need = bwd_plan(r, c).partials * c + (c > kBwdMostCols ? r : 0);
+      if (need > most) most = need;
+    }
+  }
+  return most * 4;
 }
 
 void launch_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
