@@ -425,6 +425,7 @@ int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t
 int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0)
     return fail(QSG_ERR_ARG, "qsg_rmsnorm_bwd_workspace: negative shape %lld x %lld", (long long)rows, (long long)cols);
+  if (cols > kMostNormCols) return fail(QSG_ERR_UNSUPPORTED, "qsg_rmsnorm_bwd_workspace: more than 2^24 cols");
   return qsg::rmsnorm_bwd_workspace(rows, cols);
 }
 

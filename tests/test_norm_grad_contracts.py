@@ -30,3 +30,11 @@ def test_a_workspace_serves_smaller_shapes(lib):
                 assert need[r, c] >= need[rows[i - 1], c], (r, c)
             if k:
                 assert need[r, c] >= need[r, cols[k - 1]], (r, c)
+
+
+def test_no_workspace_for_rows_that_the_backward_refuses(lib):
+    most = 1 << 24
+    assert lib.qsg_rmsnorm_bwd_workspace(4, most) > 0
+    assert lib.qsg_rmsnorm_bwd_workspace(4, most + 1) == -4
+    with pytest.raises(q.QsgError, match="2\\^24"):
+        q.qsg_rmsnorm_bwd_workspace(0, most + 1)
