@@ -461,7 +461,7 @@ int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, 
 
 /* One gradient tensor, or one chunk of it: n contiguous elements of dtype at
  * g (device), and where its clipped values go (out may be g: in place; it may
- * not overlap any other gradient). */
+ * not overlap its gradient otherwise, nor any other gradient or output). */
 typedef struct {
   const void* g;
   void* out;
@@ -480,7 +480,8 @@ typedef struct {
  *   chunks       host array for the table, or NULL to learn its length.
  *   n_chunks     in: entries that chunks has room for (chunks not NULL);
  *                out: entries of the table.
- * The caller copies the table to device memory once and keeps it as long as
+ * Outputs that overlap are refused with the table (QSG_ERR_ARG): one tensor
+ * given twice in place would be scaled twice.  The caller copies the table to device memory once and keeps it as long as
  * the tensors stay where they are. */
 int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t* n_chunks);
 

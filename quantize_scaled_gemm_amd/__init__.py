@@ -599,8 +599,9 @@ class GradPlan:
 
 def qsg_grad_plan(grads, outs=None):
     """GradPlan of contiguous fp32 or bf16 gradients of any shapes; clipped
-    values go to ``outs`` (same shapes and types; default: in place).  It is
-    made once for gradients that stay where they are, and keeps them alive."""
+    values go to ``outs`` (same shapes and types; default: in place), none of
+    which may overlap another tensor (a gradient twice in place).  It is made
+    once for gradients that stay where they are, and keeps them alive."""
     import torch
 
     grads = list(grads)

@@ -6,6 +6,9 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
+#include <new>
+
 #include "qsg.h"
 #include "qsg_internal.h"
 
@@ -461,6 +464,38 @@ int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, 
   return check_launch(fn);
 }
 
+// Whether an output of the list overlaps another tensor's gradient or output,
+// or its own gradient otherwise than in place: 1, 0, or -1 without memory.
+// Byte ranges in the order of their beginnings: one that begins before the end
+// of a range before it overlaps it.
+static int outputs_overlap(const qsg_grad* list, int64_t count) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  Range* const ranges = new (std::nothrow) Range[2 * count];
+  if (!ranges) return -1;
+  int64_t n = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const qsg_grad& t = list[k];
+    if (t.n == 0) continue;
+    const uintptr_t bytes = (uintptr_t)t.n * esize(t.dtype), g = (uintptr_t)t.g, out = (uintptr_t)t.out;
+    ranges[n++] = {g, g + bytes, out == g};
+    if (out && out != g) ranges[n++] = {out, out + bytes, true};
+  }
+  std::sort(ranges, ranges + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end = 0, written_end = 0;
+  int overlap = 0;
+  for (int64_t k = 0; k < n && !overlap; ++k) {
+    const Range& r = ranges[k];
+    overlap = r.begin < (r.written ? end : written_end);
+    if (r.end > end) end = r.end;
+    if (r.written && r.end > written_end) written_end = r.end;
+  }
+  delete[] ranges;
+  return overlap;
+}
+
 int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t* n_chunks) {
   const char* fn = "qsg_grad_plan";
   constexpr int64_t kChunk = 8192;  // elements: 8 16-byte loads a thread of fp32, all in flight at once
@@ -480,6 +515,9 @@ int qsg_grad_plan(const qsg_grad* list, int64_t count, qsg_grad* chunks, int64_t
   if (!chunks) return QSG_OK;
   if (room < total)
     return fail(QSG_ERR_ARG, "%s: the table needs %lld entries, there is room for %lld", fn, (long long)total, (long long)room);
+  const int overlap = outputs_overlap(list, count);
+  if (overlap < 0) return fail(QSG_ERR_UNSUPPORTED, "%s: no host memory to compare %lld tensors", fn, (long long)count);
+  if (overlap) return fail(QSG_ERR_ARG, "%s: an output overlaps another tensor, or its own gradient in part", fn);
   for (int64_t k = 0; k < count; ++k) {
     const qsg_grad& t = list[k];
     const int64_t esz = esize(t.dtype);

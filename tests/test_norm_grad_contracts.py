@@ -1,7 +1,10 @@
 """What the norm and clipping calls promise a caller who keeps a workspace, a
 plan or a stream across calls, on the CPU."""
 
+import ctypes
+
 import pytest
+import torch
 
 import quantize_scaled_gemm_amd as q
 from helpers import build_library, lib_is_stale
@@ -38,3 +41,67 @@ def test_no_workspace_for_rows_that_the_backward_refuses(lib):
     assert lib.qsg_rmsnorm_bwd_workspace(4, most + 1) == -4
     with pytest.raises(q.QsgError, match="2\\^24"):
         q.qsg_rmsnorm_bwd_workspace(0, most + 1)
+
+
+def table(lib, entries):
+    """Status of making the table of (g, out, n, dtype) entries."""
+    arr = (q.Grad * len(entries))(*[q.Grad(*e, 0) for e in entries])
+    n = ctypes.c_int64(0)
+    assert lib.qsg_grad_plan(arr, len(entries), None, ctypes.byref(n)) == 0
+    return lib.qsg_grad_plan(arr, len(entries), (q.Grad * max(1, n.value))(), ctypes.byref(n))
+
+
+G, O, F = 1 << 20, 1 << 24, 1 << 28  # addresses far apart: nothing is read there
+
+
+@pytest.mark.parametrize("entries", [
+    [(G, G, 100, q.F32), (G, G, 100, q.F32)],              # one tensor twice, in place: it would be scaled twice
+    [(G, G, 100, q.F32), (F, F, 7, q.BF16), (G, O, 100, q.F32)],
+    [(G, O, 100, q.F32), (F, O, 100, q.F32)],              # one output for two gradients
+    [(G, O, 100, q.F32), (F, O + 396, 100, q.F32)],        # their last and first elements
+    [(G, O, 100, q.F32), (O + 8, None, 2, q.BF16)],        # an output over another gradient
+    [(O + 8, None, 2, q.BF16), (G, O, 100, q.F32)],
+    [(G, G + 4, 100, q.F32)],                              # an output over its own gradient, one element on
+    [(G + 4, G, 100, q.F32)],
+    [(G, G, 1, q.F32), (F, F, 1, q.F32), (O, O, 20000, q.F32), (O + 79996, O + 79996, 1, q.F32)],
+])
+def test_outputs_that_overlap_are_refused(lib, entries):
+    """Chunks are clipped in any order at once: an element that two of them
+    write, or that one reads and another writes, has no one value."""
+    for e in (entries, entries[::-1]):
+        assert table(lib, e) == -1
+        assert b"overlap" in lib.qsg_last_error()
+
+
+@pytest.mark.parametrize("entries", [
+    [(G, G, 100, q.F32), (G + 400, G + 400, 100, q.F32), (G + 800, G + 800, 3, q.BF16)],   # slices of one buffer
+    [(G, O, 100, q.F32), (G, O + 400, 100, q.F32)],        # one gradient read twice
+    [(G, None, 100, q.F32), (G, None, 100, q.F32)],        # for the sum alone
+    [(G, O, 100, q.F32), (G + 400, O + 400, 5, q.F32)],
+    [(G, G, 0, q.F32), (G, G, 100, q.F32)],                # nothing at an address
+    [(G + 400, G, 100, q.F32)],
+])
+def test_outputs_beside_each_other_are_taken(lib, entries):
+    for e in (entries, entries[::-1]):
+        assert table(lib, e) == 0, lib.qsg_last_error()
+
+
+def test_the_binding_refuses_a_gradient_given_twice(lib):
+    class Tensor:
+        shape, dtype, device, is_cuda = (10, 10), torch.float32, "cuda:0", True
+
+        def __init__(self, at):
+            self.at = at
+
+        def is_contiguous(self):
+            return True
+
+        def numel(self):
+            return 100
+
+        def data_ptr(self):
+            return self.at
+
+    a, b = Tensor(G), Tensor(O)
+    with pytest.raises(q.QsgError, match="overlap"):
+        q.qsg_grad_plan([a, b, a])
