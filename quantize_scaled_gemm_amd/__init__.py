@@ -591,10 +591,21 @@ GRAD_WORKSPACE_BYTES = 8192  # QSG_GRAD_WORKSPACE_BYTES of include/qsg.h
 
 class GradPlan:
     """The chunk table of a list of gradients, on the GPU (``table``,
-    ``n_chunks``), with the tensors that it points into."""
+    ``n_chunks``), with the tensors that it points into.  It has to live until
+    a captured graph that reads it is replayed no more."""
 
-    def __init__(self, table, n_chunks, grads, outs):
+    def __init__(self, table, n_chunks, grads, outs, stream=None):
         self.table, self.n_chunks, self.grads, self.outs = table, n_chunks, grads, outs
+        self.streams = {stream}  # handles: where the table was allocated, and every one recorded below
+
+    def read_on(self, stream):
+        """A launch on this stream reads the table: its memory, once freed, is
+        not given away before that launch is done."""
+        if stream not in self.streams:
+            import torch
+
+            self.table.record_stream(torch.cuda.ExternalStream(stream, device=self.table.device))
+            self.streams.add(stream)
 
 
 def qsg_grad_plan(grads, outs=None):
@@ -628,19 +639,23 @@ def qsg_grad_plan(grads, outs=None):
     _check(lib.qsg_grad_plan(entries, len(grads), chunks, ctypes.byref(n)))
     host = torch.frombuffer(chunks, dtype=torch.uint8)
     table = host.to(grads[0].device if grads else "cuda")
-    return GradPlan(table, n.value, grads, outs)
+    return GradPlan(table, n.value, grads, outs, torch.cuda.current_stream(table.device).cuda_stream)
 
 
 def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
     """sumsq (1 fp64 on the GPU) = sum of the squares of the plan's gradients.
     workspace: GRAD_WORKSPACE_BYTES bytes on the GPU."""
+    on = _stream(stream)
     _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
-                                         _workspace(workspace, GRAD_WORKSPACE_BYTES), _stream(stream)))
+                                         _workspace(workspace, GRAD_WORKSPACE_BYTES), on))
+    plan.read_on(on)
 
 
 def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
     """The plan's outputs = gradients * min(1, max_norm / (norm + 1e-6)) with
     norm = sqrt(sumsq), written to norm_out (1 fp32) if given."""
+    on = _stream(stream)
     _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
                                         max_norm, None if norm_out is None else _dense(norm_out, "norm_out", 1, "f32"),
-                                        _stream(stream)))
+                                        on))
+    plan.read_on(on)

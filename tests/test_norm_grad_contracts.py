@@ -105,3 +105,34 @@ def test_the_binding_refuses_a_gradient_given_twice(lib):
     a, b = Tensor(G), Tensor(O)
     with pytest.raises(q.QsgError, match="overlap"):
         q.qsg_grad_plan([a, b, a])
+
+
+def test_a_plan_lives_for_every_stream_that_reads_it(lib, monkeypatch):
+    """The table is the binding's own memory: a launch on another stream than the
+    one that it was allocated on is recorded with the allocator, once per
+    stream, or the memory could be given away before that launch has read it."""
+    recorded = []
+
+    class Table:
+        is_cuda = True
+        device = "cuda:0"
+
+        def data_ptr(self):
+            return 4096
+
+        def record_stream(self, s):
+            recorded.append(s)
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: 0
+
+    monkeypatch.setattr(q, "load_library", Lib)
+    monkeypatch.setattr(q, "_stream", lambda stream: stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: (handle, device))
+    plan = q.GradPlan(Table(), 1, [], [], stream=7)
+    for s in (7, 9, 7, 9, 11):
+        q.qsg_grad_sumsq(plan, 64, 64, stream=s)
+        q.qsg_grad_clip(plan, 64, 1.0, stream=s)
+    q.qsg_grad_clip(plan, 64, 1.0, stream=13)
+    assert recorded == [(9, "cuda:0"), (11, "cuda:0"), (13, "cuda:0")]
