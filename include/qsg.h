@@ -475,8 +475,8 @@ typedef struct {
 
 /* Cuts a list of gradient tensors into chunks of one size (a host function:
  * it touches no device).
- *   list, count  host array of the tensors; out may be NULL where the table
- *                is used by qsg_grad_sumsq alone.
+ *   list, count  host array of the tensors; one whose out is NULL counts in
+ *                qsg_grad_sumsq and is left out of qsg_grad_clip.
  *   chunks       host array for the table, or NULL to learn its length.
  *   n_chunks     in: entries that chunks has room for (chunks not NULL);
  *                out: entries of the table.

@@ -145,6 +145,7 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(const qsg_grad* table, i
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = norm;
   for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
     const qsg_grad t = table[n - 1 - c];  // last chunks first: the sum has read them last
+    if (!t.out) continue;                     // a tensor of the sum alone
     if (k == 1.0f && t.out == t.g) continue;  // every product is the value itself
     if (t.dtype == QSG_BF16)
       chunk_scale(reinterpret_cast<const uint16_t*>(t.g), reinterpret_cast<uint16_t*>(t.out), (int)t.n, k);

@@ -31,7 +31,7 @@ def test_a_plan_dropped_while_another_stream_reads_it(q):
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(50_000_000)  # some 20 ms
+        torch.cuda._sleep(50_000_000)  # outlasts the lines below
         q.qsg_grad_clip(plan, sumsq, 1.0)
     del plan
     others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(64)]
@@ -43,3 +43,33 @@ def test_a_plan_dropped_while_another_stream_reads_it(q):
     want = 2.0 / 60000.0 ** 0.5
     for g in grads:
         assert abs(to_np(g) / want - 1).max() < 1e-6
+
+
+def test_a_tensor_without_an_output_is_left_out_of_the_clip(q):
+    """qsg.h lets a table for the sum alone have no outputs; a clip by such a
+    table writes the others' values and the norm."""
+    import ctypes
+
+    import torch
+
+    a, b, c = (torch.full((n,), 3.0, device="cuda") for n in (9000, 20001, 5))
+    out = torch.zeros_like(c)
+    entries = (q.Grad * 3)(q.Grad(a.data_ptr(), a.data_ptr(), a.numel(), q.F32, 0),
+                           q.Grad(b.data_ptr(), None, b.numel(), q.F32, 0),
+                           q.Grad(c.data_ptr(), out.data_ptr(), c.numel(), q.F32, 0))
+    chunks, n = (q.Grad * 8)(), ctypes.c_int64(8)
+    lib = q.load_library()
+    assert lib.qsg_grad_plan(entries, 3, chunks, ctypes.byref(n)) == 0 and n.value == 6
+    table = torch.frombuffer(chunks, dtype=torch.uint8).cuda()
+    plan = q.GradPlan(table, n.value, [a, b, c], None)
+    sumsq, norm = torch.empty(1, dtype=torch.float64, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(q.GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    for max_norm in (1.0, 1e9):
+        for t in (a, b, c):
+            t.fill_(3.0)
+        q.qsg_grad_sumsq(plan, sumsq, ws)
+        q.qsg_grad_clip(plan, sumsq, max_norm, norm)
+        assert sumsq.item() == 9.0 * 29006
+        k = min(1.0, max_norm / (9.0 * 29006) ** 0.5)
+        assert (b == 3).all() and (c == 3).all()
+        assert abs(to_np(a) / (3 * k) - 1).max() < 1e-6 and abs(to_np(out) / (3 * k) - 1).max() < 1e-6
