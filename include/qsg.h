@@ -501,10 +501,11 @@ int qsg_grad_sumsq(const qsg_grad* chunks_dev, int64_t n_chunks, double* sumsq_d
  *     out  = g * k                    (binary32, rounded once to dtype)
  *
  *   sumsq_dev    in: 1 double.
- *   max_norm     >= 0; infinity copies (or, in place, leaves) the gradients.
+ *   max_norm     >= 0; infinity copies (or, in place, leaves) the gradients
+ *                whatever the norm (k = 1).
  *   norm_out_dev out: 1 float, norm, or NULL.
- * A NaN norm gives k = NaN and an infinite one k = 0, and so NaN where it
- * meets an infinite gradient. */
+ * Under a finite max_norm a NaN norm gives k = NaN, and an infinite one k = 0
+ * and so NaN where it meets an infinite gradient. */
 int qsg_grad_clip(const qsg_grad* chunks_dev, int64_t n_chunks, const double* sumsq_dev, float max_norm,
                   float* norm_out_dev, void* stream);
 

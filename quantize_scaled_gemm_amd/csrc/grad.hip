@@ -2,6 +2,7 @@
 //
 //   S    = sum over tensors and elements of g^2          (binary64)
 //   norm = sqrt(S),  k = min(1, max_norm / (norm + 1e-6)),  out = g k
+//   (an infinite max_norm: k = 1, whatever the norm)
 //
 // The tensors are cut into chunks on the host (qsg_grad_plan) and the table
 // of chunks lies in device memory, so one launch covers any number of
@@ -15,6 +16,7 @@
 // elements: 16384 435 us and 32768 439 us for the clip (the last round of
 // workgroups is shorter).  Plain instead of non-temporal loads in the sum: 203
 // us, and 418 for the clip after them.
+#include <float.h>
 #include <hip/hip_runtime.h>
 
 #include "qsg.h"
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(256) void grad_clip_kernel(const qsg_grad* table, i
                                                         float max_norm, float* norm_out) {
   const float norm = (float)sqrt(*sumsq);
   float k = __fdiv_rn(max_norm, norm + 1e-6f);
-  if (k > 1.0f) k = 1.0f;  // a NaN stays
+  if (k > 1.0f || max_norm > FLT_MAX) k = 1.0f;  // a NaN stays under a finite limit
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out) *norm_out = norm;
   for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
     const qsg_grad t = table[n - 1 - c];  // last chunks first: the sum has read them last

@@ -73,3 +73,23 @@ def test_a_tensor_without_an_output_is_left_out_of_the_clip(q):
         k = min(1.0, max_norm / (9.0 * 29006) ** 0.5)
         assert (b == 3).all() and (c == 3).all()
         assert abs(to_np(a) / (3 * k) - 1).max() < 1e-6 and abs(to_np(out) / (3 * k) - 1).max() < 1e-6
+
+
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_an_infinite_limit_copies_whatever_the_norm(q, bad, in_place):
+    """max_norm = infinity asks for the norm alone: one bad gradient is seen in
+    the norm, and no other gradient is touched."""
+    import torch
+
+    t = torch.arange(1, 20001, device="cuda").float()
+    t[777] = float(bad)
+    before = to_np(t).copy()
+    out = t if in_place else torch.zeros_like(t)
+    sumsq, norm = torch.empty(1, dtype=torch.float64, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(q.GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    plan = q.qsg_grad_plan([t], [out])
+    q.qsg_grad_sumsq(plan, sumsq, ws)
+    q.qsg_grad_clip(plan, sumsq, float("inf"), norm)
+    assert (to_np(out) == before)[[k for k in range(20000) if k != 777]].all()
+    assert str(to_np(out)[777]) == bad and str(to_np(norm)[0]) == bad
