@@ -453,8 +453,10 @@ int64_t qsg_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
  *   workspace  device memory of qsg_rmsnorm_bwd_workspace(rows, cols) bytes,
  *              4-byte aligned; nothing has to be in it before, and calls that
  *              overlap in time need one each.
- * Sums are binary32 in an order that depends on the shape alone, so equal
- * calls give equal bits.  cols <= 2^24 (QSG_ERR_UNSUPPORTED).  rows == 0 writes dgamma = 0 unless accumulate. */
+ * Sums are binary32 (dgamma: binary32 over the rows that one workgroup takes,
+ * binary64 over the workgroups, rounded once) in an order that depends on the
+ * shape alone, so equal calls give equal bits.  cols <= 2^24
+ * (QSG_ERR_UNSUPPORTED).  rows == 0 writes dgamma = 0 unless accumulate. */
 int qsg_rmsnorm_bwd(const void* dy, const void* h, const void* dres, int dtype, int64_t rows, int64_t cols,
                     int64_t lddy, int64_t ldh, int64_t lddres, const void* gamma, int gamma_dtype, const float* rstd,
                     void* dx, int64_t lddx, float* dgamma, int accumulate, void* workspace, void* stream);

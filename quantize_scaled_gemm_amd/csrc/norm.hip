@@ -10,7 +10,8 @@
 //   dx     = rstd (dn - n sum(dn n) / cols) + dres
 //   dgamma = sum over rows of dy n
 //
-// All sums are binary32.  8 consecutive elements of a row (16 bytes of bf16,
+// Sums along rows and each group's share of dgamma are binary32, the sum of the
+// shares binary64.  8 consecutive elements of a row (16 bytes of bf16,
 // 32 of fp32) are one chunk; a lane takes whole chunks, so a 1 x 32 block is
 // 4 lanes and a 1 x 128 block 16.  The cols % 8 elements after the last whole
 // chunk go one to a lane.  Chunks are loaded and stored with vector accesses
@@ -179,6 +180,8 @@ __device__ __forceinline__ float load_gamma1(const void* gamma, bool bf16, int64
 // ---------------------------------------------------------------------------
 // sums
 // ---------------------------------------------------------------------------
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i gets 7 - i of its 8, 15 - i of its 16
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
@@ -189,7 +192,6 @@ __device__ __forceinline__ float dpp_add(float v) {
 // exchanges, 16 lanes by mirrors, rows by swaps).
 template <int LANES>
 __device__ __forceinline__ float lane_sum(float v) {
-  constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i gets 7 - i of its 8, 15 - i of its 16
   v = dpp_add<kDppXor1>(v);
   v = dpp_add<kDppXor2>(v);
   v = dpp_add<kHalfMirror>(v);
@@ -1111,15 +1113,36 @@ __global__ __launch_bounds__(256) void norm_bwd_dot_kernel(NormBwdArgs a) {
   }
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+  return v + __hiloint2double((int)dpp_u32<CTRL>((uint32_t)__double2hiint(v)), (int)dpp_u32<CTRL>((uint32_t)__double2loint(v)));
+}
+
+// Sum over 32 lanes, the same in each, by the steps of lane_sum (shuffles, which
+// pass through LDS: dgamma of 333 rows by 1111 columns 5.4 us).
+__device__ __forceinline__ double half_wave_sum(double v) {
+  v = dpp_add<kDppXor1>(v);
+  v = dpp_add<kDppXor2>(v);
+  v = dpp_add<kHalfMirror>(v);
+  v = dpp_add<kMirror>(v);
+  const uint32_t lo = (uint32_t)__double2loint(v), hi = (uint32_t)__double2hiint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+  return __hiloint2double((int)b[0], (int)a[0]) + __hiloint2double((int)b[1], (int)a[1]);
+}
+
 // dgamma[c] (+)= sum over groups of partial[group][c], in a fixed order: a
-// workgroup takes 32 columns, 8 lanes of 4 columns by 128 parts of the groups.
+// workgroup takes 32 columns, 8 lanes of 4 columns by 128 parts of the groups;
+// then a half wave takes a column, 4 parts a lane, and adds its lanes pairwise.
+// All of it is binary64, rounded once: there are up to 4096 partials, and of
+// small ones beside a large one a binary32 chain keeps none.
 __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* partial, int64_t groups, int64_t cols,
                                                           float* dgamma, bool accumulate) {
   constexpr int PARTS = 128;
-  __shared__ float sum[PARTS][33];
+  __shared__ double sum[PARTS][33];
   const int lane = threadIdx.x & 7, part = threadIdx.x >> 3;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane * 4;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
   if (c + 4 <= cols) {
 #pragma unroll 8
     for (int64_t k = part; k < groups; k += PARTS) {
@@ -1135,22 +1158,11 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* partial,
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[part][lane * 4 + i] = v[i];
   __syncthreads();
-  const int col = threadIdx.x & 31, p = threadIdx.x >> 5;
-  float s = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) s += sum[p + k * (PARTS / 4)][col];
-  __syncthreads();
-  sum[p][col] = s;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int64_t at = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    if (at < cols) {
-      s = sum[0][threadIdx.x];
-#pragma unroll
-      for (int k = 1; k < PARTS / 4; ++k) s += sum[k][threadIdx.x];
-      dgamma[at] = accumulate ? dgamma[at] + s : s;
-    }
-  }
+  const int p = threadIdx.x & 31, col = threadIdx.x >> 5;
+  double s = (sum[p][col] + sum[p + 32][col]) + (sum[p + 64][col] + sum[p + 96][col]);
+  s = half_wave_sum(s);
+  const int64_t at = (int64_t)blockIdx.x * 32 + col;
+  if (p == 0 && at < cols) dgamma[at] = (float)(accumulate ? dgamma[at] + s : s);
 }
 
 constexpr int64_t kBwdMostCols = 16391;  // of a row held in registers: 2048 chunks and 7 elements
