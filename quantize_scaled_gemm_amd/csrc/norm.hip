@@ -650,6 +650,15 @@ struct ColArgs {
 
 constexpr int CT_COLS = 64;
 
+// Between a wave's writes to LDS and its lanes' reads of each other's: the
+// memory model's order, and no instruction, since a wave's LDS accesses are
+// performed in theirs.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // max(|a|, |b|, |c|, |d|) of values that are not NaN (written out: the compiler
 // puts an instruction before each operand to quiet a NaN)
 __device__ __forceinline__ float max4_abs(float a, float b, float c, float d) {
@@ -794,7 +803,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
     }
     *reinterpret_cast<u32x4*>(&lane_max[wave][ty & 7][tx * 8]) = u32x4{cm[0], cm[1], cm[2], cm[3]};
     *reinterpret_cast<u32x4*>(&lane_max[wave][ty & 7][tx * 8 + 4]) = u32x4{cm[4], cm[5], cm[6], cm[7]};
-    __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses are performed in their order
+    wave_lds_order();
     uint32_t m = lane_max[wave][0][lane];
 #pragma unroll
     for (int k = 1; k < 8; ++k) m = umax_u32(m, lane_max[wave][k][lane]);
@@ -816,7 +825,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
         reinterpret_cast<float*>(a.st)[(c0 + lane) * (a.rows / 128) + r0 / 128] = __fdiv_rn(1.0f, s);
       easy = plain && __all(m < 0x7F800000u);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     float cs[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) cs[i] = cscale[wave][tx * 8 + i];
