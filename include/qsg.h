@@ -416,8 +416,9 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
  *              (MXFP8: rows % 32 == 0; 1X128: rows % 128 == 0); or NULL.
  *   amax_out_dev  out, DELAYED only: 1 float, max |y| (for qsg_amax_update),
  *              or NULL.
- * One of y, q and qt is needed.  Pointers are aligned to their elements;
- * cols <= 2^24 (QSG_ERR_UNSUPPORTED beyond).
+ * One of y, q and qt is needed (with a recipe, one of q and qt).  No output but
+ * h may overlap an input, and no output another.  Pointers are aligned to
+ * their elements; cols <= 2^24 (QSG_ERR_UNSUPPORTED beyond).
  * One pass over the data row-wise; with qt or TENSORWISE a second kernel
  * reads h (x without a residual) back.  rows == 0 or cols == 0 writes only
  * TENSORWISE's s (amax 0) and DELAYED's amax (0).  A row of zeros with

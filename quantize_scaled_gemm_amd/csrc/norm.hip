@@ -686,11 +686,12 @@ __device__ __forceinline__ float max4_abs(float a, float b, float c, float d) {
 // subnormal has the code of zero.
 //
 // What bounds it: the order of its accesses.  It reads 128-byte pieces of rows
-// and writes 128-byte pieces of columns; without its stores 32768 x 4096 takes
-// 52 us of 66, without its loads 56, and the vector instructions of the waves
-// are 47 % of the time.  Tried without gain: 256 or 512 rows a tile (81 and 87
-// us), 2-16 tiles a workgroup with the next one's loads in flight (66-76), a
-// tile order by XCD (the whole call 217 -> 221-225), 6-8 waves a SIMD.
+// and writes 128-byte pieces of columns; 32768 x 4096 takes 66-71 us, a copy of
+// the kernel without its stores 51, without its loads 57, and the vector
+// instructions of the waves are 44 % of the cycles.  Tried without gain: 256 or
+// 512 rows a tile (81 and 87 us), 2-16 tiles a workgroup with the next one's
+// loads in flight (66-76), a tile order by XCD (the whole call 217 -> 221-225),
+// 6-8 waves a SIMD.
 template <typename In, int QUANT>
 __global__ __launch_bounds__(256) void norm_col_kernel(ColArgs a) {
   __shared__ uint32_t codes[CT_COLS * CT_STRIDE];
@@ -1196,11 +1197,22 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols) {
   int64_t most = chunks <= 32 ? 512 : chunks <= 512 ? 1024 : chunks <= 1024 ? 512 : chunks <= 2048 ? 256 : 128;
   // Two or four rows to a workgroup, which adds their shares of dgamma in LDS:
   // less to write and read again, for a barrier that the rows share.
-  // [measured, us per call, one / two / four rows] 1024 x 4096 18.8 / 15.3 /
-  // 14.7, 1024 x 1024 11.5 / 9.6 / 9.2, 8192 x 4096 58.6 / 52.6 / 56.5 (without
-  // a residual gradient 43.8 / 41.1 / 46.9), 2048 x 2048 15.6 / 14.6 / 16.8, but
-  // 256 x 1024 7.5 / - / 8.3 and 32768 x 1024 57.8 / 60.6 / 69; 512 x 7168
-  // 17.2 / 15.7, 8192 x 7168 88 / 92.
+  // [measured, us a call in a graph with a residual gradient, one / two / four
+  // rows]
+  //   rows   1024 columns          2048                  4096                  7168
+  //    256    6.1 /  6.2 /  6.7     7.2 /  7.0 /  7.3     8.6 /  8.6 /  9.5    12.6 / 11.7
+  //    384    7.1 /  6.8 /  7.2     8.6 /  7.4 /  7.6    11.2 /  9.8 / 10.0    16.0 / 13.4
+  //    640    8.4 /  7.6 /  7.6    10.2 /  8.7 /  8.2    15.0 / 12.0 / 11.0
+  //   1024    9.4 /  8.8 /  8.1    13.1 / 10.3 /  8.9    20.7 / 15.1 / 13.0    23.5 / 21.0
+  //   1280   10.2 /  9.3 / 11.0    13.3 / 11.2 / 12.5    21.9 / 17.3 / 19.1    25.6 / 24.8
+  //   2048   11.5 / 10.2 / 12.3    15.5 / 13.2 / 15.1    25.6 / 20.6 / 23.1    31.8 / 31.6
+  //   8192   20.7 / 20.5 / 23.7    31.4 / 28.8 / 32.7
+  //  32768   56.0 / 59.7 / 66.7    96.7 / 94.0 / 97.8
+  // Around 160 chunks, one / two rows: 1280 columns 16384 rows 36.6 / 36.5,
+  // 20000 42.1 / 42.4, 32768 64.5 / 64.6; 1288 columns 38.7 / 37.0, 44.7 / 43.0,
+  // 68.2 / 65.5.  The borders are coarse: four rows stay up to 1280 where two
+  // are ahead from 1025 on, and one row beyond 1280 at 7168 columns where two
+  // are ahead by 4 % up to 1536.
   if (p.tpr == 256 && rows >= 384) {
     if (chunks <= 512 && rows <= 1280) {
       p.blk = 1024;
