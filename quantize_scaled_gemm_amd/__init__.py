@@ -601,7 +601,7 @@ class GradPlan:
     def read_on(self, stream):
         """A launch on this stream reads the table: its memory, once freed, is
         not given away before that launch is done."""
-        if stream not in self.streams:
+        if stream not in self.streams and not isinstance(self.table, int):
             import torch
 
             self.table.record_stream(torch.cuda.ExternalStream(stream, device=self.table.device))

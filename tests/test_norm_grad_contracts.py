@@ -136,3 +136,16 @@ def test_a_plan_lives_for_every_stream_that_reads_it(lib, monkeypatch):
         q.qsg_grad_clip(plan, 64, 1.0, stream=s)
     q.qsg_grad_clip(plan, 64, 1.0, stream=13)
     assert recorded == [(9, "cuda:0"), (11, "cuda:0"), (13, "cuda:0")]
+
+
+def test_a_plan_on_a_raw_table(lib, monkeypatch):
+    """A table that is an address, as every call here takes one, is its owner's."""
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: 0
+
+    monkeypatch.setattr(q, "load_library", Lib)
+    monkeypatch.setattr(q, "_stream", lambda stream: stream)
+    plan = q.GradPlan(4096, 1, [], [])
+    q.qsg_grad_sumsq(plan, 64, 64, stream=9)
+    q.qsg_grad_clip(plan, 64, 1.0, stream=11)
