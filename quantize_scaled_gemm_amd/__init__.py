@@ -601,11 +601,11 @@ class GradPlan:
     def read_on(self, stream):
         """A launch on this stream reads the table: its memory, once freed, is
         not given away before that launch is done."""
-        if stream not in self.streams and not isinstance(self.table, int):
+        if not isinstance(self.table, int):
             import torch
 
             self.table.record_stream(torch.cuda.ExternalStream(stream, device=self.table.device))
-            self.streams.add(stream)
+        self.streams.add(stream)
 
 
 def qsg_grad_plan(grads, outs=None):
@@ -648,7 +648,8 @@ def qsg_grad_sumsq(plan, sumsq, workspace, stream=None):
     on = _stream(stream)
     _check(load_library().qsg_grad_sumsq(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
                                          _workspace(workspace, GRAD_WORKSPACE_BYTES), on))
-    plan.read_on(on)
+    if on not in plan.streams:
+        plan.read_on(on)
 
 
 def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
@@ -658,4 +659,5 @@ def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
     _check(load_library().qsg_grad_clip(_ptr(plan.table), plan.n_chunks, _dense(sumsq, "sumsq", 1, "f64"),
                                         max_norm, None if norm_out is None else _dense(norm_out, "norm_out", 1, "f32"),
                                         on))
-    plan.read_on(on)
+    if on not in plan.streams:
+        plan.read_on(on)
