@@ -381,6 +381,104 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
                    int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
                    void* c, int c_dtype, int64_t ldc, void* stream);
 
+/* INT8: symmetric 8-bit integers with one scale for each token (a row) or
+ * channel (a column, in the transposed copy), or for 128 neighbours of a row.
+ * Values whose largest magnitude is amax share the scale
+ *     s = max(fp32(amax / 127), 2^-126), or 1 for amax 0,
+ *     code = rint(fp32(v * fp32(1 / s)))     (nearest, ties to even)
+ * which lies in [-127, 127]; a code stands for code * s.  Where amax is
+ * infinite or NaN, s is NaN and the codes are 0, so whatever reads them gives
+ * NaN. */
+
+/* Bytes of the workspace that qsg_quantize_int8 needs for the transposed copy
+ * of this shape and of every shape with no more rows and no more columns (0
+ * for an empty one), or a negative qsg_status. */
+int64_t qsg_quantize_int8_workspace(int64_t rows, int64_t cols);
+
+/* INT8 copies of a matrix.
+ *   x      rows x cols (dtype, ld), aligned to its element size.
+ *   q, s   out: rows x cols codes (dense) with rows fp32 scales, one for each
+ *          row; or both NULL.
+ *   qt, st out: the transposed copy, cols x rows codes (dense) with cols fp32
+ *          scales, one for each column of x; or both NULL.
+ *   workspace  for qt: qsg_quantize_int8_workspace(rows, cols) bytes of device
+ *          memory, 4-byte aligned; nothing has to be in it before, and calls
+ *          that overlap in time need one each.  Without qt it is not read and
+ *          may be NULL.
+ * No output may overlap x or another output.  rows == 0 or cols == 0 writes
+ * scales of 1 for the rows or columns that are there.  rows and cols below
+ * 2^30 (QSG_ERR_UNSUPPORTED). */
+int qsg_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* s,
+                      int8_t* qt, float* st, void* workspace, void* stream);
+
+/* Product of two INT8 matrices with a scale for each row of both:
+ *
+ *     C[m, n] = fp32(fp32(sum_k A[m, k] * B[n, k]) * sa[m]) * sb[n] + bias[n]
+ *
+ * The sum is exact (32-bit integers; K <= 131071, QSG_ERR_UNSUPPORTED beyond);
+ * its scaling is binary32 and C is rounded once.
+ *   a, sa  M x K codes (lda) with M fp32 scales;  b, sb  N x K (ldb) with N.
+ *   bias   N values of bias_dtype (QSG_F32 or QSG_BF16), or NULL.
+ *   c      M x N (ldc) of c_dtype, aligned to its element size; it may not
+ *          overlap an input.
+ * fprop takes the row-wise copies of X and W, dgrad those of dY and the
+ * transposed copy of W.  Any shape and alignment: 16-byte aligned operands
+ * with leading dimensions of whole 16 bytes and K % 256 == 0 select the
+ * fastest kernel where C has at least 128 tiles of 256 x 256. */
+int qsg_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N, int64_t K,
+                  int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype, int64_t ldc,
+                  void* stream);
+
+/* Weight gradient from a layer input that was kept in INT8 for the backward
+ * pass (the weight gradient stays in bf16, as qsg_wgrad_bf16):
+ *
+ *     C[n, k] = sum_t dY[t, n] * x'[t, k],  x' = bf16(fp32(q[t, k] * s[t]))
+ *
+ *   dy   T x N bf16 (lddy);  q  T x K codes (ldq) with T fp32 scales s, as the
+ *        row-wise copy of qsg_quantize_int8 (a scale of NaN makes C NaN).
+ *   c    N x K (ldc), QSG_BF16 (written, rounded to nearest even) or QSG_F32
+ *        (written, or with accumulate = 1 added to: the fp32 main gradient).
+ * x' is the bf16 tensor that the codes stand for; its products with dY are
+ * exact in binary32 and are summed there.  T == 0 writes zeros (or adds +0).
+ * Accumulation into bf16 returns QSG_ERR_UNSUPPORTED.  Any alignment; 16-byte
+ * aligned dy and q with lddy % 8 == 0, ldq % 16 == 0, N % 8 == 0 and
+ * K % 16 == 0 select the fast path. */
+int qsg_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
+                   int64_t ldq, void* c, int c_dtype, int64_t ldc, int accumulate, void* stream);
+
+/* Gated activation a = silu(g) * u, silu(g) = g / (1 + exp(-g)), with g and u
+ * kept in INT8 for the backward pass.
+ *   gu      rows x (2 cols) (dtype, ld): a row holds its cols values of g,
+ *           then its cols values of u.
+ *   a       out: rows x cols of dtype (dense), rounded once; or NULL.
+ *   aq, sa  out: rows x cols codes (dense) with rows fp32 scales, the INT8
+ *           copy of a (from binary32, not from its rounding to dtype) that the
+ *           next Linear reads; or both NULL.
+ *   ck, cs  out: rows x (2 cols) codes of gu (dense) with rows x 2 ceil(cols /
+ *           128) fp32 scales: those of g's blocks of 128 neighbours (the last
+ *           one may be shorter), then those of u's; or both NULL (a forward
+ *           pass that no backward pass follows).
+ * One of a, aq and ck is needed.  The formula is evaluated in binary32 from gu
+ * itself.  No output may overlap gu or another output.  rows and cols below 2^30
+ * (QSG_ERR_UNSUPPORTED). */
+int qsg_swiglu_int8_store_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* a, int8_t* aq,
+                              float* sa, int8_t* ck, float* cs, void* stream);
+
+/* Backward of the above, from the kept codes alone: with g = fp32(code * s),
+ * u likewise and p = 1 / (1 + exp(-g)),
+ *
+ *     dg = da * u * p * (1 + g * (1 - p)),   du = da * g * p
+ *
+ *   da      rows x cols (dtype, ldda), the gradient of a.
+ *   ck, cs  as qsg_swiglu_int8_store_fwd wrote them.
+ *   dgu     out: rows x (2 cols) of dtype (lddgu >= 2 cols): dg, then du; each
+ *           rounded once from binary32.
+ *   a       out: rows x cols of dtype (dense), g * p * u from the kept values
+ *           (the next Linear's weight gradient reads it); or NULL.
+ * No output may overlap an input or another output.  Limits as above. */
+int qsg_swiglu_int8_store_bwd(const void* da, int dtype, int64_t rows, int64_t cols, int64_t ldda, const int8_t* ck,
+                              const float* cs, void* dgu, int64_t lddgu, void* a, void* stream);
+
 /* Residual addition and root-mean-square norm with an FP8 output: the input
  * of a pre-norm Linear, quantized for its fprop and (transposed copy) wgrad
  * GEMMs without a high-precision copy in memory.  For each row

@@ -71,3 +71,4 @@ from .activation import (  # noqa: F401
     elementwise_check,
 )
 from . import norm  # noqa: F401  (residual + RMS norm, its gradient, gradient clipping)
+from . import int8  # noqa: F401  (INT8 codes, their product, the gated activation kept in them)

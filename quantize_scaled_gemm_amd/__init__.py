@@ -42,6 +42,12 @@ ENTRY_POINTS = (
     "qsg_wgrad_bf16",
     "qsg_quantize_nvfp4",
     "qsg_gemm_nvfp4",
+    "qsg_quantize_int8_workspace",
+    "qsg_quantize_int8",
+    "qsg_gemm_int8",
+    "qsg_wgrad_int8",
+    "qsg_swiglu_int8_store_fwd",
+    "qsg_swiglu_int8_store_bwd",
     "qsg_rmsnorm_quantize",
     "qsg_rmsnorm_bwd_workspace",
     "qsg_rmsnorm_bwd",
@@ -118,6 +124,13 @@ def load_library(path=LIB_PATH):
     lib.qsg_grad_plan.argtypes = [ctypes.POINTER(Grad), I64, ctypes.POINTER(Grad), ctypes.POINTER(I64)]
     lib.qsg_grad_sumsq.argtypes = [P, I64, P, P, P]
     lib.qsg_grad_clip.argtypes = [P, I64, P, ctypes.c_float, P, P]
+    lib.qsg_quantize_int8_workspace.restype = I64
+    lib.qsg_quantize_int8_workspace.argtypes = [I64, I64]
+    lib.qsg_quantize_int8.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P]
+    lib.qsg_gemm_int8.argtypes = [P, P, P, P, I64, I64, I64, I64, I64, P, I, P, I, I64, P]
+    lib.qsg_wgrad_int8.argtypes = [P, I64, I64, I64, P, P, I64, I64, P, I, I64, I, P]
+    lib.qsg_swiglu_int8_store_fwd.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P]
+    lib.qsg_swiglu_int8_store_bwd.argtypes = [P, I, I64, I64, I64, P, P, P, I64, P, P]
     _lib = lib
     return lib
 
@@ -160,7 +173,7 @@ def _matrix(t):
 
 def _buffer(t, name, numel, dtype, required=True):
     """Check a buffer the library reads or writes densely: on the GPU,
-    contiguous, exactly ``numel`` elements of ``dtype`` ("u8", "f32", "bf16", "f64").
+    contiguous, exactly ``numel`` elements of ``dtype`` ("u8", "i8", "f32", "bf16", "f64").
     Raw integer pointers are passed through unchecked (the C ABI's own
     contract applies to them)."""
     if t is None:
@@ -171,7 +184,8 @@ def _buffer(t, name, numel, dtype, required=True):
         return
     import torch
 
-    want = {"u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16, "f64": torch.float64}[dtype]
+    want = {"u8": torch.uint8, "i8": torch.int8, "f32": torch.float32, "bf16": torch.bfloat16,
+            "f64": torch.float64}[dtype]
     if not t.is_cuda:
         raise QsgError(f"{name} must live on the GPU")
     if t.dtype != want:
@@ -469,7 +483,8 @@ def _float_code(t):
         import torch
 
         _FLOATS.update({torch.bfloat16: (BF16, "bf16"), torch.float32: (F32, "f32")})
-        _NAMES.update({torch.bfloat16: "bf16", torch.float32: "f32", torch.uint8: "u8", torch.float64: "f64"})
+        _NAMES.update({torch.bfloat16: "bf16", torch.float32: "f32", torch.uint8: "u8", torch.float64: "f64",
+                       torch.int8: "i8"})
         e = _FLOATS[t.dtype]
     return e
 
@@ -661,3 +676,131 @@ def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
                                         on))
     if on not in plan.streams:
         plan.read_on(on)
+
+
+# ---------------------------------------------------------------------------
+# INT8
+# ---------------------------------------------------------------------------
+def _here(*tensors):
+    """The library launches on the current device: its tensors are there."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != dev:
+            raise QsgError(f"a tensor is on device {t.get_device()}, the current device is {dev}")
+
+
+def _codes(t, name):
+    """(pointer, rows, cols, ld) of an INT8 operand."""
+    p, rows, cols, ld = _rows(t, name)
+    if _NAMES.get(t.dtype) != "i8":
+        import torch
+
+        if t.dtype is not torch.int8:
+            raise QsgError(f"{name} must hold INT8 codes as int8 (got {t.dtype})")
+    return p, rows, cols, ld
+
+
+def _pair(codes, numel, cname, scales, n, sname):
+    """Pointers of codes and the scales that belong to them, or of neither."""
+    if codes is None and scales is None:
+        return None, None
+    return _dense(codes, cname, numel, "i8"), _dense(scales, sname, n, "f32")
+
+
+def qsg_quantize_int8_workspace(rows, cols):
+    """Bytes of the workspace of qsg_quantize_int8 with a transposed copy."""
+    n = load_library().qsg_quantize_int8_workspace(rows, cols)
+    if n < 0:
+        _check(n)
+    return n
+
+
+def qsg_quantize_int8(x, q=None, s=None, qt=None, st=None, workspace=None, stream=None):
+    """INT8 copies of x (rows x cols): row-wise q (int8) with one fp32 scale for
+    each row in s, and / or transposed qt (cols x rows) with one for each column
+    in st, for which workspace holds qsg_quantize_int8_workspace(rows, cols)
+    bytes."""
+    px, rows, cols, ld = _rows(x, "x")
+    dt = _float_code(x)[0]
+    pq, ps = _pair(q, rows * cols, "q", s, rows, "s")
+    pqt, pst = _pair(qt, rows * cols, "qt", st, cols, "st")
+    pw = None if qt is None else _workspace(workspace, qsg_quantize_int8_workspace(rows, cols))
+    _here(x, q, s, qt, st, workspace)
+    _check(load_library().qsg_quantize_int8(px, dt, rows, cols, ld, pq, ps, pqt, pst, pw, _stream(stream)))
+
+
+def qsg_gemm_int8(a, sa, b, sb, c, bias=None, stream=None):
+    """C (M x N) = (A B^T) sa[:, None] sb (+ bias): A is M x K and B is N x K
+    (int8), sa (M) and sb (N) fp32 scales, bias N values of fp32 or bf16."""
+    pa, M, K, lda = _codes(a, "A")
+    pb, N, Kb, ldb = _codes(b, "B")
+    if Kb != K:
+        raise QsgError(f"K mismatch: A has {K}, B has {Kb}")
+    pc, Mc, Nc, ldc = _rows(c, "C")
+    if (Mc, Nc) != (M, N):
+        raise QsgError(f"C is {Mc}x{Nc}, expected {M}x{N}")
+    ct = _float_code(c)[0]
+    psa, psb = _dense(sa, "sa", M, "f32"), _dense(sb, "sb", N, "f32")
+    pbias, bt = None, 0
+    if bias is not None:
+        bt, bname = _float_code(bias)
+        pbias = _dense(bias, "bias", N, bname)
+    _here(a, sa, b, sb, c, bias)
+    _check(load_library().qsg_gemm_int8(pa, psa, pb, psb, M, N, K, lda, ldb, pbias, bt, pc, ct, ldc, _stream(stream)))
+
+
+def qsg_wgrad_int8(dy, q, s, c, accumulate=False, stream=None):
+    """C (N x K) = dY^T bf16(q s[:, None]), or C += for an fp32 C: dY T x N
+    (bf16), q T x K (int8) with T fp32 scales in s."""
+    pdy, T, N, lddy = _rows(dy, "dY")
+    if _dtype_code(dy) != BF16:
+        raise QsgError("qsg_wgrad_int8 takes a bf16 dY")
+    pq, Tq, K, ldq = _codes(q, "q")
+    if Tq != T:
+        raise QsgError(f"token count mismatch: dY has {T}, q has {Tq}")
+    pc, Nc, Kc, ldc = _rows(c, "C")
+    if (Nc, Kc) != (N, K):
+        raise QsgError(f"C is {Nc}x{Kc}, expected {N}x{K}")
+    ct = _float_code(c)[0]
+    ps = _dense(s, "s", T, "f32")
+    _here(dy, q, s, c)
+    _check(load_library().qsg_wgrad_int8(pdy, T, N, lddy, pq, ps, K, ldq, pc, ct, ldc, 1 if accumulate else 0,
+                                         _stream(stream)))
+
+
+def _gate_and_up(t, name):
+    p, rows, both, ld = _rows(t, name)
+    if both % 2:
+        raise QsgError(f"{name} has {both} columns: those of g, then as many of u are expected")
+    return p, rows, both // 2, ld
+
+
+def qsg_swiglu_int8_store_fwd(gu, a=None, aq=None, sa=None, ck=None, cs=None, stream=None):
+    """a = silu(g) u of gu = [g, u] (rows x 2 cols): a (rows x cols, the type of
+    gu) and / or its INT8 copy (aq, sa as qsg_quantize_int8); ck (rows x 2 cols,
+    int8) and cs (rows x 2 ceil(cols / 128)) keep g and u for backward."""
+    p, rows, cols, ld = _gate_and_up(gu, "gu")
+    dt, dname = _float_code(gu)
+    pa = None if a is None else _dense(a, "a", rows * cols, dname)
+    paq, psa = _pair(aq, rows * cols, "aq", sa, rows, "sa")
+    pck, pcs = _pair(ck, rows * 2 * cols, "ck", cs, rows * 2 * -(-cols // 128), "cs")
+    _here(gu, a, aq, sa, ck, cs)
+    _check(load_library().qsg_swiglu_int8_store_fwd(p, dt, rows, cols, ld, pa, paq, psa, pck, pcs, _stream(stream)))
+
+
+def qsg_swiglu_int8_store_bwd(da, ck, cs, dgu, a=None, stream=None):
+    """dgu = [dg, du] (rows x 2 cols) from da (rows x cols) and what the forward
+    pass kept; a (rows x cols) is computed again on request.  One type for da,
+    dgu and a."""
+    p, rows, cols, ldda = _rows(da, "da")
+    dt, dname = _float_code(da)
+    po, lddgu = _same_matrix(dgu, "dgu", (rows, 2 * cols), da.dtype)
+    if po is None:
+        raise QsgError("dgu is required")
+    pck = _dense(ck, "ck", rows * 2 * cols, "i8")
+    pcs = _dense(cs, "cs", rows * 2 * -(-cols // 128), "f32")
+    pa = None if a is None else _dense(a, "a", rows * cols, dname)
+    _here(da, ck, cs, dgu, a)
+    _check(load_library().qsg_swiglu_int8_store_bwd(p, dt, rows, cols, ldda, pck, pcs, po, lddgu, pa, _stream(stream)))

@@ -52,6 +52,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));  // 8 bytes at any address
 
 constexpr int WT = 256;    // output tile (features of dY x features of X)
 constexpr int BT = 64;     // tokens per K step
@@ -65,6 +66,8 @@ struct Bf16Args {
   bool vec;         // 16-byte loads of both operands
   bool out_bf16;
   bool accumulate;  // fp32 C only
+  const int8_t* q;  // INT8 X: its codes (leading dimension ldx) and a scale for
+  const float* qs;  // each token, in place of x
 };
 
 // chunk c of row f at position c ^ ((f >> 1) & 7): 16 lanes reading one chunk
@@ -92,6 +95,42 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
   }
 }
 
+// The same of INT8 codes: r[i] holds a token's 8 codes and its scale.
+__device__ __forceinline__ void load_block_int8(const int8_t* p, const float* qs, int64_t ld, int64_t t0, int64_t f0,
+                                                int64_t T, int64_t F, u32x4 (&r)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t t = t0 + i;
+    u32x2 w = {0u, 0u};
+    uint32_t s = 0u;
+    if (t < T) {
+      const int8_t* at = p + t * ld + f0;
+      s = __float_as_uint(qs[t]);
+      if (f0 + 8 <= F) {
+        w = *reinterpret_cast<const u32x2_b*>(at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (f0 + e < F) w[e >> 2] |= (uint32_t)(uint8_t)at[e] << (8 * (e & 3));
+      }
+    }
+    r[i] = u32x4{w.x, w.y, s, 0u};
+  }
+}
+// Codes times their token's scale, rounded to bf16: what the codes stand for.
+__device__ __forceinline__ void widen_block_int8(u32x4 (&r)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = __uint_as_float(r[i].z);
+    const uint32_t w[2] = {r[i].x, r[i].y};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t c = w[k >> 1] >> (16 * (k & 1));
+      r[i][k] = pack_bf16x2((float)(int8_t)c * s, (float)(int8_t)(c >> 8) * s);
+    }
+  }
+}
+
 // Transpose the 8 x 8 block (r[token] = 8 features) and store feature rows:
 // row (frow + j) gets the 8 tokens of feature j as chunk `chunk`.
 __device__ __forceinline__ void store_block_t(uint8_t* lds, int frow, int chunk, const u32x4 (&r)[8]) {
@@ -106,6 +145,8 @@ __device__ __forceinline__ void store_block_t(uint8_t* lds, int frow, int chunk,
   }
 }
 
+// X8: X is INT8, widened where its block goes to LDS
+template <bool X8>
 __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   // two stages: step s writes stage s & 1 while slower waves may still read
   // the other, so one barrier per step suffices
@@ -126,6 +167,16 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   const int wn = wave >> 1, wk = wave & 1;
 
   const int64_t nsteps = (g.T + BT - 1) / BT;
+  auto load = [&](int64_t t0, u32x4 (&r)[8]) {
+    if (X8 && is_b)
+      load_block_int8(g.q, g.qs, ld, t0, fbase, g.T, F, r);
+    else
+      load_block(src, ld, t0, fbase, g.T, F, g.vec, r);
+  };
+  auto store = [&](uint8_t* lds, int chunk, u32x4 (&r)[8]) {
+    if (X8 && is_b) widen_block_int8(r);
+    store_block_t(lds, fg * 8, chunk, r);
+  };
   v16f acc[4][4];
   // One K step s, on the block already in LDS stage s & 1: the block of step
   // s + 1 (registers RN) is transposed into the other stage and the block of
@@ -139,12 +190,12 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   auto step = [&](u32x4 (&RN)[2][8], u32x4 (&RF)[2][8], int64_t s, auto first, auto stage) {
     constexpr int ST = decltype(stage)::value;
     if (s + 1 < nsteps) {
-      store_block_t(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], fg * 8, tg, RN[0]);
-      store_block_t(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], fg * 8, tg + 4, RN[1]);
+      store(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], tg, RN[0]);
+      store(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], tg + 4, RN[1]);
     }
     if (s + 2 < nsteps) {
-      load_block(src, ld, (s + 2) * BT + tg * 8, fbase, g.T, F, g.vec, RF[0]);
-      load_block(src, ld, (s + 2) * BT + (tg + 4) * 8, fbase, g.T, F, g.vec, RF[1]);
+      load((s + 2) * BT + tg * 8, RF[0]);
+      load((s + 2) * BT + (tg + 4) * 8, RF[1]);
     }
 #pragma unroll
     for (int ks = 0; ks < BT / 16; ++ks) {
@@ -190,14 +241,14 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   }
   // two register blocks in flight: even steps' blocks in r0, odd steps' in r1
   u32x4 r0[2][8], r1[2][8];
-  load_block(src, ld, (int64_t)tg * 8, fbase, g.T, F, g.vec, r0[0]);
-  load_block(src, ld, (int64_t)(tg + 4) * 8, fbase, g.T, F, g.vec, r0[1]);
+  load((int64_t)tg * 8, r0[0]);
+  load((int64_t)(tg + 4) * 8, r0[1]);
   if (nsteps > 1) {
-    load_block(src, ld, BT + (int64_t)tg * 8, fbase, g.T, F, g.vec, r1[0]);
-    load_block(src, ld, BT + (int64_t)(tg + 4) * 8, fbase, g.T, F, g.vec, r1[1]);
+    load(BT + (int64_t)tg * 8, r1[0]);
+    load(BT + (int64_t)(tg + 4) * 8, r1[1]);
   }
-  store_block_t(is_b ? lds_b[0] : lds_a[0], fg * 8, tg, r0[0]);
-  store_block_t(is_b ? lds_b[0] : lds_a[0], fg * 8, tg + 4, r0[1]);
+  store(is_b ? lds_b[0] : lds_a[0], tg, r0[0]);
+  store(is_b ? lds_b[0] : lds_a[0], tg + 4, r0[1]);
   __syncthreads();
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
@@ -509,7 +560,20 @@ void launch_wgrad_bf16(const void* dy, int64_t T, int64_t N, int64_t lddy, const
   if (dma)
     hipLaunchKernelGGL(gemm_wgrad_bf16_dma_kernel, dim3(grid.x * grid.y), dim3(256), 0, st, g);
   else
-    hipLaunchKernelGGL(gemm_wgrad_bf16_kernel, grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL(gemm_wgrad_bf16_kernel<false>, grid, dim3(256), 0, st, g);
+}
+
+void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
+                       int64_t ldq, void* c, int c_dtype, int64_t ldc, bool accumulate, hipStream_t st) {
+  Bf16Args g{};
+  g.dy = reinterpret_cast<const uint16_t*>(dy);
+  g.q = q; g.qs = s;
+  g.T = T; g.N = N; g.K = K; g.lddy = lddy; g.ldx = ldq; g.ldc = ldc; g.c = c;
+  g.vec = (uintptr_t)dy % 16 == 0 && lddy % 8 == 0;
+  g.out_bf16 = c_dtype == QSG_BF16;
+  g.accumulate = accumulate && !g.out_bf16;
+  const dim3 grid((unsigned)((K + WT - 1) / WT), (unsigned)((N + WT - 1) / WT));
+  hipLaunchKernelGGL(gemm_wgrad_bf16_kernel<true>, grid, dim3(256), 0, st, g);
 }
 
 }  // namespace qsg

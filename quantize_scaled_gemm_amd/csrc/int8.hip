@@ -1,0 +1,586 @@
+// INT8 copies of a matrix and the gated activation that keeps its input in
+// INT8 for the backward pass.
+//
+// Values whose largest magnitude is amax share a scale:
+//   s = max(fp32(amax / 127), 2^-126)   (1 for amax 0, NaN for one not finite)
+//   code = rint(fp32(v * fp32(1 / s))), and a code stands for code * s.
+// A row (a token) shares one, a column (a channel) of the transposed copy, or
+// a block of 128 neighbours of the kept activations.
+#include <hip/hip_runtime.h>
+
+#include "qsg_device.h"
+#include "qsg_internal.h"
+
+namespace qsg {
+
+namespace {
+
+// Vectors that ask for the alignment of an element only: gfx950 loads and
+// stores them at any address, so odd leading dimensions take the same path.
+typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
+
+constexpr int kBlock = 128;  // neighbours that share a scale of the kept activations
+
+__device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float widen(float v) { return v; }
+
+// 8 consecutive values, of which the first n (0..8) are there; the rest are 0.
+__device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p, int n) {
+  if (n >= 8) {
+    const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? widen(p[i]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void load8(float (&v)[8], const float* p, int n) {
+  if (n >= 8) {
+    const u32x4 a = *reinterpret_cast<const u32x4_e*>(p), b = *reinterpret_cast<const u32x4_e*>(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8], int n) {
+  const u32x4 u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  if (n >= 8) {
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_e*>(p));
+  } else {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int n) {
+  if (n >= 8) {
+    const u32x4 a = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    const u32x4 b = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    *reinterpret_cast<u32x4_e*>(p) = a;
+    *reinterpret_cast<u32x4_e*>(p + 4) = b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store8(int8_t* p, u32x2 c, int n) {
+  if (n >= 8) {
+    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_b*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = (int8_t)(c[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// how many of the 8 values from c on are inside a row
+__device__ __forceinline__ int left8(int64_t cols, int64_t c) {
+  const int64_t n = cols - c;
+  return n < 0 ? 0 : (n < 8 ? (int)n : 8);
+}
+
+// largest magnitude as a bit pattern: infinity and every NaN are larger than
+// any finite one
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = umax_u32(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+struct Scale {
+  float s, inv;
+  uint32_t keep;  // 0 where the codes are 0 because the maximum is not finite
+};
+__device__ __forceinline__ Scale scale_of(uint32_t amax) {
+  Scale r;
+  r.keep = amax < 0x7F800000u ? ~0u : 0u;
+  const float q = __fdiv_rn(__uint_as_float(amax), 127.0f);
+  r.s = amax == 0 ? 1.0f : fmaxf(q, 0x1p-126f);
+  r.inv = __fdiv_rn(1.0f, r.s);
+  if (!r.keep) {
+    r.s = __uint_as_float(0x7FC00000u);
+    r.inv = 0.0f;
+  }
+  return r;
+}
+// the same of a scale that is in memory
+__device__ __forceinline__ Scale scale_again(float s) {
+  Scale r;
+  r.s = s;
+  r.keep = s == s ? ~0u : 0u;
+  r.inv = r.keep ? __fdiv_rn(1.0f, s) : 0.0f;
+  return r;
+}
+
+// rint(fp32(v * inv)) in the low byte: adding 1.5 * 2^23 rounds to a whole
+// number, ties to even, whose two's complement is the sum's lowest bits (the
+// product and the sum are rounded apart, so they may not become one fma)
+__device__ __forceinline__ uint32_t code_of(float v, float inv) {
+#pragma clang fp contract(off)
+  const float p = v * inv;
+  return __float_as_uint(p + 12582912.0f);
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const Scale& s) {
+  const uint32_t lo = __builtin_amdgcn_perm(code_of(b, s.inv), code_of(a, s.inv), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(code_of(d, s.inv), code_of(c, s.inv), 0x04000c0cu);
+  return (lo | hi) & s.keep;
+}
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], const Scale& s) {
+  return u32x2{codes4(v[0], v[1], v[2], v[3], s), codes4(v[4], v[5], v[6], v[7], s)};
+}
+
+// Maximum over the TPR threads (consecutive ones of the workgroup) that share
+// a row.  For TPR > 64 every thread of the workgroup calls it together.
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
+  if constexpr (TPR < 64) {
+    static_assert(TPR == 16, "groups of a row of lanes");
+    return group_max_u32<0xF>(m);
+  } else {
+    m = wave_max_u32(m);
+    if constexpr (TPR > 64) {
+      constexpr int W = TPR / 64;
+      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+      __syncthreads();
+      red += threadIdx.x / TPR * W;
+      m = red[0];
+#pragma unroll
+      for (int i = 1; i < W; ++i) m = umax_u32(m, red[i]);
+    }
+    return m;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// row-wise copy
+// ---------------------------------------------------------------------------
+struct QuantArgs {
+  const void* x;
+  int64_t rows, cols, ld;
+  int8_t* q;   // or null
+  float* s;
+  int8_t* qt;  // or null
+  float* st;
+  float* part;  // column maxima of groups of rows
+  int parts;
+  int64_t tile0;  // first tile of a launch of int8_col_kernel
+};
+
+// A row in the registers of TPR threads, CH chunks of 8 values each.
+template <typename In, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_row_kernel(QuantArgs a) {
+  constexpr int NT = TPR < 256 ? 256 : TPR;
+  __shared__ uint32_t red[NT / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
+  const bool there = row < a.rows;
+  const In* x = reinterpret_cast<const In*>(a.x) + (there ? row * a.ld : 0);
+  const int cols = there ? (int)a.cols : 0;
+  float v[CH][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) load8(v[i], x + (i * TPR + t) * 8, cols - (i * TPR + t) * 8);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) m = amax8(v[i], m);
+  const Scale s = scale_of(row_max<TPR>(m, red));
+  if (!there) return;
+  int8_t* q = a.q + row * a.cols;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) store8(q + (i * TPR + t) * 8, codes8(v[i], s), cols - (i * TPR + t) * 8);
+  if (t == 0) a.s[row] = s.s;
+}
+
+// Rows that are too long for registers are read twice.
+template <typename In>
+__global__ __launch_bounds__(1024) void int8_long_row_kernel(QuantArgs a) {
+  __shared__ uint32_t red[16];
+  const In* x = reinterpret_cast<const In*>(a.x) + (int64_t)blockIdx.x * a.ld;
+  int8_t* q = a.q + (int64_t)blockIdx.x * a.cols;
+  float v[8];
+  uint32_t m = 0;
+  for (int64_t c = threadIdx.x * 8; c < a.cols; c += 8192) {
+    load8(v, x + c, left8(a.cols, c));
+    m = amax8(v, m);
+  }
+  const Scale s = scale_of(row_max<1024>(m, red));
+  for (int64_t c = threadIdx.x * 8; c < a.cols; c += 8192) {
+    const int n = left8(a.cols, c);
+    load8(v, x + c, n);
+    store8(q + c, codes8(v, s), n);
+  }
+  if (threadIdx.x == 0) a.s[blockIdx.x] = s.s;
+}
+
+// ---------------------------------------------------------------------------
+// transposed copy: the columns' maxima, their scales, the codes
+// ---------------------------------------------------------------------------
+constexpr int kMostParts = 512;
+
+// Maxima of 512 columns over a part of the rows: a wave reads a row's 512
+// columns at a time, the waves take rows in turn.
+template <typename In>
+__global__ __launch_bounds__(256) void int8_colmax_kernel(QuantArgs a) {
+  __shared__ uint32_t red[4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 512 + lane * 8;
+  const int n = left8(a.cols, c);
+  uint32_t m[8] = {};
+  for (int64_t r = (int64_t)blockIdx.y * 4 + wave; r < a.rows; r += (int64_t)a.parts * 4) {
+    float v[8];
+    load8(v, reinterpret_cast<const In*>(a.x) + r * a.ld + c, n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = umax_u32(m[i], __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[wave][lane * 8 + i] = m[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int64_t col = (int64_t)blockIdx.x * 512 + i;
+    if (col < a.cols)
+      reinterpret_cast<uint32_t*>(a.part)[(int64_t)blockIdx.y * a.cols + col] =
+          umax_u32(umax_u32(red[0][i], red[1][i]), umax_u32(red[2][i], red[3][i]));
+  }
+}
+
+// 64 columns a workgroup, 4 waves over the parts
+__global__ __launch_bounds__(256) void int8_colscale_kernel(QuantArgs a) {
+  __shared__ uint32_t red[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  uint32_t m = 0;
+  if (col < a.cols)
+    for (int p = wave; p < a.parts; p += 4)
+      m = umax_u32(m, reinterpret_cast<const uint32_t*>(a.part)[(int64_t)p * a.cols + col]);
+  red[wave][lane] = m;
+  __syncthreads();
+  if (wave == 0 && col < a.cols)
+    a.st[col] = scale_of(umax_u32(umax_u32(red[0][lane], red[1][lane]), umax_u32(red[2][lane], red[3][lane]))).s;
+}
+
+// A tile of 128 rows x 64 columns: a thread encodes 4 rows x 8 columns and
+// puts each column's 4 codes into LDS as one word; a column's 128 codes then
+// leave as one run of 8 lanes.
+constexpr int kColRow = 33;  // words of an LDS column: 32, and one that spreads the banks
+template <typename In>
+__global__ __launch_bounds__(256) void int8_col_kernel(QuantArgs a) {
+  __shared__ uint32_t tile[64 * kColRow];
+  const int64_t tile_rows = (a.rows + 127) / 128, at = a.tile0 + blockIdx.x;
+  const int64_t r0 = at % tile_rows * 128, c0 = at / tile_rows * 64;
+  const int ch = threadIdx.x & 7, rg = threadIdx.x >> 3;
+  const int64_t c = c0 + ch * 8;
+  const int n = left8(a.cols, c);
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + rg * 4 + i;
+    load8(v[i], reinterpret_cast<const In*>(a.x) + (r < a.rows ? r * a.ld : 0) + c, r < a.rows ? n : 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k < n) {
+      const Scale s = scale_again(a.st[c + k]);
+      tile[(ch * 8 + k) * kColRow + rg] = codes4(v[0][k], v[1][k], v[2][k], v[3][k], s);
+    }
+  }
+  __syncthreads();
+  const int64_t r = r0 + (threadIdx.x & 7) * 16;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int col = (threadIdx.x >> 3) + k * 32;
+    if (c0 + col >= a.cols || r >= a.rows) continue;
+    const uint32_t* w = tile + col * kColRow + (threadIdx.x & 7) * 4;
+    int8_t* p = a.qt + (c0 + col) * a.rows + r;
+    if (r + 16 <= a.rows) {
+      const u32x4 u = {w[0], w[1], w[2], w[3]};
+      *reinterpret_cast<u32x4_b*>(p) = u;
+    } else {
+      const int left = (int)(a.rows - r);
+      for (int i = 0; i < left; ++i) p[i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+  }
+}
+
+// The threads of a launch are counted in 32 bits: what has more workgroups than
+// this is launched in pieces.
+constexpr int64_t kMostGroups = 1 << 21;
+
+// f(first row, rows of the launch), with `per` rows to a workgroup
+template <typename F>
+void in_pieces(int64_t rows, int64_t per, F f) {
+  for (int64_t r = 0; r < rows; r += kMostGroups * per) f(r, rows - r < kMostGroups * per ? rows - r : kMostGroups * per);
+}
+
+template <typename In, int TPR, int CH>
+void launch_rows(const QuantArgs& all, hipStream_t st) {
+  constexpr int NT = TPR < 256 ? 256 : TPR, PER = NT / TPR;
+  in_pieces(all.rows, PER, [&](int64_t r, int64_t n) {
+    QuantArgs a = all;
+    a.x = reinterpret_cast<const In*>(all.x) + r * all.ld;
+    a.q += r * all.cols;
+    a.s += r;
+    a.rows = n;
+    if constexpr (CH > 0)
+      hipLaunchKernelGGL((int8_row_kernel<In, TPR, CH>), dim3((unsigned)((n + PER - 1) / PER)), dim3(NT), 0, st, a);
+    else
+      hipLaunchKernelGGL(int8_long_row_kernel<In>, dim3((unsigned)n), dim3(NT), 0, st, a);
+  });
+}
+
+template <typename In>
+void launch_quantize(const QuantArgs& a, hipStream_t st) {
+  // by the scales: an empty copy may have no address
+  if (a.s) {
+    if (a.cols <= 256) launch_rows<In, 16, 2>(a, st);
+    else if (a.cols <= 1024) launch_rows<In, 64, 2>(a, st);
+    else if (a.cols <= 2048) launch_rows<In, 64, 4>(a, st);
+    else if (a.cols <= 4096) launch_rows<In, 256, 2>(a, st);
+    else if (a.cols <= 8192) launch_rows<In, 256, 4>(a, st);
+    else if (a.cols <= 16384) launch_rows<In, 512, 4>(a, st);
+    else if (a.cols <= 32768) launch_rows<In, 1024, 4>(a, st);
+    else launch_rows<In, 1024, 0>(a, st);
+  }
+  if (a.st && a.cols > 0) {
+    if (a.rows > 0)
+      hipLaunchKernelGGL(int8_colmax_kernel<In>, dim3((unsigned)((a.cols + 511) / 512), a.parts), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(int8_colscale_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(256), 0, st, a);
+    in_pieces((a.rows + 127) / 128 * ((a.cols + 63) / 64), 1, [&](int64_t t, int64_t n) {
+      QuantArgs b = a;
+      b.tile0 = t;
+      hipLaunchKernelGGL(int8_col_kernel<In>, dim3((unsigned)n), dim3(256), 0, st, b);
+    });
+  }
+}
+
+int quantize_parts(int64_t rows) { return (int)(rows < kMostParts ? rows : kMostParts); }
+
+// ---------------------------------------------------------------------------
+// gated activation
+// ---------------------------------------------------------------------------
+struct GluArgs {
+  const void* x;  // forward: gu; backward: da
+  int64_t rows, cols, ld;
+  int64_t nb;     // blocks of 128 in a row of g
+  void* a;        // dense, or null
+  int8_t* aq;     // forward
+  float* sa;
+  int8_t* ck;     // forward: out or null; backward: in
+  float* cs;
+  void* dgu;      // backward
+  int64_t lddgu;
+};
+
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
+}
+
+// Codes and scale of one block, held by 16 neighbouring lanes.
+__device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* ck, float* cs, int n, bool first) {
+  const Scale s = scale_of(group_max_u32<0xF>(amax8(v, 0)));
+  store8(ck, codes8(v, s), n);
+  if (first) *cs = s.s;
+}
+
+// One block of 128 of g and of u to 16 neighbouring lanes, 8 values of both
+// each; groups of lanes take the blocks of the matrix in turn.
+template <typename In>
+__global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
+  const int t = threadIdx.x & 15;
+  const int64_t units = a.rows * a.nb, stride = (int64_t)gridDim.x * 16;
+  for (int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); unit < units; unit += stride) {
+    const int64_t row = unit / a.nb, b = unit - row * a.nb;
+    const int64_t c = b * kBlock + t * 8;
+    const int n = left8(a.cols, c);
+    const In* x = reinterpret_cast<const In*>(a.x) + row * a.ld + c;
+    float g[8], u[8];
+    load8(g, x, n);
+    load8(u, x + a.cols, n);
+    if (a.ck) {
+      int8_t* ck = a.ck + row * 2 * a.cols + c;
+      float* cs = a.cs + row * 2 * a.nb + b;
+      keep_block(g, ck, cs, n, t == 0);
+      keep_block(u, ck + a.cols, cs + a.nb, n, t == 0);
+    }
+    if (a.a) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
+      store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, g, n);
+    }
+  }
+}
+
+// With an INT8 copy of a: a row to a workgroup, which holds a in registers (CH
+// > 0, CH chunks of 8 a thread) or computes it twice (CH == 0).
+template <typename In, int NT, int CH>
+__global__ __launch_bounds__(NT) void swiglu_row_kernel(GluArgs a) {
+  __shared__ uint32_t red[NT / 64];
+  const int64_t row = blockIdx.x;
+  const In* x = reinterpret_cast<const In*>(a.x) + row * a.ld;
+  float h[CH ? CH : 1][8];
+  uint32_t m = 0;
+  // chunk k of the row: its blocks, a, and a's maximum
+  auto chunk = [&](int64_t k, float (&o)[8], bool first_time) {
+    const int64_t c = k * 8;
+    const int n = left8(a.cols, c);
+    float g[8], u[8];
+    load8(g, x + c, n);
+    load8(u, x + a.cols + c, n);
+    if (first_time && a.ck && k / 16 < a.nb) {
+      int8_t* ck = a.ck + row * 2 * a.cols + c;
+      float* cs = a.cs + row * 2 * a.nb + k / 16;
+      keep_block(g, ck, cs, n, (k & 15) == 0);
+      keep_block(u, ck + a.cols, cs + a.nb, n, (k & 15) == 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
+    if (first_time) {
+      m = amax8(o, m);
+      if (a.a) store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, o, n);
+    }
+    return n;
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) chunk(i * NT + threadIdx.x, h[i], true);
+  } else {
+    for (int64_t k = threadIdx.x; k * 8 < (a.cols + kBlock - 1) / kBlock * kBlock; k += NT) chunk(k, h[0], true);
+  }
+  const Scale s = scale_of(row_max<NT>(m, red));
+  int8_t* aq = a.aq + row * a.cols;
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int64_t c = ((int64_t)i * NT + threadIdx.x) * 8;
+      store8(aq + c, codes8(h[i], s), left8(a.cols, c));
+    }
+  } else {
+    for (int64_t k = threadIdx.x; k * 8 < a.cols; k += NT) {
+      const int n = chunk(k, h[0], false);
+      store8(aq + k * 8, codes8(h[0], s), n);
+    }
+  }
+  if (threadIdx.x == 0) a.sa[row] = s.s;
+}
+
+// 8 codes times their scale
+__device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, float s, int n) {
+  if (n >= 8) {
+    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_b*>(p));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))) * s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] * s : 0.0f;
+  }
+}
+
+template <typename In>
+__global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
+  const int t = threadIdx.x & 15;
+  const int64_t units = a.rows * a.nb, stride = (int64_t)gridDim.x * 16;
+  for (int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); unit < units; unit += stride) {
+    const int64_t row = unit / a.nb, b = unit - row * a.nb;
+    const int64_t c = b * kBlock + t * 8;
+    const int n = left8(a.cols, c);
+    const float* cs = a.cs + row * 2 * a.nb + b;
+    const int8_t* ck = a.ck + row * 2 * a.cols + c;
+    float d[8], g[8], u[8], h[8];
+    load8(d, reinterpret_cast<const In*>(a.x) + row * a.ld + c, n);
+    load_codes(g, ck, cs[0], n);
+    load_codes(u, ck + a.cols, cs[a.nb], n);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = sigmoid(g[i]), w = g[i] * p;  // silu(g)
+      const float du = d[i] * w;
+      g[i] = d[i] * u[i] * (p * (1.0f + g[i] * (1.0f - p)));
+      h[i] = w * u[i];
+      u[i] = du;
+    }
+    In* o = reinterpret_cast<In*>(a.dgu) + row * a.lddgu + c;
+    store8(o, g, n);
+    store8(o + a.cols, u, n);
+    if (a.a) store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, h, n);
+  }
+}
+
+unsigned glu_grid(const GluArgs& a) {
+  const int64_t need = (a.rows * a.nb + 15) / 16, most = (int64_t)256 * 32;
+  return (unsigned)(need < most ? need : most);
+}
+
+template <typename In, int NT, int CH>
+void launch_glu_row(const GluArgs& all, hipStream_t st) {
+  in_pieces(all.rows, 1, [&](int64_t r, int64_t n) {
+    GluArgs a = all;
+    a.x = reinterpret_cast<const In*>(all.x) + r * all.ld;
+    if (all.a) a.a = reinterpret_cast<In*>(all.a) + r * all.cols;
+    a.aq += r * all.cols;
+    a.sa += r;
+    if (all.ck) {
+      a.ck += r * 2 * all.cols;
+      a.cs += r * 2 * all.nb;
+    }
+    hipLaunchKernelGGL((swiglu_row_kernel<In, NT, CH>), dim3((unsigned)n), dim3(NT), 0, st, a);
+  });
+}
+
+template <typename In>
+void launch_glu_fwd(const GluArgs& a, hipStream_t st) {
+  if (a.sa) {  // an empty copy may have no address
+    if (a.cols <= 2048) launch_glu_row<In, 256, 1>(a, st);
+    else if (a.cols <= 8192) launch_glu_row<In, 512, 2>(a, st);
+    else if (a.cols <= 16384) launch_glu_row<In, 512, 4>(a, st);
+    else if (a.cols <= 32768) launch_glu_row<In, 1024, 4>(a, st);
+    else launch_glu_row<In, 1024, 0>(a, st);
+  } else if (a.rows > 0 && a.cols > 0) {
+    hipLaunchKernelGGL(swiglu_fwd_kernel<In>, dim3(glu_grid(a)), dim3(256), 0, st, a);
+  }
+}
+
+}  // namespace
+
+int64_t quantize_int8_workspace(int64_t rows, int64_t cols) { return 4 * cols * quantize_parts(rows); }
+
+void launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* s,
+                          int8_t* qt, float* st_, void* workspace, hipStream_t st) {
+  QuantArgs a{};
+  a.x = x; a.rows = rows; a.cols = cols; a.ld = ld;
+  a.q = q; a.s = s; a.qt = qt; a.st = st_;
+  a.part = reinterpret_cast<float*>(workspace);
+  a.parts = quantize_parts(rows);
+  if (dtype == QSG_BF16) launch_quantize<uint16_t>(a, st);
+  else launch_quantize<float>(a, st);
+}
+
+void launch_swiglu_int8_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* out, int8_t* aq,
+                            float* sa, int8_t* ck, float* cs, hipStream_t st) {
+  GluArgs a{};
+  a.x = gu; a.rows = rows; a.cols = cols; a.ld = ld;
+  a.nb = (cols + kBlock - 1) / kBlock;
+  a.a = out; a.aq = aq; a.sa = sa; a.ck = ck; a.cs = cs;
+  if (dtype == QSG_BF16) launch_glu_fwd<uint16_t>(a, st);
+  else launch_glu_fwd<float>(a, st);
+}
+
+void launch_swiglu_int8_bwd(const void* da, int dtype, int64_t rows, int64_t cols, int64_t ldda, const int8_t* ck,
+                            const float* cs, void* dgu, int64_t lddgu, void* out, hipStream_t st) {
+  if (rows == 0 || cols == 0) return;
+  GluArgs a{};
+  a.x = da; a.rows = rows; a.cols = cols; a.ld = ldda;
+  a.nb = (cols + kBlock - 1) / kBlock;
+  a.a = out; a.ck = const_cast<int8_t*>(ck); a.cs = const_cast<float*>(cs);
+  a.dgu = dgu; a.lddgu = lddgu;
+  if (dtype == QSG_BF16) hipLaunchKernelGGL(swiglu_bwd_kernel<uint16_t>, dim3(glu_grid(a)), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(swiglu_bwd_kernel<float>, dim3(glu_grid(a)), dim3(256), 0, st, a);
+}
+
+}  // namespace qsg

@@ -348,6 +348,123 @@ int qsg_gemm_nvfp4(const uint8_t* a, const uint8_t* sa, const float* sdec_a_dev,
   return check_launch(fn);
 }
 
+static constexpr int64_t kMostInt8 = (int64_t)1 << 30;  // rows and columns of an INT8 copy
+
+int64_t qsg_quantize_int8_workspace(int64_t rows, int64_t cols) {
+  const char* fn = "qsg_quantize_int8_workspace";
+  if (rows < 0 || cols < 0) return fail(QSG_ERR_ARG, "%s: negative shape %lld x %lld", fn, (long long)rows, (long long)cols);
+  if (rows >= kMostInt8 || cols >= kMostInt8) return fail(QSG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^30", fn);
+  return qsg::quantize_int8_workspace(rows, cols);
+}
+
+int qsg_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* s,
+                      int8_t* qt, float* st, void* workspace, void* stream) {
+  const char* fn = "qsg_quantize_int8";
+  int rc = check_matrix(fn, x, dtype, rows, cols, ld);
+  if (rc) return rc;
+  if (rows >= kMostInt8 || cols >= kMostInt8) return fail(QSG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^30", fn);
+  const bool empty = rows == 0 || cols == 0;
+  if (!q && !qt && !s && !st && !empty) return fail(QSG_ERR_ARG, "%s: q and qt are both null", fn);
+  if (!empty && (!q != !s || !qt != !st)) return fail(QSG_ERR_ARG, "%s: codes and scales of a copy go together", fn);
+  if (!aligned(s, 4) || !aligned(st, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
+  if (!empty && qt) {
+    if (!workspace) return fail(QSG_ERR_ARG, "%s: the transposed copy needs a workspace", fn);
+    if (!aligned(workspace, 4)) return fail(QSG_ERR_ALIGN, "%s: workspace not 4-byte aligned", fn);
+  }
+  if ((q && (q == qt || (const void*)q == x)) || (qt && (const void*)qt == x) || (s && s == st))
+    return fail(QSG_ERR_ARG, "%s: an output overlaps another tensor", fn);
+  qsg::launch_quantize_int8(x, dtype, rows, cols, ld, q, s, qt, st, workspace, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N, int64_t K,
+                  int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype, int64_t ldc,
+                  void* stream) {
+  const char* fn = "qsg_gemm_int8";
+  if (!valid_dtype(c_dtype)) return fail(QSG_ERR_ARG, "%s: bad output dtype %d", fn, c_dtype);
+  if (bias && !valid_dtype(bias_dtype)) return fail(QSG_ERR_ARG, "%s: bad bias dtype %d", fn, bias_dtype);
+  if (M < 0 || N < 0 || K < 0) return fail(QSG_ERR_ARG, "%s: negative shape", fn);
+  // |code| <= 128, and 128^2 (2^17 - 1) is the largest sum that 32 bits hold
+  if (K > 131071) return fail(QSG_ERR_UNSUPPORTED, "%s: K %lld exceeds 131071, beyond which a sum may not fit 32 bits", fn, (long long)K);
+  if (M > (1 << 26) || N > (1 << 26)) return fail(QSG_ERR_UNSUPPORTED, "%s: M and N must be at most 2^26", fn);
+  if (M == 0 || N == 0) return QSG_OK;
+  if (((M + 127) / 128) * ((N + 127) / 128) > (1 << 23))
+    return fail(QSG_ERR_UNSUPPORTED, "%s: C has more than 2^23 tiles of 128 x 128", fn);
+  if (!c || !sa || !sb) return fail(QSG_ERR_ARG, "%s: null C or scales", fn);
+  if (ldc < N) return fail(QSG_ERR_ARG, "%s: ldc < N", fn);
+  if (!aligned(c, esize(c_dtype))) return fail(QSG_ERR_ALIGN, "%s: C not aligned to its element size", fn);
+  if (!aligned(sa, 4) || !aligned(sb, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
+  if (bias && !aligned(bias, esize(bias_dtype))) return fail(QSG_ERR_ALIGN, "%s: bias not aligned to its element size", fn);
+  if (K > 0) {
+    if (!a || !b) return fail(QSG_ERR_ARG, "%s: null operand", fn);
+    if (lda < K || ldb < K) return fail(QSG_ERR_ARG, "%s: lda/ldb < K", fn);
+  }
+  if (c == (const void*)a || c == (const void*)b) return fail(QSG_ERR_ARG, "%s: C overlaps an operand", fn);
+  qsg::launch_gemm_int8(a, sa, b, sb, M, N, K, lda, ldb, bias, bias_dtype, c, c_dtype, ldc, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
+                   int64_t ldq, void* c, int c_dtype, int64_t ldc, int accumulate, void* stream) {
+  const char* fn = "qsg_wgrad_int8";
+  if (!valid_dtype(c_dtype)) return fail(QSG_ERR_ARG, "%s: bad output dtype %d", fn, c_dtype);
+  if (T < 0 || N < 0 || K < 0) return fail(QSG_ERR_ARG, "%s: negative shape", fn);
+  if (accumulate && c_dtype != QSG_F32) return fail(QSG_ERR_UNSUPPORTED, "%s: accumulation needs an fp32 C", fn);
+  if (N == 0 || K == 0) return QSG_OK;
+  if (N > 65535 * 256LL || K > (1 << 26)) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 65535 x 2^18 tiles of 256 x 256", fn);
+  if (!c) return fail(QSG_ERR_ARG, "%s: null C", fn);
+  if (ldc < K) return fail(QSG_ERR_ARG, "%s: ldc < K", fn);
+  if (!aligned(c, esize(c_dtype))) return fail(QSG_ERR_ALIGN, "%s: C not aligned to its element size", fn);
+  if (T > 0) {
+    if (!dy || !q || !s) return fail(QSG_ERR_ARG, "%s: null operand", fn);
+    if (lddy < N || ldq < K) return fail(QSG_ERR_ARG, "%s: lddy < N or ldq < K", fn);
+    if (!aligned(dy, 2)) return fail(QSG_ERR_ALIGN, "%s: dy not aligned to 2 bytes", fn);
+    if (!aligned(s, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
+  }
+  qsg::launch_wgrad_int8(dy, T, N, lddy, q, s, K, ldq, c, c_dtype, ldc, accumulate != 0, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_swiglu_int8_store_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* a, int8_t* aq,
+                              float* sa, int8_t* ck, float* cs, void* stream) {
+  const char* fn = "qsg_swiglu_int8_store_fwd";
+  if (rows < 0 || cols < 0) return fail(QSG_ERR_ARG, "%s: negative shape %lld x %lld", fn, (long long)rows, (long long)cols);
+  if (rows >= kMostInt8 || cols >= kMostInt8) return fail(QSG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^30", fn);
+  int rc = check_matrix(fn, gu, dtype, rows, 2 * cols, ld);
+  if (rc) return rc;
+  const bool empty = rows == 0 || cols == 0;
+  if (!empty) {
+    if (!a && !aq && !ck) return fail(QSG_ERR_ARG, "%s: a, aq and ck are all null", fn);
+    if (!aq != !sa || !ck != !cs) return fail(QSG_ERR_ARG, "%s: codes and scales go together", fn);
+    if (a && !aligned(a, esize(dtype))) return fail(QSG_ERR_ALIGN, "%s: a not aligned to its element size", fn);
+    if (a == gu || (aq && (aq == ck || (const void*)aq == gu || (const void*)aq == a)) ||
+        (ck && ((const void*)ck == gu || (const void*)ck == a)) || (sa && sa == cs))
+      return fail(QSG_ERR_ARG, "%s: an output overlaps another tensor", fn);
+  }
+  if (!aligned(sa, 4) || !aligned(cs, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
+  if (empty && !sa) return QSG_OK;
+  qsg::launch_swiglu_int8_fwd(gu, dtype, rows, cols, ld, a, aq, sa, ck, cs, as_stream(stream));
+  return check_launch(fn);
+}
+
+int qsg_swiglu_int8_store_bwd(const void* da, int dtype, int64_t rows, int64_t cols, int64_t ldda, const int8_t* ck,
+                              const float* cs, void* dgu, int64_t lddgu, void* a, void* stream) {
+  const char* fn = "qsg_swiglu_int8_store_bwd";
+  int rc = check_matrix(fn, da, dtype, rows, cols, ldda);
+  if (rc) return rc;
+  if (rows >= kMostInt8 || cols >= kMostInt8) return fail(QSG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^30", fn);
+  if (rows == 0 || cols == 0) return QSG_OK;
+  if (!ck || !cs || !dgu) return fail(QSG_ERR_ARG, "%s: null pointer", fn);
+  if (lddgu < 2 * cols) return fail(QSG_ERR_ARG, "%s: lddgu %lld < 2 cols", fn, (long long)lddgu);
+  if (!aligned(cs, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
+  if (!aligned(dgu, esize(dtype)) || (a && !aligned(a, esize(dtype))))
+    return fail(QSG_ERR_ALIGN, "%s: dgu or a not aligned to its element size", fn);
+  if (dgu == da || a == da || a == dgu || dgu == (const void*)ck || a == (const void*)ck)
+    return fail(QSG_ERR_ARG, "%s: an output overlaps another tensor", fn);
+  qsg::launch_swiglu_int8_bwd(da, dtype, rows, cols, ldda, ck, cs, dgu, lddgu, a, as_stream(stream));
+  return check_launch(fn);
+}
+
 static constexpr int64_t kMostNormCols = 1 << 24;  // a column's index and a launch's threads are 32 bits wide
 
 int qsg_rmsnorm_quantize(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, int64_t ldx,

@@ -82,6 +82,22 @@ void launch_scaled_gemm(const uint8_t* a, int fa, int ka, const void* sa, const 
                         int kb, const void* sb, int64_t M, int64_t N, int64_t K, int64_t lda,
                         int64_t ldb, void* c, int c_dtype, int64_t ldc, bool accumulate, hipStream_t st);
 
+// INT8 (symmetric, codes in [-127, 127]): row-wise (q, s) and / or transposed
+// (qt, st_, with the workspace) copies; their product; the weight gradient from
+// an INT8 input; the gated activation that keeps its input in INT8.
+int64_t quantize_int8_workspace(int64_t rows, int64_t cols);
+void launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld, int8_t* q, float* s,
+                          int8_t* qt, float* st_, void* workspace, hipStream_t st);
+void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
+                      int64_t K, int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype,
+                      int64_t ldc, hipStream_t st);
+void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
+                       int64_t ldq, void* c, int c_dtype, int64_t ldc, bool accumulate, hipStream_t st);
+void launch_swiglu_int8_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* a, int8_t* aq,
+                            float* sa, int8_t* ck, float* cs, hipStream_t st);
+void launch_swiglu_int8_bwd(const void* da, int dtype, int64_t rows, int64_t cols, int64_t ldda, const int8_t* ck,
+                            const float* cs, void* dgu, int64_t lddgu, void* a, hipStream_t st);
+
 // Residual addition + RMS norm with an FP8 output (scaling < 0: none): one
 // pass, or two where a transposed copy or the current scaling is asked for.
 void launch_rmsnorm_quantize(const void* x, const void* r, int dtype, int64_t rows, int64_t cols, int64_t ldx,
