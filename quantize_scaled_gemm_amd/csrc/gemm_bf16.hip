@@ -52,7 +52,6 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));  // 8 bytes at any address
 
 constexpr int WT = 256;    // output tile (features of dY x features of X)
 constexpr int BT = 64;     // tokens per K step
@@ -95,42 +94,6 @@ __device__ __forceinline__ void load_block(const uint16_t* p, int64_t ld, int64_
   }
 }
 
-// The same of INT8 codes: r[i] holds a token's 8 codes and its scale.
-__device__ __forceinline__ void load_block_int8(const int8_t* p, const float* qs, int64_t ld, int64_t t0, int64_t f0,
-                                                int64_t T, int64_t F, u32x4 (&r)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t t = t0 + i;
-    u32x2 w = {0u, 0u};
-    uint32_t s = 0u;
-    if (t < T) {
-      const int8_t* at = p + t * ld + f0;
-      s = __float_as_uint(qs[t]);
-      if (f0 + 8 <= F) {
-        w = *reinterpret_cast<const u32x2_b*>(at);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-          if (f0 + e < F) w[e >> 2] |= (uint32_t)(uint8_t)at[e] << (8 * (e & 3));
-      }
-    }
-    r[i] = u32x4{w.x, w.y, s, 0u};
-  }
-}
-// Codes times their token's scale, rounded to bf16: what the codes stand for.
-__device__ __forceinline__ void widen_block_int8(u32x4 (&r)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = __uint_as_float(r[i].z);
-    const uint32_t w[2] = {r[i].x, r[i].y};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t c = w[k >> 1] >> (16 * (k & 1));
-      r[i][k] = pack_bf16x2((float)(int8_t)c * s, (float)(int8_t)(c >> 8) * s);
-    }
-  }
-}
-
 // Transpose the 8 x 8 block (r[token] = 8 features) and store feature rows:
 // row (frow + j) gets the 8 tokens of feature j as chunk `chunk`.
 __device__ __forceinline__ void store_block_t(uint8_t* lds, int frow, int chunk, const u32x4 (&r)[8]) {
@@ -145,8 +108,6 @@ __device__ __forceinline__ void store_block_t(uint8_t* lds, int frow, int chunk,
   }
 }
 
-// X8: X is INT8, widened where its block goes to LDS
-template <bool X8>
 __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   // two stages: step s writes stage s & 1 while slower waves may still read
   // the other, so one barrier per step suffices
@@ -167,16 +128,6 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   const int wn = wave >> 1, wk = wave & 1;
 
   const int64_t nsteps = (g.T + BT - 1) / BT;
-  auto load = [&](int64_t t0, u32x4 (&r)[8]) {
-    if (X8 && is_b)
-      load_block_int8(g.q, g.qs, ld, t0, fbase, g.T, F, r);
-    else
-      load_block(src, ld, t0, fbase, g.T, F, g.vec, r);
-  };
-  auto store = [&](uint8_t* lds, int chunk, u32x4 (&r)[8]) {
-    if (X8 && is_b) widen_block_int8(r);
-    store_block_t(lds, fg * 8, chunk, r);
-  };
   v16f acc[4][4];
   // One K step s, on the block already in LDS stage s & 1: the block of step
   // s + 1 (registers RN) is transposed into the other stage and the block of
@@ -190,12 +141,12 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   auto step = [&](u32x4 (&RN)[2][8], u32x4 (&RF)[2][8], int64_t s, auto first, auto stage) {
     constexpr int ST = decltype(stage)::value;
     if (s + 1 < nsteps) {
-      store(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], tg, RN[0]);
-      store(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], tg + 4, RN[1]);
+      store_block_t(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], fg * 8, tg, RN[0]);
+      store_block_t(is_b ? lds_b[ST ^ 1] : lds_a[ST ^ 1], fg * 8, tg + 4, RN[1]);
     }
     if (s + 2 < nsteps) {
-      load((s + 2) * BT + tg * 8, RF[0]);
-      load((s + 2) * BT + (tg + 4) * 8, RF[1]);
+      load_block(src, ld, (s + 2) * BT + tg * 8, fbase, g.T, F, g.vec, RF[0]);
+      load_block(src, ld, (s + 2) * BT + (tg + 4) * 8, fbase, g.T, F, g.vec, RF[1]);
     }
 #pragma unroll
     for (int ks = 0; ks < BT / 16; ++ks) {
@@ -241,14 +192,14 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_kernel(Bf16Args g) {
   }
   // two register blocks in flight: even steps' blocks in r0, odd steps' in r1
   u32x4 r0[2][8], r1[2][8];
-  load((int64_t)tg * 8, r0[0]);
-  load((int64_t)(tg + 4) * 8, r0[1]);
+  load_block(src, ld, (int64_t)tg * 8, fbase, g.T, F, g.vec, r0[0]);
+  load_block(src, ld, (int64_t)(tg + 4) * 8, fbase, g.T, F, g.vec, r0[1]);
   if (nsteps > 1) {
-    load(BT + (int64_t)tg * 8, r1[0]);
-    load(BT + (int64_t)(tg + 4) * 8, r1[1]);
+    load_block(src, ld, BT + (int64_t)tg * 8, fbase, g.T, F, g.vec, r1[0]);
+    load_block(src, ld, BT + (int64_t)(tg + 4) * 8, fbase, g.T, F, g.vec, r1[1]);
   }
-  store(is_b ? lds_b[0] : lds_a[0], tg, r0[0]);
-  store(is_b ? lds_b[0] : lds_a[0], tg + 4, r0[1]);
+  store_block_t(is_b ? lds_b[0] : lds_a[0], fg * 8, tg, r0[0]);
+  store_block_t(is_b ? lds_b[0] : lds_a[0], fg * 8, tg + 4, r0[1]);
   __syncthreads();
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
@@ -382,12 +333,42 @@ __device__ __forceinline__ void tile_of(int b, int nx, int ny, int& tx, int& ty)
   tx = idx / h;
 }
 
+// An INT8 X (X8) cannot go to LDS as it lies in memory.  A thread loads 16
+// codes of one token (3 tokens a step, XL), and writes what they stand for,
+// 32 bytes of bf16, where the direct load of a bf16 X would have put them, so
+// the rest of the kernel is the same.  The codes of step s + 2 replace those
+// of step s + 1 in their registers once these are widened, in the shadow of
+// step s's MFMAs.
+constexpr int XL = DT / 16;
+
+// Codes times their token's scale, rounded to bf16: two 16-byte chunks.
+// (The unsigned byte of code + 128 converts in one instruction; the fma takes
+// 128 s off again and rounds once, to fp32(code * s).)
+__device__ __forceinline__ void widen16(u32x4 c, float s, u32x4& lo, u32x4& hi) {
+  const float off = -128.0f * s;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t b = c[k] ^ 0x80808080u;
+    const uint32_t w0 = pack_bf16x2(fmaf((float)(b & 0xFF), s, off), fmaf((float)((b >> 8) & 0xFF), s, off));
+    const uint32_t w1 = pack_bf16x2(fmaf((float)((b >> 16) & 0xFF), s, off), fmaf((float)(b >> 24), s, off));
+    u32x4& o = k < 2 ? lo : hi;
+    o[2 * (k & 1)] = w0;
+    o[2 * (k & 1) + 1] = w1;
+  }
+}
+
+template <bool X8>
 __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g) {
   // three distinct stage objects, so that reads of one stage need no wait for
-  // the loads in flight into the others; [0, DOP) dY, [DOP, 2 DOP) X
-  __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * DOP];
-  __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * DOP];
-  __shared__ __attribute__((aligned(1024))) uint8_t st2[2 * DOP];
+  // the loads in flight into the others; [0, DOP) dY, [DOP, 2 DOP) X.  An INT8
+  // X has stages of its own, whose writes wait for no load into dY's.
+  constexpr int SB = X8 ? DOP : 2 * DOP, XB = X8 ? DOP : 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[SB];
+  __shared__ __attribute__((aligned(1024))) uint8_t st2[SB];
+  __shared__ __attribute__((aligned(16))) uint8_t sx0[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t sx1[XB];
+  __shared__ __attribute__((aligned(16))) uint8_t sx2[XB];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tx, ty;
@@ -402,29 +383,62 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
     const int t = 2 * (j * 4 + wave) + (lane >> 5);
     const int c = tswz(t, lane & 31);
     voa[j] = n0 + 8 * c < g.N ? (uint32_t)((t * g.lddy + 8 * c) * 2) : OUT_OF_RANGE;
-    vob[j] = k0 + 8 * c < g.K ? (uint32_t)((t * g.ldx + 8 * c) * 2) : OUT_OF_RANGE;
+    if constexpr (!X8) vob[j] = k0 + 8 * c < g.K ? (uint32_t)((t * g.ldx + 8 * c) * 2) : OUT_OF_RANGE;
   }
   const int wn = wave >> 1, wk = wave & 1;
   int offa[4], offb[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     offa[i] = tr_offset(wn * 128 + i * 32, lane);
-    offb[i] = DOP + tr_offset(wk * 128 + i * 32, lane);
+    offb[i] = (X8 ? 0 : DOP) + tr_offset(wk * 128 + i * 32, lane);
   }
+  // INT8 X: this thread's token of load j is 16 j + xt, its codes 16 xc .. +15
+  const int xt = wave * 4 + (lane >> 4), xc = lane & 15;
+  uint32_t xoff[XL];
+#pragma unroll
+  for (int j = 0; j < XL; ++j)
+    xoff[j] = k0 + 16 * xc < g.K ? (uint32_t)((16 * j + xt) * g.ldx + 16 * xc) : OUT_OF_RANGE;
+  u32x4 xq[XL];
+  uint32_t xs[XL];
+  auto x_load = [&](int j, __amdgpu_buffer_rsrc_t r, __amdgpu_buffer_rsrc_t rs) {
+    xq[j] = __builtin_amdgcn_raw_buffer_load_b128(r, xoff[j], 0, 0);
+    xs[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, (16 * j + xt) * 4, 0, 0);
+  };
+  auto x_put = [&](int j, uint8_t* dst) {
+    u32x4 lo, hi;
+    widen16(xq[j], __uint_as_float(xs[j]), lo, hi);
+    const int t = 16 * j + xt;
+    *reinterpret_cast<u32x4*>(dst + t * DROWB + tswz(t, 2 * xc) * 16) = lo;
+    *reinterpret_cast<u32x4*>(dst + t * DROWB + tswz(t, 2 * xc + 1) * 16) = hi;
+  };
+  auto x_rsrc = [&](int64_t step) {
+    int64_t rows = g.T - step * DT;
+    rows = rows < 0 ? 0 : (rows > DT ? DT : rows);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(g.q + step * DT * g.ldx + k0), 0, (int)(rows * g.ldx), 0x00020000);
+  };
+  auto s_rsrc = [&](int64_t step) {
+    int64_t rows = g.T - step * DT;
+    rows = rows < 0 ? 0 : (rows > DT ? DT : rows);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(g.qs + step * DT), 0, (int)(rows * 4), 0x00020000);
+  };
 
   const int64_t nsteps = (g.T + DT - 1) / DT;
   // the loads of step `step` into stage object `dst`
   auto issue = [&](uint8_t* dst, int64_t step) {
     const __amdgpu_buffer_rsrc_t ra = step_rsrc(g.dy, g.lddy, n0, g.T, step);
-    const __amdgpu_buffer_rsrc_t rb = step_rsrc(g.x, g.ldx, k0, g.T, step);
 #pragma unroll
     for (int j = 0; j < DLOADS; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(dst + (j * 4 + wave) * 1024), 16, voa[j], 0, 0, 0);
+    if constexpr (!X8) {
+      const __amdgpu_buffer_rsrc_t rb = step_rsrc(g.x, g.ldx, k0, g.T, step);
 #pragma unroll
-    for (int j = 0; j < DLOADS; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(dst + DOP + (j * 4 + wave) * 1024), 16, vob[j], 0,
-                                               0, 0);
+      for (int j = 0; j < DLOADS; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(dst + DOP + (j * 4 + wave) * 1024), 16, vob[j], 0,
+                                                 0, 0);
+    }
   };
+  // loads of a step: two operands, or dY, codes and scales
+  constexpr int LOADS = X8 ? DLOADS + 2 * XL : 2 * DLOADS;
 
   v16f acc[4][4];
   // Step s on stage `cur`: the loads of step s + 2 go into `next2` (the
@@ -432,15 +446,21 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
   // MFMAs run on `cur`, then the wait for step s + 1's loads (at most the
   // younger step's 2 DLOADS loads are still in flight) and a barrier.
   // FIRST: the first MFMA of each accumulator tile starts from C = 0.
-  auto step = [&](const uint8_t* cur, uint8_t* next2, int64_t s, auto first) {
+  // INT8 X: curx holds its step s; step s + 1 goes to nextx.
+  auto step = [&](const uint8_t* cur, uint8_t* next2, const uint8_t* curx, uint8_t* nextx, int64_t s, auto first) {
     issue(next2, s + 2);
+    const __amdgpu_buffer_rsrc_t rx = x_rsrc(s + 2), rs = s_rsrc(s + 2);
 #pragma unroll
     for (int ks = 0; ks < DT / 16; ++ks) {
       bf16x8 fa[4], fb[4];
+      if constexpr (X8) {
+        x_put(ks, nextx);
+        x_load(ks, rx, rs);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) fa[i] = tr_frag(cur + ks * 16 * DROWB + offa[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fb[j] = tr_frag(cur + ks * 16 * DROWB + offb[j]);
+      for (int j = 0; j < 4; ++j) fb[j] = tr_frag((X8 ? curx : cur) + ks * 16 * DROWB + offb[j]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -455,30 +475,50 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
     }
     // spread this step's fetches over its MFMAs (one per 3), rather than
     // letting them issue as one burst that stalls the MFMA issue
+    if constexpr (X8) {
 #pragma unroll
-    for (int q = 0; q < 2 * DLOADS; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);  // MFMA
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+      for (int q = 0; q < 16 * XL; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // VALU: the widening
+        if (q % 4 == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2 * DLOADS; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 3, 0);  // MFMA
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+      }
     }
-    wait_vm<2 * DLOADS>();
+    wait_vm<LOADS>();
     lds_barrier();
   };
 
+  if constexpr (X8) {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) x_load(j, x_rsrc(0), s_rsrc(0));
+  }
   issue(st0, 0);
+  if constexpr (X8) {
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+      x_put(j, sx0);
+      x_load(j, x_rsrc(1), s_rsrc(1));
+    }
+  }
   issue(st1, 1);
-  wait_vm<2 * DLOADS>();
+  wait_vm<LOADS>();
   lds_barrier();
-  step(st0, st2, 0, std::true_type{});
+  step(st0, st2, sx0, sx1, 0, std::true_type{});
   int64_t s = 1;
   // whole groups of 3 steps in the loop, the rest after it (a loop with
   // exits between its steps makes the compiler drain every load at its head)
   for (; s + 3 <= nsteps; s += 3) {
-    step(st1, st0, s, std::false_type{});
-    step(st2, st1, s + 1, std::false_type{});
-    step(st0, st2, s + 2, std::false_type{});
+    step(st1, st0, sx1, sx2, s, std::false_type{});
+    step(st2, st1, sx2, sx0, s + 1, std::false_type{});
+    step(st0, st2, sx0, sx1, s + 2, std::false_type{});
   }
-  if (s < nsteps) step(st1, st0, s++, std::false_type{});
-  if (s < nsteps) step(st2, st1, s++, std::false_type{});
+  if (s < nsteps) step(st1, st0, sx1, sx2, s++, std::false_type{});
+  if (s < nsteps) step(st2, st1, sx2, sx0, s++, std::false_type{});
   wait_vm<0>();  // the loads past the last step (empty resources) have landed
 
   // accumulator tile (i, j): lane l holds column k = l % 32 and rows
@@ -540,6 +580,171 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
     }
 }
 
+// ---- INT8 X, any shape and alignment, and few tiles ----
+//
+// TILE x TILE outputs to a workgroup of 4 waves, (TILE / 2) x (TILE / 2) each;
+// 64 tokens a step through registers into one of two LDS stages, in the
+// layout that the transpose reads want: dY as it lies in memory, X widened to
+// bf16.  Loads ask for no alignment.  Features past the end of an operand
+// only reach results that are not stored, so a row may be read past its end
+// where memory goes on, into the next row; only a step in which it might not
+// (the last one or two) is loaded element by element.
+template <int TILE>
+struct SmallStage {
+  static constexpr int ROW = TILE * 2;                // bytes of a token
+  static constexpr int AC = TILE / 32, XC = TILE / 64;  // 16-byte chunks of dY, of X a thread loads per step
+};
+
+// chunk c of token row t: 4 consecutive rows x 4 chunks on distinct banks
+template <int TILE>
+__device__ __forceinline__ int small_swz(int t, int c) {
+  return TILE >= 128 ? c ^ ((t & 3) << 2) : c ^ (((t >> 1) & 1) << 2);
+}
+template <int TILE>
+__device__ __forceinline__ int small_tr_offset(int fblk, int lane) {
+  const int g = lane >> 4, e = (lane >> 2) & 3, q = lane & 3;
+  const int t = 8 * (g >> 1) + e;
+  const int c = (fblk >> 3) + 2 * (g & 1) + (q >> 1);
+  return t * SmallStage<TILE>::ROW + small_swz<TILE>(t, c) * 16 + (q & 1) * 8;
+}
+
+typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
+
+template <int TILE>
+__global__ __launch_bounds__(256) void gemm_wgrad_int8_kernel(Bf16Args g) {
+  using S = SmallStage<TILE>;
+  constexpr int NT = TILE / 64;  // 32 x 32 MFMA tiles of a wave, each way
+  __shared__ __attribute__((aligned(16))) uint8_t la[2][BT * S::ROW];
+  __shared__ __attribute__((aligned(16))) uint8_t lx[2][BT * S::ROW];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wn = wave >> 1, wk = wave & 1;
+  const int64_t n0 = (int64_t)blockIdx.y * TILE, k0 = (int64_t)blockIdx.x * TILE;
+  // chunk i of a thread: token at[i], features af (dY); token xt[i], codes xf
+  int at[S::AC], xt[S::XC];
+  const int ac = tid % (TILE / 8), xc = tid % (TILE / 16);
+#pragma unroll
+  for (int i = 0; i < S::AC; ++i) at[i] = (i * 256 + tid) / (TILE / 8);
+#pragma unroll
+  for (int i = 0; i < S::XC; ++i) xt[i] = (i * 256 + tid) / (TILE / 16);
+  // a chunk that begins past the end reads the last one that does not
+  const int64_t a_last = (g.N - 1) / 8 * 8, x_last = (g.K - 1) / 16 * 16;
+  const int64_t af = n0 + 8 * ac < a_last ? n0 + 8 * ac : a_last;
+  const int64_t xf = k0 + 16 * xc < x_last ? k0 + 16 * xc : x_last;
+  const int64_t a_end = (g.T - 1) * g.lddy + g.N, x_end = (g.T - 1) * g.ldx + g.K;  // elements that are there
+
+  u32x4 ra[S::AC], rx[S::XC];
+  float rs[S::XC];
+  auto fetch = [&](int64_t s) {
+    const int64_t t0 = s * BT, tl = t0 + BT - 1;
+    if (tl < g.T && tl * g.lddy + a_last + 8 <= a_end && tl * g.ldx + x_last + 16 <= x_end) {
+#pragma unroll
+      for (int i = 0; i < S::AC; ++i) ra[i] = *reinterpret_cast<const u32x4_e*>(g.dy + (t0 + at[i]) * g.lddy + af);
+#pragma unroll
+      for (int i = 0; i < S::XC; ++i) {
+        rx[i] = *reinterpret_cast<const u32x4_b*>(g.q + (t0 + xt[i]) * g.ldx + xf);
+        rs[i] = g.qs[t0 + xt[i]];
+      }
+    } else {
+      // every element by a load of its own from an address that is there
+#pragma unroll
+      for (int i = 0; i < S::AC; ++i) {
+        const bool in = t0 + at[i] < g.T;
+        const uint16_t* p = g.dy + (in ? t0 + at[i] : g.T - 1) * g.lddy;
+        u32x4 r = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e >> 1] |= (uint32_t)p[af + e < g.N ? af + e : g.N - 1] << (16 * (e & 1));
+        ra[i] = in ? r : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < S::XC; ++i) {
+        const bool in = t0 + xt[i] < g.T;
+        const int64_t t = in ? t0 + xt[i] : g.T - 1;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(g.q) + t * g.ldx;
+        u32x4 r = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 16; ++e) r[e >> 2] |= (uint32_t)p[xf + e < g.K ? xf + e : g.K - 1] << (8 * (e & 3));
+        rx[i] = r;
+        rs[i] = in ? g.qs[t] : 0.0f;
+      }
+    }
+  };
+  auto put = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < S::AC; ++i)
+      *reinterpret_cast<u32x4*>(la[st] + at[i] * S::ROW + small_swz<TILE>(at[i], ac) * 16) = ra[i];
+#pragma unroll
+    for (int i = 0; i < S::XC; ++i) {
+      u32x4 lo, hi;
+      widen16(rx[i], rs[i], lo, hi);
+      *reinterpret_cast<u32x4*>(lx[st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc) * 16) = lo;
+      *reinterpret_cast<u32x4*>(lx[st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc + 1) * 16) = hi;
+    }
+  };
+  auto frag = [&](const uint8_t* p) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * S::ROW));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  int offa[NT], offx[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    offa[i] = small_tr_offset<TILE>(wn * (TILE / 2) + i * 32, lane);
+    offx[i] = small_tr_offset<TILE>(wk * (TILE / 2) + i * 32, lane);
+  }
+  v16f acc[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  const int64_t nsteps = (g.T + BT - 1) / BT;
+  if (nsteps > 0) {
+    fetch(0);
+    put(0);
+  }
+  __syncthreads();
+  for (int64_t s = 0; s < nsteps; ++s) {
+    const int st = (int)(s & 1);
+    if (s + 1 < nsteps) fetch(s + 1);
+#pragma unroll
+    for (int ks = 0; ks < BT / 16; ++ks) {
+      bf16x8 fa[NT], fx[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        fa[i] = frag(la[st] + ks * 16 * S::ROW + offa[i]);
+        fx[i] = frag(lx[st] + ks * 16 * S::ROW + offx[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fx[j], acc[i][j], 0, 0, 0);
+    }
+    if (s + 1 < nsteps) put(st ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t k = k0 + wk * (TILE / 2) + j * 32 + (lane & 31);
+      if (k >= g.K) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t n = n0 + wn * (TILE / 2) + i * 32 + 8 * (v / 4) + 4 * (lane >> 5) + (v % 4);
+        if (n >= g.N) continue;
+        if (g.out_bf16) {
+          reinterpret_cast<uint16_t*>(g.c)[n * g.ldc + k] = (uint16_t)(pack_bf16x2(acc[i][j][v], 0.0f) & 0xFFFF);
+        } else {
+          float* cp = reinterpret_cast<float*>(g.c) + n * g.ldc + k;
+          *cp = g.accumulate ? *cp + acc[i][j][v] : acc[i][j][v];
+        }
+      }
+    }
+}
+
 }  // namespace
 
 void launch_wgrad_bf16(const void* dy, int64_t T, int64_t N, int64_t lddy, const void* x, int64_t K, int64_t ldx,
@@ -558,9 +763,9 @@ void launch_wgrad_bf16(const void* dy, int64_t T, int64_t N, int64_t lddy, const
   const bool dma = g.vec && N % 8 == 0 && K % 8 == 0 && lddy < (1 << 24) && ldx < (1 << 24) && T > 0 &&
                    (uint64_t)grid.x * grid.y <= 0x7FFFFFFFu;
   if (dma)
-    hipLaunchKernelGGL(gemm_wgrad_bf16_dma_kernel, dim3(grid.x * grid.y), dim3(256), 0, st, g);
+    hipLaunchKernelGGL(gemm_wgrad_bf16_dma_kernel<false>, dim3(grid.x * grid.y), dim3(256), 0, st, g);
   else
-    hipLaunchKernelGGL(gemm_wgrad_bf16_kernel<false>, grid, dim3(256), 0, st, g);
+    hipLaunchKernelGGL(gemm_wgrad_bf16_kernel, grid, dim3(256), 0, st, g);
 }
 
 void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
@@ -569,11 +774,21 @@ void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const
   g.dy = reinterpret_cast<const uint16_t*>(dy);
   g.q = q; g.qs = s;
   g.T = T; g.N = N; g.K = K; g.lddy = lddy; g.ldx = ldq; g.ldc = ldc; g.c = c;
-  g.vec = (uintptr_t)dy % 16 == 0 && lddy % 8 == 0;
   g.out_bf16 = c_dtype == QSG_BF16;
   g.accumulate = accumulate && !g.out_bf16;
-  const dim3 grid((unsigned)((K + WT - 1) / WT), (unsigned)((N + WT - 1) / WT));
-  hipLaunchKernelGGL(gemm_wgrad_bf16_kernel<true>, grid, dim3(256), 0, st, g);
+  auto tiles = [&](int64_t t) { return ((K + t - 1) / t) * ((N + t - 1) / t); };
+  // direct loads of dY: as for a bf16 X, with whole 16-byte chunks of codes
+  const bool dma = (uintptr_t)dy % 16 == 0 && (uintptr_t)q % 16 == 0 && lddy % 8 == 0 && ldq % 16 == 0 && N % 8 == 0 &&
+                   K % 16 == 0 && lddy < (1 << 24) && ldq < (1 << 24) && T > 0 && tiles(WT) <= 0x7FFFFF;
+  if (dma && tiles(WT) >= 128) {
+    hipLaunchKernelGGL(gemm_wgrad_bf16_dma_kernel<true>, dim3((unsigned)tiles(WT)), dim3(256), 0, st, g);
+  } else if (tiles(128) >= 256) {
+    hipLaunchKernelGGL(gemm_wgrad_int8_kernel<128>, dim3((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128)),
+                       dim3(256), 0, st, g);
+  } else {
+    hipLaunchKernelGGL(gemm_wgrad_int8_kernel<64>, dim3((unsigned)((K + 63) / 64), (unsigned)((N + 63) / 64)),
+                       dim3(256), 0, st, g);
+  }
 }
 
 }  // namespace qsg

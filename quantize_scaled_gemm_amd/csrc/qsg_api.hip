@@ -411,7 +411,7 @@ int qsg_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int
   if (T < 0 || N < 0 || K < 0) return fail(QSG_ERR_ARG, "%s: negative shape", fn);
   if (accumulate && c_dtype != QSG_F32) return fail(QSG_ERR_UNSUPPORTED, "%s: accumulation needs an fp32 C", fn);
   if (N == 0 || K == 0) return QSG_OK;
-  if (N > 65535 * 256LL || K > (1 << 26)) return fail(QSG_ERR_UNSUPPORTED, "%s: more than 65535 x 2^18 tiles of 256 x 256", fn);
+  if (N > 65535 * 128 || K > (1 << 26)) return fail(QSG_ERR_UNSUPPORTED, "%s: N must be at most 65535 x 128 and K at most 2^26", fn);
   if (!c) return fail(QSG_ERR_ARG, "%s: null C", fn);
   if (ldc < K) return fail(QSG_ERR_ARG, "%s: ldc < K", fn);
   if (!aligned(c, esize(c_dtype))) return fail(QSG_ERR_ALIGN, "%s: C not aligned to its element size", fn);
