@@ -45,6 +45,8 @@
 //     many work items of half the size.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "qsg_device.h"
 #include "qsg_internal.h"
 
@@ -54,6 +56,8 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
@@ -74,6 +78,7 @@ struct FastArgs {
   uint32_t gm;      // tile-rows per group of the tile order
   const float* ta;  // NVFP4: the operands' per-tensor decode scales
   const float* tb;
+  const void* bias;  // INT8: a value for each column
 };
 
 // 16-byte chunk c of LDS row r is stored at position c ^ row_swizzle(r).  A
@@ -196,8 +201,10 @@ __device__ __forceinline__ uint32_t* group_sb() { return GB ? lds_gsb1 : lds_gsb
 // Scale handling of a kernel instance: SC_NONE per-tensor (one scale pair in
 // the epilogue); SC_MX E8M0 bytes fetched with every K tile (4 bytes per row);
 // SC_MXG E8M0 bytes fetched once per group of 4 K tiles (16 bytes per row,
-// a quarter of the fetch instructions, each covering 64 rows).
-constexpr int SC_NONE = 0, SC_MX = 1, SC_MXG = 2;
+// a quarter of the fetch instructions, each covering 64 rows); SC_I8 INT8
+// codes with an fp32 scale for each row of A and of B (and a bias), which come
+// to LDS with a tile's first K step and are applied in its epilogue.
+constexpr int SC_NONE = 0, SC_MX = 1, SC_MXG = 2, SC_I8 = 3;
 
 // Fetch of K tile kt of a tile into stage S: part 0 = the A tile (+ MX
 // scale words), part 1 = the B tile; `wl` is this wave's 1 KB block offset.
@@ -323,6 +330,20 @@ __device__ __forceinline__ void mfma_range(v16f (&acc)[TMW][TN], const Frags<TN>
   }
 }
 
+// INT8: the two halves of a fragment are the operands of two 32-K
+// instructions, each lane half's 16 bytes being 16 of their K values.
+template <bool MX, int FA, int FB, int LO, int HI, int TN, int OPS = 0>
+__device__ __forceinline__ void mfma_range(v16i (&acc)[TMW][TN], const Frags<TN>& f) {
+#pragma unroll
+  for (int q = LO; q < HI; ++q) {
+    const int i = q / TN, j = q % TN;
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_shufflevector(f.b[j], f.b[j], 0, 1, 2, 3),
+                                                      __builtin_shufflevector(f.a[i], f.a[i], 0, 1, 2, 3), acc[i][j], 0, 0, 0);
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_shufflevector(f.b[j], f.b[j], 4, 5, 6, 7),
+                                                      __builtin_shufflevector(f.a[i], f.a[i], 4, 5, 6, 7), acc[i][j], 0, 0, 0);
+  }
+}
+
 // The 16 accumulators of one 32 x 32 tile copied to VGPRs (keeps the
 // accumulators in AGPRs for the register allocator).  The reads come as one
 // block into 16 distinct registers, so the multiplies that follow find their
@@ -336,6 +357,56 @@ __device__ __forceinline__ void acc_read16(const v16f& a, float (&o)[16]) {
         : "a"(a[q]), "a"(a[q + 1]), "a"(a[q + 2]), "a"(a[q + 3]));
 }
 
+__device__ __forceinline__ void acc_read16(const v16i& a, float (&o)[16]) {
+  int t[16];
+#pragma unroll
+  for (int q = 0; q < 16; q += 4)
+    asm("v_accvgpr_read_b32 %0, %4\n\tv_accvgpr_read_b32 %1, %5\n\t"
+        "v_accvgpr_read_b32 %2, %6\n\tv_accvgpr_read_b32 %3, %7"
+        : "=v"(t[q]), "=v"(t[q + 1]), "=v"(t[q + 2]), "=v"(t[q + 3])
+        : "a"(a[q]), "a"(a[q + 1]), "a"(a[q + 2]), "a"(a[q + 3]));
+#pragma unroll
+  for (int q = 0; q < 16; ++q) o[q] = (float)t[q];
+}
+
+// What a tile's results are multiplied by in the epilogue: one factor, or for
+// INT8 the scales of the lane's row i and of its 16 columns j, and the bias of
+// those (in registers the biases would be too many: they are read from LDS
+// where they are added).
+struct ScaleTensor {
+  float alpha;
+  __device__ __forceinline__ void apply(float (&v)[16], int, int) const {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] *= alpha;
+  }
+};
+enum { BIAS_NONE = 0, BIAS_F32 = 1, BIAS_BF16 = 2 };
+
+template <int TN, int BIAS>
+struct ScaleRows {
+  float a[TMW];
+  float4 b[TN][4];
+  const uint32_t* bias;  // LDS, of the tile's first column
+  int n;                 // the lane's first column in the tile
+  __device__ __forceinline__ void apply(float (&v)[16], int i, int j) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float s[4] = {b[j][q].x, b[j][q].y, b[j][q].z, b[j][q].w};
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int at = n + j * 32 + 8 * q;
+      if constexpr (BIAS == BIAS_F32) {
+        const float4 w = *reinterpret_cast<const float4*>(bias + at);
+        c[0] = w.x; c[1] = w.y; c[2] = w.z; c[3] = w.w;
+      } else if constexpr (BIAS == BIAS_BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(bias + at / 2);
+        c[0] = bf16lo(w.x); c[1] = bf16hi(w.x); c[2] = bf16lo(w.y); c[3] = bf16hi(w.y);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] = fmaf(v[4 * q + e] * a[i], s[e], c[e]);
+    }
+  }
+};
+
 typedef __attribute__((address_space(1))) uint8_t gbyte;
 
 // One 32 x 32 accumulator tile scaled by alpha and rearranged for 64-byte
@@ -348,13 +419,12 @@ typedef __attribute__((address_space(1))) uint8_t gbyte;
 // ys[pr] rows 16..31 of the 64-byte column pair pr (bf16: one pair, fp32:
 // two).  All 16 reads come first, then all multiplies, then the conversions,
 // so each stage uses results issued several instructions earlier.
-template <bool OUT_BF16>
-__device__ __forceinline__ void tile_pieces(const v16f& acc, float alpha, u32x4 (&xs)[OUT_BF16 ? 1 : 2],
-                                            u32x4 (&ys)[OUT_BF16 ? 1 : 2]) {
+template <bool OUT_BF16, typename Acc, typename Scale>
+__device__ __forceinline__ void tile_pieces(const Acc& acc, const Scale& scale, int i, int j,
+                                            u32x4 (&xs)[OUT_BF16 ? 1 : 2], u32x4 (&ys)[OUT_BF16 ? 1 : 2]) {
   float v[16];
   acc_read16(acc, v);
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] *= alpha;
+  scale.apply(v, i, j);
   constexpr int NPAIR = OUT_BF16 ? 1 : 2;
   u32x4 lo[2], hi[2];  // per pair: the 16-byte pieces before the row swap
   if constexpr (OUT_BF16) {
@@ -406,11 +476,11 @@ __device__ __forceinline__ void tile_coords(const FastArgs& g, uint32_t logical,
   n0 = ((logical % per_group) / gsize) * (TN * 64);
 }
 
-// Epilogue of one workgroup tile: scale by alpha, convert, store straight
+// Epilogue of one workgroup tile: scale, convert, store straight
 // from registers (see tile_pieces); every store writes 16 rows x 64
 // contiguous bytes.  (cm0, cn0): the tile's first row and column.
-template <bool OUT_BF16, int TN>
-__device__ __forceinline__ void store_tile(const FastArgs& g, v16f (&acc)[TMW][TN], float alpha, int64_t cm0,
+template <bool OUT_BF16, int TN, typename Acc, typename Scale>
+__device__ __forceinline__ void store_tile(const FastArgs& g, Acc (&acc)[TMW][TN], const Scale& scale, int64_t cm0,
                                            int64_t cn0, int wm, int wn, int lane) {
   constexpr int WM = FBM / 2, WN = TN * 32, TBN = TN * 64;
   constexpr int ESZ = OUT_BF16 ? 2 : 4;
@@ -440,7 +510,7 @@ __device__ __forceinline__ void store_tile(const FastArgs& g, v16f (&acc)[TMW][T
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         u32x4 xs[NPAIR], ys[NPAIR];
-        tile_pieces<OUT_BF16>(acc[i][j], alpha, xs, ys);
+        tile_pieces<OUT_BF16>(acc[i][j], scale, i, j, xs, ys);
 #pragma unroll
         for (int pr = 0; pr < NPAIR; ++pr) {
           const int cb = j * 32 * ESZ + pr * 64;  // byte column of the pair in the wave's block
@@ -467,7 +537,7 @@ __device__ __forceinline__ void store_tile(const FastArgs& g, v16f (&acc)[TMW][T
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         u32x4 xs[NPAIR], ys[NPAIR];
-        tile_pieces<OUT_BF16>(acc[i][j], alpha, xs, ys);
+        tile_pieces<OUT_BF16>(acc[i][j], scale, i, j, xs, ys);
 #pragma unroll
         for (int pr = 0; pr < NPAIR; ++pr) {
           const int cb = j * 32 * ESZ + pr * 64;
@@ -511,9 +581,10 @@ __device__ __forceinline__ void store_tile(const FastArgs& g, v16f (&acc)[TMW][T
   }
 }
 
-template <int SC, int FA, int FB, bool OUT_BF16, int TN>
+template <int SC, int FA, int FB, bool OUT_BF16, int TN, int BIAS = BIAS_NONE>
 __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
-  constexpr bool MX = SC != SC_NONE;
+  constexpr bool MX = SC == SC_MX || SC == SC_MXG, I8 = SC == SC_I8;
+  constexpr int MM = I8 ? 2 : 1;  // instructions of a 64-K MFMA step and accumulator tile
   constexpr int WM = FBM / 2, WN = TN * 32;
   constexpr int NQ = TMW * TN;  // MFMAs per 64-K step
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -546,7 +617,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
   const int sh0 = 8 * h, sh1 = 8 * h + 16;
   constexpr int OPS1 = SC == SC_MXG ? 2 : 0;  // scale byte of the second 64-K step
   float alpha = 1.0f;
-  if constexpr (!MX) alpha = *reinterpret_cast<const float*>(g.sa) * *reinterpret_cast<const float*>(g.sb);
+  if constexpr (SC == SC_NONE) alpha = *reinterpret_cast<const float*>(g.sa) * *reinterpret_cast<const float*>(g.sb);
 
   uint32_t voa[NCHUNK], vob[NCHUNK];
   chunk_offsets(voa, g.lda);
@@ -564,6 +635,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
     }
     return t;
   };
+  uint32_t odd = 0;  // INT8: which of two buffers holds the tile's scales
 
   uint32_t m0, n0;
   tile_coords<TN>(g, logical, m0, n0);
@@ -577,7 +649,7 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
   wait_vm_lgkm0<NS>();  // stage 0 landed
   lds_barrier();
 
-  v16f acc[TMW][TN];
+  std::conditional_t<I8, v16i, v16f> acc[TMW][TN];
   Frags<TN> f0, f1;
   GroupWords<TN> gw;
   load_frags<0, SC, 0, 0, TN>(f0, gw, 0, a_row_off, b_row_off, c00, c01, a_srow, b_srow, a_gs, b_gs, sh0);
@@ -596,7 +668,20 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    if constexpr (I8) {
+      // The tile's scales, a row to a thread.  The waits of the first K step
+      // cover them.  Another wave may still read the last tile's scales, so
+      // tiles take two buffers in turn; the barriers of a K loop lie between
+      // two uses of one.
+      const uint32_t row4 = threadIdx.x * 4;
+      dma4(rows_rsrc(g.sa, cm0, g.M, 4), row4, 0, (odd ? lds_sa1 : lds_sa0) + wl / 16);
+      dma4(rows_rsrc(g.sb, cn0, g.N, 4), row4, 0, (odd ? lds_sb1 : lds_sb0) + wl / 16);
+      // (of a bf16 bias 128 words are read; an even number of columns, so that
+      // the last one is whole)
+      if constexpr (BIAS != BIAS_NONE)
+        dma4(rows_rsrc(g.bias, cn0, g.N, BIAS == BIAS_F32 ? 4 : 2), row4, 0, (odd ? lds_gsa1 : lds_gsa0) + wl / 16);
+    }
 
   // One K tile KT in stage S (f0 holds its first 64-K fragments), in three
   // phases around two barriers:
@@ -623,10 +708,10 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
     }                                                                                          \
     mfma_range<MX, FA, FB, 0, P1>(acc, f0);                                                    \
     _Pragma("unroll") for (int q = 0; q < P1 - 1; ++q) {                                       \
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                       \
+      __builtin_amdgcn_sched_group_barrier(0x008, MM, 0);                                       \
       __builtin_amdgcn_sched_group_barrier(0x100, 2 * (TMW + TN) / (P1 - 1), 0);               \
     }                                                                                          \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                         \
+    __builtin_amdgcn_sched_group_barrier(0x008, MM, 0);                                         \
     __builtin_amdgcn_sched_barrier(0);                                                         \
     wait_vm_lgkm0<63>();                                                                       \
     lds_barrier();                                                                             \
@@ -643,11 +728,11 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
     mfma_range<MX, FA, FB, P1, NQ>(acc, f0);                                                   \
     mfma_range<MX, FA, FB, 0, P2, TN, OPS1>(acc, f1);                                          \
     _Pragma("unroll") for (int q = 0; q < (NAS < NQ - P1 + P2 ? NAS : NQ - P1 + P2); ++q) {    \
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);                                       \
+      __builtin_amdgcn_sched_group_barrier(0x008, MM, 1);                                       \
       __builtin_amdgcn_sched_group_barrier(0x001, 3, 1);                                       \
     }                                                                                          \
     if constexpr (NQ - P1 + P2 > NAS)                                                          \
-      __builtin_amdgcn_sched_group_barrier(0x008, NQ - P1 + P2 - NAS, 1);                      \
+      __builtin_amdgcn_sched_group_barrier(0x008, MM * (NQ - P1 + P2 - NAS), 1);                      \
     __builtin_amdgcn_sched_barrier(0);                                                         \
     wait_vm_lgkm0<NAS>();                                                                      \
     lds_barrier();                                                                             \
@@ -656,11 +741,11 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
     issue_part<S, 1, SC, TN>(RES, voa, vob, vos, wl, FK);                                      \
     mfma_range<MX, FA, FB, P2, NQ, TN, OPS1>(acc, f1);                                         \
     _Pragma("unroll") for (int q = 0; q < NQ - P2 - 1; ++q) {                                  \
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 2);                                       \
+      __builtin_amdgcn_sched_group_barrier(0x008, MM, 2);                                       \
       __builtin_amdgcn_sched_group_barrier(0x100, 2 * (TMW + TN) / (NQ - P2 - 1), 2);          \
       __builtin_amdgcn_sched_group_barrier(0x001, 3, 2);                                       \
     }                                                                                          \
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 2);                                         \
+    __builtin_amdgcn_sched_group_barrier(0x008, MM, 2);                                         \
     __builtin_amdgcn_sched_barrier(0);                                                         \
   }
 
@@ -695,7 +780,23 @@ __global__ __launch_bounds__(256, 1) void gemm_fast_kernel(FastArgs g) {
     // (The last step's reads of f0 are repeated after it, so that the
     // fragments are not held through the epilogue.)
 
-    store_tile<OUT_BF16, TN>(g, acc, alpha, cm0, cn0, wm, wn, lane);
+    if constexpr (I8) {
+      ScaleRows<TN, BIAS> scale;
+      const float* sa = reinterpret_cast<const float*>(odd ? lds_sa1 : lds_sa0) + a_srow;
+      const float* sb = reinterpret_cast<const float*>(odd ? lds_sb1 : lds_sb0) + wn * WN + 4 * h;
+#pragma unroll
+      for (int i = 0; i < TMW; ++i) scale.a[i] = sa[i * 32];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) scale.b[j][q] = *reinterpret_cast<const float4*>(sb + j * 32 + 8 * q);
+      scale.bias = odd ? lds_gsa1 : lds_gsa0;
+      scale.n = wn * WN + 4 * h;
+      store_tile<OUT_BF16, TN>(g, acc, scale, cm0, cn0, wm, wn, lane);
+      odd ^= 1;
+    } else {
+      store_tile<OUT_BF16, TN>(g, acc, ScaleTensor{alpha}, cm0, cn0, wm, wn, lane);
+    }
     if (!more) {
       wait_vm_lgkm0<0>();  // the repeated fetches of the last step land before the workgroup ends
       break;
@@ -953,7 +1054,7 @@ __global__ __launch_bounds__(256, 1) void gemm_nvfp4_fast_kernel(FastArgs g) {
       nv_ktile<1>(acc, r0, gw, fa, fb, ad, kt + 3 < nk ? cur : nxt_t, kt + 3 < nk ? kt + 3 : kt + 3 - nk, voa, vob, vos, wl);
       kt += 2;
     } while (kt < nk);
-    store_tile<OUT_BF16, TN>(g, acc, alpha, cm0, cn0, wm, wn, lane);
+    store_tile<OUT_BF16, TN>(g, acc, ScaleTensor{alpha}, cm0, cn0, wm, wn, lane);
     if (!more) {
       wait_vm_lgkm0<0>();  // the repeated fetches land before the workgroup ends
       break;
@@ -985,20 +1086,20 @@ int device_cu_count() {
 // elsewhere.
 uint32_t tile_group_rows(int64_t K, int64_t tiles_n) { return (K <= 4096 && tiles_n <= 16) ? 8u : 4u; }
 
-template <int SC, int FA, int FB>
+template <int SC, int FA, int FB, int BIAS = BIAS_NONE>
 void launch_fast_cfg(const FastArgs& g, bool out_bf16, int tn, hipStream_t st) {
   const int64_t tiles = g.tiles_m * g.tiles_n;
   const unsigned grid = (unsigned)(tiles < g.max_wgs ? tiles : g.max_wgs);
   if (tn == 4) {
     if (out_bf16)
-      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, true, 4>), dim3(grid), dim3(256), 0, st, g);
+      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, true, 4, BIAS>), dim3(grid), dim3(256), 0, st, g);
     else
-      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, false, 4>), dim3(grid), dim3(256), 0, st, g);
+      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, false, 4, BIAS>), dim3(grid), dim3(256), 0, st, g);
   } else {
     if (out_bf16)
-      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, true, 2>), dim3(grid), dim3(256), 0, st, g);
+      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, true, 2, BIAS>), dim3(grid), dim3(256), 0, st, g);
     else
-      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, false, 2>), dim3(grid), dim3(256), 0, st, g);
+      hipLaunchKernelGGL((gemm_fast_kernel<SC, FA, FB, false, 2, BIAS>), dim3(grid), dim3(256), 0, st, g);
   }
 }
 
@@ -1008,6 +1109,34 @@ void launch_fast_fmt(const FastArgs& g, int fa, int fb, bool out_bf16, int tn, h
   else if (fa == kE5M2 && fb == kE4M3) launch_fast_cfg<SC, kE5M2, kE4M3>(g, out_bf16, tn, st);
   else if (fa == kE4M3 && fb == kE5M2) launch_fast_cfg<SC, kE4M3, kE5M2>(g, out_bf16, tn, st);
   else launch_fast_cfg<SC, kE5M2, kE5M2>(g, out_bf16, tn, st);
+}
+
+// The launches of a product: launch(arguments, 4 or 2).  A last round that
+// would leave at least half of the workgroups idle, made of whole tile-rows,
+// runs as a second launch of 256 x 128 tiles (twice as many, each half the
+// work; every output element is computed the same way, so the results do not
+// change).  `sa_row`: bytes of A's scales in a row.
+template <typename Launch>
+void launch_rounds(const FastArgs& g, int esz, int64_t sa_row, Launch launch) {
+  const int64_t T = g.tiles_m * g.tiles_n, G = g.max_wgs, R = T % G;
+  if (T > G && R > 0 && 2 * R <= G && R % g.tiles_n == 0) {
+    const int64_t tail_rows = R / g.tiles_n;
+    const int64_t m_main = (g.tiles_m - tail_rows) * FBM;
+    FastArgs gm = g;
+    gm.M = m_main;
+    gm.tiles_m = g.tiles_m - tail_rows;
+    launch(gm, 4);
+    FastArgs gt = g;
+    gt.a = g.a + m_main * g.lda;
+    gt.c = reinterpret_cast<uint8_t*>(g.c) + m_main * g.ldc * esz;
+    gt.sa = reinterpret_cast<const uint8_t*>(g.sa) + m_main * sa_row;
+    gt.M = g.M - m_main;
+    gt.tiles_m = tail_rows;
+    gt.tiles_n = (g.N + 127) / 128;
+    launch(gt, 2);
+  } else {
+    launch(g, 4);
+  }
 }
 
 }  // namespace
@@ -1045,29 +1174,35 @@ bool launch_scaled_gemm_fast(const uint8_t* a, int fa, bool mx, const void* sa, 
     else
       launch_fast_fmt<SC_NONE>(ga, fa, fb, out_bf16, tn, st);
   };
-  // A last round that would leave at least half of the workgroups idle, made
-  // of whole tile-rows: those rows run as a second launch of 256 x 128 tiles
-  // (twice as many, each half the work; every output element is computed the
-  // same way, so the results do not change).
-  const int64_t T = tiles_m * tiles_n, G = g.max_wgs, R = T % G;
-  if (T > G && R > 0 && 2 * R <= G && R % tiles_n == 0) {
-    const int64_t tail_rows = R / tiles_n;
-    const int64_t m_main = (tiles_m - tail_rows) * FBM;
-    FastArgs gm = g;
-    gm.M = m_main;
-    gm.tiles_m = tiles_m - tail_rows;
-    launch(gm, 4);
-    FastArgs gt = g;
-    gt.a = a + m_main * lda;
-    gt.c = reinterpret_cast<uint8_t*>(c) + m_main * ldc * esz;
-    if (mx) gt.sa = reinterpret_cast<const uint8_t*>(sa) + m_main * (K / 32);
-    gt.M = M - m_main;
-    gt.tiles_m = tail_rows;
-    gt.tiles_n = (N + 127) / 128;
-    launch(gt, 2);
-  } else {
-    launch(g, 4);
-  }
+  launch_rounds(g, esz, mx ? K / 32 : 0, launch);
+  return true;
+}
+
+bool launch_gemm_int8_fast(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
+                           int64_t K, int64_t lda, int64_t ldb, const void* bias, bool bias_bf16, void* c, int c_dtype,
+                           int64_t ldc, hipStream_t st) {
+  if (bias && ((uintptr_t)bias % 4 || (bias_bf16 && N % 2))) return false;
+  if (K <= 0 || K % (2 * FBK) != 0) return false;
+  if ((uintptr_t)a % 16 || (uintptr_t)b % 16 || lda % 16 || ldb % 16) return false;
+  if (M * lda >= (int64_t)1 << 32 || N * ldb >= (int64_t)1 << 32) return false;
+  FastArgs g{};
+  g.tiles_m = (M + FBM - 1) / FBM;
+  g.tiles_n = (N + FBN - 1) / FBN;
+  if (g.tiles_m * g.tiles_n < 128) return false;
+  g.a = reinterpret_cast<const uint8_t*>(a);
+  g.b = reinterpret_cast<const uint8_t*>(b);
+  g.sa = sa; g.sb = sb; g.bias = bias;
+  g.M = M; g.N = N; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.c = c;
+  const bool out_bf16 = (c_dtype == 1);
+  const int esz = out_bf16 ? 2 : 4;
+  g.vec_c = ((uintptr_t)c % 16 == 0) && ((ldc * esz) % 16 == 0);
+  g.max_wgs = device_cu_count();
+  g.gm = tile_group_rows(K, g.tiles_n);
+  launch_rounds(g, esz, sizeof(float), [&](const FastArgs& ga, int tn) {
+    if (!bias) launch_fast_cfg<SC_I8, 0, 0>(ga, out_bf16, tn, st);
+    else if (bias_bf16) launch_fast_cfg<SC_I8, 0, 0, BIAS_BF16>(ga, out_bf16, tn, st);
+    else launch_fast_cfg<SC_I8, 0, 0, BIAS_F32>(ga, out_bf16, tn, st);
+  });
   return true;
 }
 

@@ -267,6 +267,7 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   g.bias_bf16 = bias_dtype == QSG_BF16;
   g.M = M; g.N = N; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.c = c;
   const bool bf16 = c_dtype == QSG_BF16;
+  if (M > 64 && launch_gemm_int8_fast(a, sa, b, sb, M, N, K, lda, ldb, bias, g.bias_bf16, c, c_dtype, ldc, st)) return;
   if (M <= 16) launch_few<1, 8>(g, bf16, st);
   else if (M <= 32) launch_few<2, 8>(g, bf16, st);
   else if (M <= 64) launch_few<4, 8>(g, bf16, st);

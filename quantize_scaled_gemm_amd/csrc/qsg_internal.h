@@ -91,6 +91,11 @@ void launch_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, 
 void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
                       int64_t K, int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype,
                       int64_t ldc, hipStream_t st);
+// 256x256 persistent kernel; returns false (and launches nothing) when the
+// problem is not eligible.
+bool launch_gemm_int8_fast(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N,
+                           int64_t K, int64_t lda, int64_t ldb, const void* bias, bool bias_bf16, void* c, int c_dtype,
+                           int64_t ldc, hipStream_t st);
 void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
                        int64_t ldq, void* c, int c_dtype, int64_t ldc, bool accumulate, hipStream_t st);
 void launch_swiglu_int8_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* a, int8_t* aq,

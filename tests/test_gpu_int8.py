@@ -203,6 +203,32 @@ def test_product_bias(q, M, N, K, bias):
     product(q, M, N, K, F32, bias)
 
 
+@pytest.mark.parametrize("out, bias", [(BF, None), (F32, None), (BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("M, N, K, pad", [
+    (4096, 2048, 512, 0), (2900, 4098, 256, 0), (4250, 4096, 768, 16),  # 128 tiles of 256 x 256, ragged, a tail launch
+    (8500, 4100, 1280, 32), (2900, 4097, 512, 0), (4000, 2304, 640, 0), (3000, 4096, 512, 8)])
+def test_large_product(q, M, N, K, pad, out, bias):
+    """Every output against exact sums, which a product in 64 bits gives."""
+    g = torch.Generator("cuda").manual_seed(M + N + K)
+    a = torch.randint(-128, 128, (M, K + pad), device="cuda", dtype=torch.int8, generator=g)[:, :K]
+    b = torch.randint(-128, 128, (N, K + pad), device="cuda", dtype=torch.int8, generator=g)[:, :K]
+    sa, sb = torch.rand(M, device="cuda", generator=g), torch.rand(N, device="cuda", generator=g)
+    bd = None if bias is None else (torch.randn(N, device="cuda", generator=g) * 1000).to(bias)
+    full = torch.full((M, N + 3), 7.0, device="cuda", dtype=out)
+    q.qsg_gemm_int8(a, sa, b, sb, full[:, :N], bias=bd)
+    c = (a.double() @ b.double().t()) * sa.double()[:, None] * sb.double()
+    p = c.abs()
+    if bd is not None:
+        c += bd.double()
+        p += bd.double().abs()
+    e = 2.0 ** -24 * (4 * p + c.abs())
+    assert ((full[:, :N].double() - c).abs() <= e + HALF[out] * (c.abs() + e)).all()
+    assert (full[:, N:] == 7).all()
+    dense = torch.empty((M, N), device="cuda", dtype=out)
+    q.qsg_gemm_int8(a, sa, b, sb, dense, bias=bd)
+    assert torch.equal(dense, full[:, :N])
+
+
 @pytest.mark.parametrize("pad", [1, 3, 16])
 @pytest.mark.parametrize("M, N, K", [(3, 50, 300), (50, 40, 256), (150, 140, 333)])
 def test_product_views(q, M, N, K, pad):
