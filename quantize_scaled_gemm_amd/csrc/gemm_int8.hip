@@ -12,6 +12,8 @@
 //   * everything else: 128 x 128 tiles through LDS.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "qsg_device.h"
 #include "qsg_internal.h"
 
@@ -25,6 +27,7 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 typedef int v4i_u __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
 
 struct Int8Args {
   const int8_t* a;
@@ -38,9 +41,31 @@ struct Int8Args {
   int64_t tiles_m;
 };
 
-// 16 bytes of a row of K bytes at k; what lies past its end is 0
+// v shifted down by n bytes (16 and more: nothing is left)
+__device__ __forceinline__ v4i shift_down(v4i v, int n) {
+  const int d = n >> 2;
+  uint32_t t[5];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = i; k < 4; ++k) w = d == k - i ? (uint32_t)v[k] : w;
+    t[i] = w;
+  }
+  t[4] = 0;
+  v4i r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = (int)__builtin_amdgcn_alignbyte(t[i + 1], t[i], n & 3);
+  return r;
+}
+
+// 16 bytes of a row of K bytes at k; what lies past its end is 0.  One load
+// without a branch where a row has 16 bytes: the last 16 of them, shifted.
 __device__ __forceinline__ v4i load_chunk(const int8_t* row, int64_t k, int64_t K) {
-  if (k + 16 <= K) return *reinterpret_cast<const v4i_u*>(row + k);
+  if (K >= 16) {
+    const int64_t at = k < K - 16 ? k : K - 16;
+    return shift_down(*reinterpret_cast<const v4i_u*>(row + at), (int)(k - at < 16 ? k - at : 16));
+  }
   v4i r = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 15; ++i)
@@ -54,16 +79,27 @@ __device__ __forceinline__ float bias_at(const Int8Args& g, int64_t n) {
                      : reinterpret_cast<const float*>(g.bias)[n];
 }
 
+// Scales and biases of 4 consecutive columns (past the last one: the last one's)
+struct Cols {
+  float s[4], c[4];
+  __device__ __forceinline__ void read(const Int8Args& g, int64_t n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = n + i < g.N ? n + i : g.N - 1;
+      s[i] = g.sb[at];
+      c[i] = bias_at(g, at);
+    }
+  }
+};
+
 // 4 consecutive outputs of row m from their sums
 template <bool OUT_BF16>
-__device__ __forceinline__ void store4(const Int8Args& g, int64_t m, int64_t n, const int (&sum)[4], float sa) {
+__device__ __forceinline__ void store4(const Int8Args& g, int64_t m, int64_t n, const int (&sum)[4], float sa,
+                                       const Cols& col) {
   if (m >= g.M || n >= g.N) return;
   float v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t at = n + i < g.N ? n + i : n;
-    v[i] = fmaf((float)sum[i] * sa, g.sb[at], bias_at(g, at));
-  }
+  for (int i = 0; i < 4; ++i) v[i] = fmaf((float)sum[i] * sa, col.s[i], col.c[i]);
   if constexpr (OUT_BF16) {
     uint16_t* p = reinterpret_cast<uint16_t*>(g.c) + m * g.ldc + n;
     const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
@@ -89,62 +125,224 @@ __device__ __forceinline__ void store4(const Int8Args& g, int64_t m, int64_t n, 
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-// MT x 16 rows of A against 16 rows of B.  Lane l holds row l % 16 of either
-// operand and, of a step of 128 K, bytes 32 (l / 16) .. +31 as two chunks of
-// two instructions: both operands split K between lanes alike, so every
-// product is made once.  The instruction takes (B, A), and lane l then holds
-// row l % 16 of A and columns 4 (l / 16) .. +3.
-template <int MT, int WAVES, bool OUT_BF16>
-__global__ __launch_bounds__(WAVES * 64) void gemm_int8_few_kernel(Int8Args g) {
-  __shared__ v4i red[WAVES][MT][64];
+// 16 rows of A against 16 rows of B, any alignment.  Lane l holds row l % 16
+// of either operand and, of a step of 128 K, bytes 32 (l / 16) .. +31 as two
+// chunks of two instructions: both operands split K between lanes alike, so
+// every product is made once.  The instruction takes (B, A), and lane l then
+// holds row l % 16 of A and columns 4 (l / 16) .. +3.  The workgroup's waves
+// split K; a wave takes 8 steps at a time, all of their loads first.
+constexpr int kFewWaves = 4, kFewSteps = 8;
+
+template <bool OUT_BF16>
+__global__ __launch_bounds__(kFewWaves * 64) void gemm_int8_few_kernel(Int8Args g) {
+  __shared__ v4i red[kFewWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int at = (lane >> 4) * 32;
+  // rows past the end read the last one; their results are not stored
+  const int64_t m = (lane & 15) < g.M ? (lane & 15) : g.M - 1;
+  const int64_t n = n0 + (lane & 15) < g.N ? n0 + (lane & 15) : g.N - 1;
+  const int8_t* a = g.a + m * g.lda;
+  const int8_t* b = g.b + n * g.ldb;
+  // read before the sums, so that a workgroup waits for memory once
+  const float sa = g.sa[m];
+  Cols cols;
+  cols.read(g, n0 + 4 * (lane >> 4));
+  v4i acc = {0, 0, 0, 0};
+  // C steps from s on
+  auto steps = [&](int64_t s, auto count) {
+    constexpr int C = decltype(count)::value;
+    v4i fb[C][2], fa[C][2];
+#pragma unroll
+    for (int u = 0; u < C; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fb[u][h] = *reinterpret_cast<const v4i_u*>(b + (s + u) * 128 + at + 16 * h);
+#pragma unroll
+    for (int u = 0; u < C; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) fa[u][h] = *reinterpret_cast<const v4i_u*>(a + (s + u) * 128 + at + 16 * h);
+#pragma unroll
+    for (int u = 0; u < C; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][h], fa[u][h], acc, 0, 0, 0);
+  };
+  const int64_t whole = g.K / 128, grouped = whole / kFewSteps * kFewSteps;
+  for (int64_t s = wave * kFewSteps; s < grouped; s += kFewWaves * kFewSteps)
+    steps(s, std::integral_constant<int, kFewSteps>{});
+  for (int64_t s = grouped + wave; s < whole; s += kFewWaves) steps(s, std::integral_constant<int, 1>{});
+  if (g.K % 128 && whole % kFewWaves == wave) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t k = whole * 128 + at + 16 * h;
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(load_chunk(b, k, g.K), load_chunk(a, k, g.K), acc, 0, 0, 0);
+    }
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+    v4i v = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += red[w][lane];
+    const int sum[4] = {v[0], v[1], v[2], v[3]};
+    store4<OUT_BF16>(g, lane & 15, n0 + 4 * (lane >> 4), sum, sa, cols);
+  }
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;  // past any resource below
+
+// s_waitcnt vmcnt(N) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt field");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+// Workgroup barrier without a memory fence (a fence would also wait for the
+// loads in flight); the waits it needs are explicit.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// the same behind this wave's own LDS accesses
+__device__ __forceinline__ void lds_barrier_lgkm() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// `most` rows from row0 on, as far as there are so many
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* p, int64_t row0, int64_t rows, int64_t ld,
+                                                            int most) {
+  int64_t n = rows - row0;
+  n = n < most ? n : most;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(p + row0 * ld), 0, (int)(n * ld), 0x00020000);
+}
+
+// The same with operands of whole 16 bytes.  Lanes that are neighbours load
+// different rows above, 16 bytes each, which the vector-memory path takes one
+// lane a clock; here a wave's loads cover whole 128-byte row segments and go to
+// LDS directly, into a ring of R steps that is the wave's own, so it waits for
+// its own loads only.  16-byte chunk c of row r is at position c ^ ring_swz(r):
+// of a fragment read (lane l: row l % 16, chunk l / 16 or 4 + l / 16) the lanes
+// that the LDS serves together (8p .. 8p+7 with 8p+32 .. 8p+39) then meet
+// distinct banks.
+__device__ __forceinline__ int ring_swz(int r) { return ((r >> 1) & 1) | ((r >> 3) & 1) << 1 | ((r >> 2) & 1) << 2; }
+
+template <int MT, int NT, int WAVES, int R, bool OUT_BF16>
+__global__ __launch_bounds__(WAVES * 64) void gemm_int8_ring_kernel(Int8Args g) {
+  constexpr int ROWS = 16 * (MT + NT), STEP = ROWS * 128, LOADS = STEP / 1024;
+  static_assert(MT * NT * 1024 <= STEP, "a wave's sums fit its part of a stage");
+  // distinct objects: reads of one stage wait for no load into another
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[WAVES * STEP];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[WAVES * STEP];
+  __shared__ __attribute__((aligned(1024))) uint8_t st2[R > 2 ? WAVES * STEP : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t st3[R > 3 ? WAVES * STEP : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t tm = blockIdx.x % g.tiles_m, tn = blockIdx.x / g.tiles_m;
-  const int64_t m0 = tm * (16 * MT), n0 = tn * 16;
-  // rows past the end read the last one; their results are not stored
-  const int64_t bn = n0 + (lane & 15) < g.N ? n0 + (lane & 15) : g.N - 1;
-  const int8_t* b = g.b + bn * g.ldb;
-  const int8_t* a[MT];
+  const int64_t m0 = tm * (16 * MT), n0 = tn * (16 * NT);
+  // load i of a step fills 1 KB: rows 8 i + lane / 8 (B's rows, then A's),
+  // position lane % 8
+  const int pr = lane >> 3;
+  const __amdgpu_buffer_rsrc_t ra = rows_rsrc(g.a, m0, g.M, g.lda, 16 * MT), rb = rows_rsrc(g.b, n0, g.N, g.ldb, 16 * NT);
+  int ch[2];
+  uint32_t va[2], vb[2];  // of rows 0..7 and 8..15; 16 rows further are 16 ld more
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + i * 16 + (lane & 15);
-    a[i] = g.a + (m < g.M ? m : g.M - 1) * g.lda;
+  for (int i = 0; i < 2; ++i) {
+    ch[i] = (lane & 7) ^ ring_swz(8 * i + pr);
+    va[i] = (8 * i + pr) * (uint32_t)g.lda + ch[i] * 16;
+    vb[i] = (8 * i + pr) * (uint32_t)g.ldb + ch[i] * 16;
   }
-  const int at = (lane >> 4) * 32;
-  v4i acc[MT];
+  const int K = (int)g.K, nk = (K + 127) / 128, rounds = (nk + WAVES - 1) / WAVES;
+  uint32_t mine = wave * STEP;
+  auto issue = [&](uint8_t* st, int round) {
+    const int k = (round * WAVES + wave) * 128;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = v4i{0, 0, 0, 0};
-  const int64_t whole = g.K / 128;
-#pragma unroll 4
-  for (int64_t s = wave; s < whole; s += WAVES) {
-    const int64_t k = s * 128 + at;
-    const v4i b0 = *reinterpret_cast<const v4i_u*>(b + k), b1 = *reinterpret_cast<const v4i_u*>(b + k + 16);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const v4i a0 = *reinterpret_cast<const v4i_u*>(a[i] + k), a1 = *reinterpret_cast<const v4i_u*>(a[i] + k + 16);
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a0, acc[i], 0, 0, 0);
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1, acc[i], 0, 0, 0);
+    for (int i = 0; i < 2 * NT; ++i) {
+      const uint32_t off = k + ch[i & 1] * 16 < K ? vb[i & 1] + (uint32_t)(i >> 1) * 16 * (uint32_t)g.ldb + k : OUT_OF_RANGE;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(st + mine + i * 1024), 16, off, 0, 0, 0);
     }
-  }
-  if (g.K % 128 && whole % WAVES == wave) {
-    const int64_t k = whole * 128 + at;
-    const v4i b0 = load_chunk(b, k, g.K), b1 = load_chunk(b, k + 16, g.K);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const v4i a0 = load_chunk(a[i], k, g.K), a1 = load_chunk(a[i], k + 16, g.K);
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a0, acc[i], 0, 0, 0);
-      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1, acc[i], 0, 0, 0);
+    for (int i = 0; i < 2 * MT; ++i) {
+      const uint32_t off = k + ch[i & 1] * 16 < K ? va[i & 1] + (uint32_t)(i >> 1) * 16 * (uint32_t)g.lda + k : OUT_OF_RANGE;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(st + mine + (2 * NT + i) * 1024), 16, off, 0, 0, 0);
     }
-  }
+  };
+  // scales of the tiles that this wave joins in the end
+  constexpr int PER = (MT * NT + WAVES - 1) / WAVES;
+  Cols cols[PER];
+  float sa[PER];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) red[wave][i][lane] = acc[i];
+  for (int k = 0; k < PER; ++k) {
+    const int t = wave + k * WAVES;
+    const int64_t m = m0 + t / NT * 16 + (lane & 15);
+    sa[k] = g.sa[m < g.M ? m : g.M - 1];
+    cols[k].read(g, n0 + t % NT * 16 + 4 * (lane >> 4));
+  }
+  v4i acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  int fo[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) fo[h] = (lane & 15) * 128 + (((4 * h + (lane >> 4)) ^ ring_swz(lane & 15)) * 16);
+  auto step = [&](uint8_t* st, int round) {
+    wait_vm<(R - 1) * LOADS>();
+    asm volatile("" ::: "memory");
+    v4i fb[NT][2], fa[MT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[j][h] = *reinterpret_cast<const v4i*>(st + mine + j * 2048 + fo[h]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i][h] = *reinterpret_cast<const v4i*>(st + mine + (NT + i) * 2048 + fo[h]);
+    }
+    // the reads have returned before the loads that replace what they read
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    issue(st, round + R);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j][h], fa[i][h], acc[i][j], 0, 0, 0);
+  };
+  issue(st0, 0);
+  issue(st1, 1);
+  if constexpr (R > 2) issue(st2, 2);
+  if constexpr (R > 3) issue(st3, 3);
+  int r = 0;
+  for (; r + R <= rounds; r += R) {
+    step(st0, r);
+    step(st1, r + 1);
+    if constexpr (R > 2) step(st2, r + 2);
+    if constexpr (R > 3) step(st3, r + 3);
+  }
+  if (r < rounds) step(st0, r++);
+  if (R > 2 && r < rounds) step(st1, r++);
+  if constexpr (R > 3) {
+    if (r < rounds) step(st2, r++);
+  }
+  wait_vm<0>();  // the loads past the last step have landed, in this wave's part alone
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *reinterpret_cast<v4i*>(st0 + mine + (i * NT + j) * 1024 + lane * 16) = acc[i][j];
   __syncthreads();
-  for (int i = wave; i < MT; i += WAVES) {
-    v4i t = red[0][i][lane];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) t += red[w][i][lane];
-    const int64_t m = m0 + i * 16 + (lane & 15);
-    const int sum[4] = {t[0], t[1], t[2], t[3]};
-    store4<OUT_BF16>(g, m, n0 + 4 * (lane >> 4), sum, m < g.M ? g.sa[m] : 0.0f);
+  for (int k = 0; k < PER; ++k) {
+    const int t = wave + k * WAVES;
+    if (t < MT * NT) {
+      v4i v = *reinterpret_cast<const v4i*>(st0 + t * 1024 + lane * 16);
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const v4i*>(st0 + w * STEP + t * 1024 + lane * 16);
+      const int sum[4] = {v[0], v[1], v[2], v[3]};
+      store4<OUT_BF16>(g, m0 + t / NT * 16 + (lane & 15), n0 + t % NT * 16 + 4 * (lane >> 4), sum, sa[k], cols[k]);
+    }
   }
 }
 
@@ -158,102 +356,347 @@ constexpr int TB = 128;  // rows of either operand, and bytes of K, of a tile
 // on distinct banks
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
-template <bool OUT_BF16>
-__global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][TB * TB];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
-  const int64_t m0 = (blockIdx.x % g.tiles_m) * TB, n0 = (blockIdx.x / g.tiles_m) * TB;
-  // thread: chunk tid % 8 of rows tid / 8 + 32 i of both operands
-  const int ch = tid & 7, r0 = tid >> 3;
-  const int8_t* pa[4];
-  const int8_t* pb[4];
+// Scales of a wave's 32 NI x 32 NJ outputs from row m0 and column n0 on (read
+// before the K loop, which hides their latency): lane l holds row l % 32 and,
+// of group q, columns 8 q + 4 (l / 32) .. +3.
+template <int NI, int NJ>
+struct TileScales {
+  float sa[NI];
+  Cols col[NJ][4];
+  __device__ __forceinline__ TileScales(const Int8Args& g, int64_t m0, int64_t n0, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + r0 + 32 * i, n = n0 + r0 + 32 * i;
-    pa[i] = g.a + (m < g.M ? m : g.M - 1) * g.lda;
-    pb[i] = g.b + (n < g.N ? n : g.N - 1) * g.ldb;
-  }
-  const int64_t nk = (g.K + TB - 1) / TB;
-  v4i ra[4], rb[4];
-  auto fetch = [&](int64_t kt) {
-    const int64_t k = kt * TB + ch * 16;
-    if ((kt + 1) * TB <= g.K) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ra[i] = *reinterpret_cast<const v4i_u*>(pa[i] + k);
-        rb[i] = *reinterpret_cast<const v4i_u*>(pb[i] + k);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ra[i] = load_chunk(pa[i], k, g.K);
-        rb[i] = load_chunk(pb[i], k, g.K);
-      }
+    for (int i = 0; i < NI; ++i) {
+      const int64_t m = m0 + i * 32 + (lane & 31);
+      sa[i] = g.sa[m < g.M ? m : g.M - 1];
     }
-  };
-  auto put = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = r0 + 32 * i, p = r * TB + ((ch ^ swz(r)) * 16);
-      *reinterpret_cast<v4i*>(lds[st][0] + p) = ra[i];
-      *reinterpret_cast<v4i*>(lds[st][1] + p) = rb[i];
-    }
-  };
-  v16i acc[2][2];
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  if (nk > 0) {
-    fetch(0);
-    put(0);
+      for (int q = 0; q < 4; ++q) col[j][q].read(g, n0 + j * 32 + 8 * q + 4 * (lane >> 5));
   }
-  __syncthreads();
-  for (int64_t kt = 0; kt < nk; ++kt) {
-    const int st = (int)(kt & 1);
-    if (kt + 1 < nk) fetch(kt + 1);
+};
+
+// The outputs, 32 rows at a time through the wave's own part of LDS, from which
+// they leave in whole row segments of 32 NJ outputs (straight from the
+// registers a store would write 8 bytes of each of 32 rows).
+template <bool OUT_BF16, int NJ>
+constexpr int kTilePitch = 32 * NJ * (OUT_BF16 ? 2 : 4) + 16;
+template <bool OUT_BF16, int NI, int NJ>
+__device__ __forceinline__ void store_tile(const Int8Args& g, const v16i (&acc)[NI][NJ], const TileScales<NI, NJ>& sc,
+                                           int64_t m0, int64_t n0, int lane, uint8_t* lds) {
+  constexpr int ESZ = OUT_BF16 ? 2 : 4, PITCH = kTilePitch<OUT_BF16, NJ>;
+  constexpr int LPR = 32 * NJ * ESZ / 16, RPI = 64 / LPR;  // lanes of a row, rows of a store
+  const int64_t n = n0 + lane % LPR * (16 / ESZ);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      v4i fa[2], fb[2];
+  for (int i = 0; i < NI; ++i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = 2 * s + (lane >> 5);
-        const int ar = wm * 64 + i * 32 + (lane & 31), br = wn * 64 + i * 32 + (lane & 31);
-        fa[i] = *reinterpret_cast<const v4i*>(lds[st][0] + ar * TB + ((c ^ swz(ar)) * 16));
-        fb[i] = *reinterpret_cast<const v4i*>(lds[st][1] + br * TB + ((c ^ swz(br)) * 16));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
-    if (kt + 1 < nk) put(st ^ 1);
-    __syncthreads();
-  }
-  // lane l holds row l % 32 and, of group q, columns 8 q + 4 (l / 32) .. +3
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = m0 + wm * 64 + i * 32 + (lane & 31);
-    const float sa = m < g.M ? g.sa[m] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int sum[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        store4<OUT_BF16>(g, m, n0 + wn * 64 + j * 32 + 8 * q + 4 * (lane >> 5), sum, sa);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = fmaf((float)acc[i][j][4 * q + e] * sc.sa[i], sc.col[j][q].s[e], sc.col[j][q].c[e]);
+        uint8_t* p = lds + (lane & 31) * PITCH + (j * 32 + 8 * q + 4 * (lane >> 5)) * ESZ;
+        if constexpr (OUT_BF16) *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
       }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // other lanes' writes
+#pragma unroll
+    for (int k = 0; k < 32 / RPI; ++k) {
+      const int r = k * RPI + lane / LPR;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(lds + r * PITCH + lane % LPR * 16);
+      const int64_t m = m0 + i * 32 + r;
+      if (m < g.M) {
+        uint8_t* p = reinterpret_cast<uint8_t*>(g.c) + (m * g.ldc + n) * ESZ;
+        if (n + 16 / ESZ <= g.N) {
+          *reinterpret_cast<u32x4_e*>(p) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16 / ESZ; ++e)
+            if (n + e < g.N) {
+              if constexpr (OUT_BF16) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+              else reinterpret_cast<uint32_t*>(p)[e] = w[e];
+            }
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the reads, before the next rows' writes
   }
 }
 
-template <int MT, int WAVES>
-void launch_few(Int8Args g, bool bf16, hipStream_t st) {
+// Any alignment: through registers, two K tiles ahead.  A K tile is four phases
+// of 32 K, and a phase's fragments are read during the phase before; the
+// barrier behind which the next K tile is there lies before the last phase,
+// whose instructions cover the first reads from it.
+template <int TM, int TN, bool OUT_BF16>
+__global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
+  constexpr int NI = TM / 64, NJ = TN / 64, LA = TM / 32, LB = TN / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[(TM + TN) * TB];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[(TM + TN) * TB];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t m0 = (blockIdx.x % g.tiles_m) * TM, n0 = (blockIdx.x / g.tiles_m) * TN;
+  // thread: chunk tid % 8 of rows tid / 8 + 32 i of both operands
+  const int ch = tid & 7, r0 = tid >> 3;
+  const int8_t* pa[LA];
+  const int8_t* pb[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i) pa[i] = g.a + (m0 + r0 + 32 * i < g.M ? m0 + r0 + 32 * i : g.M - 1) * g.lda;
+#pragma unroll
+  for (int i = 0; i < LB; ++i) pb[i] = g.b + (n0 + r0 + 32 * i < g.N ? n0 + r0 + 32 * i : g.N - 1) * g.ldb;
+  const TileScales<NI, NJ> scales(g, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane);
+  const int K = (int)g.K, nk = (K + TB - 1) / TB;
+  struct Regs {
+    v4i a[LA], b[LB];
+  };
+  Regs x0, x1;
+  auto fetch = [&](Regs& x, int kt) {
+    const int k = kt * TB + ch * 16;
+    if ((kt + 1) * TB <= K) {
+#pragma unroll
+      for (int i = 0; i < LA; ++i) x.a[i] = *reinterpret_cast<const v4i_u*>(pa[i] + k);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) x.b[i] = *reinterpret_cast<const v4i_u*>(pb[i] + k);
+    } else if (kt < nk) {
+#pragma unroll
+      for (int i = 0; i < LA; ++i) x.a[i] = load_chunk(pa[i], k, K);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) x.b[i] = load_chunk(pb[i], k, K);
+    }
+  };
+  auto put = [&](uint8_t* st, const Regs& x) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int r = r0 + 32 * i;
+      *reinterpret_cast<v4i*>(st + r * TB + ((ch ^ swz(r)) * 16)) = x.a[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int r = r0 + 32 * i;
+      *reinterpret_cast<v4i*>(st + (TM + r) * TB + ((ch ^ swz(r)) * 16)) = x.b[i];
+    }
+  };
+  int fo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) fo[s] = (lane & 31) * TB + (((2 * s + (lane >> 5)) ^ swz(lane & 31)) * 16);
+  v16i acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  v4i fa[2][NI], fb[2][NJ];
+  auto read = [&](const uint8_t* st, int s) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) fa[s & 1][i] = *reinterpret_cast<const v4i*>(st + (wm * (TM / 2) + i * 32) * TB + fo[s]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      fb[s & 1][j] = *reinterpret_cast<const v4i*>(st + TM * TB + (wn * (TN / 2) + j * 32) * TB + fo[s]);
+  };
+  // K tile kt in `cur`; kt + 1 goes from `ready` to `next`, kt + 2 is fetched into `other`
+  auto step = [&](const uint8_t* cur, uint8_t* next, const Regs& ready, Regs& other, int kt) {
+    fetch(other, kt + 2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s < 3) {
+        read(cur, s + 1);
+      } else {
+        lds_barrier_lgkm();
+        read(next, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s & 1][j], fa[s & 1][i], acc[i][j], 0, 0, 0);
+      if (s == 1) put(next, ready);
+    }
+  };
+  fetch(x0, 0);
+  fetch(x1, 1);
+  put(st0, x0);
+  lds_barrier_lgkm();
+  read(st0, 0);
+  int kt = 0;
+  for (; kt + 2 <= nk; kt += 2) {
+    step(st0, st1, x1, x0, kt);
+    step(st1, st0, x0, x1, kt + 1);
+  }
+  if (kt < nk) step(st0, st1, x1, x0, kt);
+  lds_barrier_lgkm();  // no wave reads a stage any more
+  constexpr int PART = 32 * kTilePitch<OUT_BF16, NJ>;
+  static_assert(2 * PART <= sizeof(st0), "two waves' rows fit a stage");
+  store_tile<OUT_BF16, NI, NJ>(g, acc, scales, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane,
+                               (wave < 2 ? st0 : st1) + (wave & 1) * PART);
+}
+
+// TM x TN tiles of operands of whole 16 bytes: the loads go to LDS directly, S
+// - 1 K tiles ahead in a ring of S stages.  (Through registers and one tile
+// ahead, as above, a workgroup a CU waits for each tile's loads.)  A K tile is
+// four phases of 32 K, and a phase's fragments are read during the phase
+// before; the barrier behind which the next K tile is there lies before the
+// last phase, whose instructions cover the first reads from it.
+template <int TM, int TN, int S, bool OUT_BF16>
+__global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
+  constexpr int NI = TM / 64, NJ = TN / 64;   // 32 x 32 tiles of a wave
+  constexpr int LA = TM / 32, LB = TN / 32;   // loads of a wave and K tile
+  constexpr int STAGE = (TM + TN) * TB, WAIT = (S - 2) * (LA + LB);
+  // distinct objects: reads of one stage wait for no load into another; A's
+  // rows of 128 bytes, then B's
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st3[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st4[S > 4 ? STAGE : 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  // Workgroups go to the 8 XCDs in turn: each XCD gets a contiguous part of an
+  // order that walks groups of 8 tile-rows column by column
+  const uint32_t T = gridDim.x, tiles_m = (uint32_t)g.tiles_m, tiles_n = T / tiles_m;
+  const uint32_t at = T % 8 == 0 ? blockIdx.x % 8 * (T / 8) + blockIdx.x / 8 : blockIdx.x;
+  const uint32_t y0 = at / (8 * tiles_n) * 8, high = tiles_m - y0 < 8 ? tiles_m - y0 : 8;
+  const uint32_t in = at - y0 * tiles_n;
+  const int64_t m0 = (int64_t)(y0 + in % high) * TM, n0 = (int64_t)(in / high) * TN;
+
+  // load i of a wave fills the 1 KB block i * 4 + wave of an operand: rows
+  // 8 (i * 4 + wave) + lane / 8, position lane % 8
+  const int pr = lane >> 3, ch = (lane & 7) ^ pr ^ (wave & 1);  // swz(row), the same for every i
+  const uint32_t va = (wave * 8 + pr) * (uint32_t)g.lda + ch * 16, vb = (wave * 8 + pr) * (uint32_t)g.ldb + ch * 16;
+  const __amdgpu_buffer_rsrc_t ra = rows_rsrc(g.a, m0, g.M, g.lda, TM), rb = rows_rsrc(g.b, n0, g.N, g.ldb, TN);
+  const TileScales<NI, NJ> scales(g, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane);
+  const int K = (int)g.K, nk = (K + TB - 1) / TB;
+  // load i (of A's and then B's) of K tile kt; past the last row, or the
+  // last 16 bytes of a row, 0 is read
+  auto issue1 = [&](uint8_t* dst, int kt, int i) {
+    const bool is_a = i < LA;
+    const int j = is_a ? i : i - LA;
+    const uint32_t off = kt * TB + ch * 16 < K ? kt * TB : OUT_OF_RANGE;
+    const uint32_t v = is_a ? va + j * 32 * (uint32_t)g.lda : vb + j * 32 * (uint32_t)g.ldb;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb,
+                                             (lds_ptr_t)(dst + (is_a ? 0 : TM * TB) + (j * 4 + wave) * 1024), 16, v + off,
+                                             0, 0, 0);
+  };
+  auto issue = [&](uint8_t* dst, int kt) {
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) issue1(dst, kt, i);
+  };
+  int fo[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) fo[s] = (lane & 31) * TB + (((2 * s + (lane >> 5)) ^ swz(lane & 31)) * 16);
+  v16i acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  v4i fa[2][NI], fb[2][NJ];
+  auto read = [&](const uint8_t* st, int s) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) fa[s & 1][i] = *reinterpret_cast<const v4i*>(st + (wm * (TM / 2) + i * 32) * TB + fo[s]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      fb[s & 1][j] = *reinterpret_cast<const v4i*>(st + TM * TB + (wn * (TN / 2) + j * 32) * TB + fo[s]);
+  };
+  // K tile kt in `cur`, the next one in `next`; `dst` held the one before
+  auto step = [&](const uint8_t* cur, const uint8_t* next, uint8_t* dst, int kt) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s < 3) {
+        read(cur, s + 1);
+      } else {
+        wait_vm<WAIT>();
+        lds_barrier();
+        read(next, 0);
+      }
+      // a third of the loads in each of the first three phases
+      constexpr int L3 = (LA + LB + 2) / 3;
+      if (s < 3) {
+#pragma unroll
+        for (int i = s * L3; i < (s + 1) * L3 && i < LA + LB; ++i) issue1(dst, kt + S - 1, i);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[s & 1][j], fa[s & 1][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < NI * NJ; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (NI + NJ + NI * NJ - 1) / (NI * NJ), 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  issue(st0, 0);
+  issue(st1, 1);
+  issue(st2, 2);
+  if constexpr (S > 4) issue(st3, 3);
+  wait_vm<WAIT>();
+  lds_barrier();
+  read(st0, 0);
+  int kt = 0;
+  if constexpr (S == 4) {
+    for (; kt + 4 <= nk; kt += 4) {
+      step(st0, st1, st3, kt);
+      step(st1, st2, st0, kt + 1);
+      step(st2, st3, st1, kt + 2);
+      step(st3, st0, st2, kt + 3);
+    }
+    if (kt < nk) step(st0, st1, st3, kt++);
+    if (kt < nk) step(st1, st2, st0, kt++);
+    if (kt < nk) step(st2, st3, st1, kt++);
+  } else {
+    for (; kt + 5 <= nk; kt += 5) {
+      step(st0, st1, st4, kt);
+      step(st1, st2, st0, kt + 1);
+      step(st2, st3, st1, kt + 2);
+      step(st3, st4, st2, kt + 3);
+      step(st4, st0, st3, kt + 4);
+    }
+    if (kt < nk) step(st0, st1, st4, kt++);
+    if (kt < nk) step(st1, st2, st0, kt++);
+    if (kt < nk) step(st2, st3, st1, kt++);
+    if (kt < nk) step(st3, st4, st2, kt++);
+  }
+  wait_vm<0>();  // the loads past the last K tile have landed, and
+  lds_barrier();  // no wave reads a stage any more
+  constexpr int PART = 32 * kTilePitch<OUT_BF16, NJ>;
+  static_assert(2 * PART <= STAGE, "two waves' rows fit a stage");
+  store_tile<OUT_BF16, NI, NJ>(g, acc, scales, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane,
+                               (wave < 2 ? st0 : st1) + (wave & 1) * PART);
+}
+
+void launch_few(const Int8Args& g, bool bf16, hipStream_t st) {
+  const dim3 grid((unsigned)((g.N + 15) / 16)), block(kFewWaves * 64);
+  if (bf16) hipLaunchKernelGGL(gemm_int8_few_kernel<true>, grid, block, 0, st, g);
+  else hipLaunchKernelGGL(gemm_int8_few_kernel<false>, grid, block, 0, st, g);
+}
+
+template <int MT, int NT, int WAVES, int R>
+void launch_ring(Int8Args g, bool bf16, hipStream_t st) {
   g.tiles_m = (g.M + 16 * MT - 1) / (16 * MT);
-  const dim3 grid((unsigned)(g.tiles_m * ((g.N + 15) / 16))), block(WAVES * 64);
-  if (bf16) hipLaunchKernelGGL((gemm_int8_few_kernel<MT, WAVES, true>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((gemm_int8_few_kernel<MT, WAVES, false>), grid, block, 0, st, g);
+  const dim3 grid((unsigned)(g.tiles_m * ((g.N + 16 * NT - 1) / (16 * NT)))), block(WAVES * 64);
+  if (bf16) hipLaunchKernelGGL((gemm_int8_ring_kernel<MT, NT, WAVES, R, true>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((gemm_int8_ring_kernel<MT, NT, WAVES, R, false>), grid, block, 0, st, g);
+}
+
+template <int TM, int TN>
+void launch_any(Int8Args g, bool bf16, hipStream_t st) {
+  g.tiles_m = (g.M + TM - 1) / TM;
+  const dim3 grid((unsigned)(g.tiles_m * ((g.N + TN - 1) / TN)));
+  if (bf16) hipLaunchKernelGGL((gemm_int8_kernel<TM, TN, true>), grid, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((gemm_int8_kernel<TM, TN, false>), grid, dim3(256), 0, st, g);
+}
+
+template <int TM, int TN, int S>
+void launch_tile(Int8Args g, bool bf16, hipStream_t st) {
+  g.tiles_m = (g.M + TM - 1) / TM;
+  const dim3 grid((unsigned)(g.tiles_m * ((g.N + TN - 1) / TN)));
+  if (bf16) hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, S, true>), grid, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, S, false>), grid, dim3(256), 0, st, g);
 }
 
 }  // namespace
@@ -268,15 +711,24 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   g.M = M; g.N = N; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.c = c;
   const bool bf16 = c_dtype == QSG_BF16;
   if (M > 64 && launch_gemm_int8_fast(a, sa, b, sb, M, N, K, lda, ldb, bias, g.bias_bf16, c, c_dtype, ldc, st)) return;
-  if (M <= 16) launch_few<1, 8>(g, bf16, st);
-  else if (M <= 32) launch_few<2, 8>(g, bf16, st);
-  else if (M <= 64) launch_few<4, 8>(g, bf16, st);
-  else {
-    g.tiles_m = (M + TB - 1) / TB;
-    const dim3 grid((unsigned)(g.tiles_m * ((N + TB - 1) / TB)));
-    if (bf16) hipLaunchKernelGGL(gemm_int8_kernel<true>, grid, dim3(256), 0, st, g);
-    else hipLaunchKernelGGL(gemm_int8_kernel<false>, grid, dim3(256), 0, st, g);
+  // direct loads: whole chunks, 31-bit offsets in 128 rows
+  const bool dma = (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && K % 16 == 0 &&
+                   K > 0 && lda < (1 << 24) && ldb < (1 << 24);
+  auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
+  if (!dma) {
+    if (M > 64 && tiles(128, 128) >= 192) launch_any<128, 128>(g, bf16, st);
+    else if (M > 16 || tiles(64, 64) >= 100) launch_any<64, 64>(g, bf16, st);
+    else launch_few(g, bf16, st);
+    return;
   }
+  if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128, 4>(g, bf16, st);
+  else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128, 4>(g, bf16, st);
+  else if (M > 32 && tiles(64, 64) >= 100) launch_tile<64, 64, 4>(g, bf16, st);
+  else if (M <= 4 && N >= 12288) launch_few(g, bf16, st);
+  else if (M <= 16 && N >= 12288) launch_ring<1, 2, 4, 2>(g, bf16, st);
+  else if (M <= 16) launch_ring<1, 1, 4, 4>(g, bf16, st);
+  else if (M <= 32 && N < 12288) launch_ring<2, 1, 4, 3>(g, bf16, st);
+  else launch_ring<2, 2, 4, 2>(g, bf16, st);
 }
 
 }  // namespace qsg
