@@ -27,9 +27,12 @@ __device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uin
 __device__ __forceinline__ float widen(float v) { return v; }
 
 // 8 consecutive values, of which the first n (0..8) are there; the rest are 0.
+// ONCE: nothing reads them again.
+template <bool ONCE = true>
 __device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p, int n) {
   if (n >= 8) {
-    const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(p));
+    const u32x4 u = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_e*>(p))
+                         : *reinterpret_cast<const u32x4_e*>(p);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
@@ -38,6 +41,7 @@ __device__ __forceinline__ void load8(float (&v)[8], const uint16_t* p, int n) {
     for (int i = 0; i < 8; ++i) v[i] = i < n ? widen(p[i]) : 0.0f;
   }
 }
+template <bool ONCE = true>
 __device__ __forceinline__ void load8(float (&v)[8], const float* p, int n) {
   if (n >= 8) {
     const u32x4 a = *reinterpret_cast<const u32x4_e*>(p), b = *reinterpret_cast<const u32x4_e*>(p + 4);
@@ -221,6 +225,57 @@ __global__ __launch_bounds__(1024) void int8_long_row_kernel(QuantArgs a) {
   if (threadIdx.x == 0) a.s[blockIdx.x] = s.s;
 }
 
+// The row-wise copy with the columns' maxima of the transposed one: a workgroup
+// takes every a.parts-th row, keeps the maxima of a thread's columns in
+// registers, and leaves them as one part.  The next row is loaded while a row
+// is worked on.  Plain loads: the second pass reads x again, and what is still
+// in the cache then comes from there.
+template <typename In, int TPR, int CH>
+__global__ __launch_bounds__(TPR) void int8_row_col_kernel(QuantArgs a) {
+  __shared__ uint32_t red[2][TPR / 64];
+  const int t = threadIdx.x, cols = (int)a.cols;
+  uint32_t m[CH][8] = {};
+  float v[CH][8], w[CH][8];
+  auto load = [&](float (&d)[CH][8], int64_t row) {
+    const In* x = reinterpret_cast<const In*>(a.x) + row * a.ld;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) load8<false>(d[i], x + (i * TPR + t) * 8, row < a.rows ? cols - (i * TPR + t) * 8 : 0);
+  };
+  int turn = 0;
+  auto work = [&](const float (&d)[CH][8], int64_t row) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t b = __float_as_uint(d[i][k]) & 0x7FFFFFFFu;
+        m[i][k] = umax_u32(m[i][k], b);
+        top = umax_u32(top, b);
+      }
+    const Scale s = scale_of(row_max<TPR>(top, red[turn]));
+    turn ^= 1;
+    int8_t* q = a.q + row * a.cols;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) store8(q + (i * TPR + t) * 8, codes8(d[i], s), cols - (i * TPR + t) * 8);
+    if (t == 0) a.s[row] = s.s;
+  };
+  int64_t row = blockIdx.x;
+  load(v, row);
+  for (; row < a.rows; row += 2 * a.parts) {
+    load(w, row + a.parts);
+    work(v, row);
+    if (row + a.parts >= a.rows) break;
+    load(v, row + 2 * a.parts);
+    work(w, row + a.parts);
+  }
+  uint32_t* part = reinterpret_cast<uint32_t*>(a.part) + blockIdx.x * a.cols;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if ((i * TPR + t) * 8 + k < cols) part[(i * TPR + t) * 8 + k] = m[i][k];
+}
+
 // ---------------------------------------------------------------------------
 // transposed copy: the columns' maxima, their scales, the codes
 // ---------------------------------------------------------------------------
@@ -252,19 +307,27 @@ __global__ __launch_bounds__(256) void int8_colmax_kernel(QuantArgs a) {
   }
 }
 
-// 64 columns a workgroup, 4 waves over the parts
-__global__ __launch_bounds__(256) void int8_colscale_kernel(QuantArgs a) {
-  __shared__ uint32_t red[4][64];
+// 64 columns a workgroup, 16 waves over the parts, 8 loads of a wave in flight
+__global__ __launch_bounds__(1024) void int8_colscale_kernel(QuantArgs a) {
+  __shared__ uint32_t red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (col < a.cols ? col : a.cols - 1);
   uint32_t m = 0;
-  if (col < a.cols)
-    for (int p = wave; p < a.parts; p += 4)
-      m = umax_u32(m, reinterpret_cast<const uint32_t*>(a.part)[(int64_t)p * a.cols + col]);
+  for (int k = wave; k < a.parts; k += 128) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[(int64_t)(k + 16 * i < a.parts ? k + 16 * i : k) * a.cols];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = umax_u32(m, v[i]);
+  }
   red[wave][lane] = m;
   __syncthreads();
-  if (wave == 0 && col < a.cols)
-    a.st[col] = scale_of(umax_u32(umax_u32(red[0][lane], red[1][lane]), umax_u32(red[2][lane], red[3][lane]))).s;
+  if (wave == 0 && col < a.cols) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) m = umax_u32(m, red[w][lane]);
+    a.st[col] = scale_of(m).s;
+  }
 }
 
 // A tile of 128 rows x 64 columns: a thread encodes 4 rows x 8 columns and
@@ -274,8 +337,10 @@ constexpr int kColRow = 33;  // words of an LDS column: 32, and one that spreads
 template <typename In>
 __global__ __launch_bounds__(256) void int8_col_kernel(QuantArgs a) {
   __shared__ uint32_t tile[64 * kColRow];
-  const int64_t tile_rows = (a.rows + 127) / 128, at = a.tile0 + blockIdx.x;
-  const int64_t r0 = at % tile_rows * 128, c0 = at / tile_rows * 64;
+  const int64_t tile_rows = (a.rows + 127) / 128, tile_cols = (a.cols + 63) / 64;
+  // the last rows first: the pass before read them last
+  const int64_t at = tile_rows * tile_cols - 1 - (a.tile0 + blockIdx.x);
+  const int64_t r0 = at / tile_cols * 128, c0 = at % tile_cols * 64;
   const int ch = threadIdx.x & 7, rg = threadIdx.x >> 3;
   const int64_t c = c0 + ch * 8;
   const int n = left8(a.cols, c);
@@ -338,8 +403,15 @@ void launch_rows(const QuantArgs& all, hipStream_t st) {
 
 template <typename In>
 void launch_quantize(const QuantArgs& a, hipStream_t st) {
-  // by the scales: an empty copy may have no address
-  if (a.s) {
+  // both copies of rows that 256 or 512 threads hold: one pass for the rows and
+  // the columns' maxima
+  const bool fused = a.q && a.qt && a.cols > 2048 && a.cols <= 16384;
+  if (fused) {
+    auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(a.parts), dim3(threads), 0, st, a); };
+    if (a.cols <= 4096) go(int8_row_col_kernel<In, 512, 1>, 512);
+    else if (a.cols <= 8192) go(int8_row_col_kernel<In, 512, 2>, 512);
+    else go(int8_row_col_kernel<In, 1024, 2>, 1024);
+  } else if (a.s) {  // by the scales: an empty copy may have no address
     if (a.cols <= 256) launch_rows<In, 16, 2>(a, st);
     else if (a.cols <= 1024) launch_rows<In, 64, 2>(a, st);
     else if (a.cols <= 2048) launch_rows<In, 64, 4>(a, st);
@@ -350,9 +422,9 @@ void launch_quantize(const QuantArgs& a, hipStream_t st) {
     else launch_rows<In, 1024, 0>(a, st);
   }
   if (a.st && a.cols > 0) {
-    if (a.rows > 0)
+    if (a.rows > 0 && !fused)
       hipLaunchKernelGGL(int8_colmax_kernel<In>, dim3((unsigned)((a.cols + 511) / 512), a.parts), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(int8_colscale_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(int8_colscale_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, st, a);
     in_pieces((a.rows + 127) / 128 * ((a.cols + 63) / 64), 1, [&](int64_t t, int64_t n) {
       QuantArgs b = a;
       b.tile0 = t;
@@ -361,7 +433,14 @@ void launch_quantize(const QuantArgs& a, hipStream_t st) {
   }
 }
 
-int quantize_parts(int64_t rows) { return (int)(rows < kMostParts ? rows : kMostParts); }
+// Groups of rows whose column maxima are joined by a kernel of their own: what
+// fills the chip, as far as each has 16 rows to spread the join's traffic over
+// (4096 x 14336 fp32: 256 groups 117 us, 512 131; 14336 x 4096: 111 either
+// way; 16384 x 7168 bf16: 256 groups 210, 512 168).
+int quantize_parts(int64_t rows) {
+  const int64_t some = rows < 256 ? rows : 256;
+  return (int)(rows / 16 < some ? some : rows / 16 < kMostParts ? rows / 16 : kMostParts);
+}
 
 // ---------------------------------------------------------------------------
 // gated activation
