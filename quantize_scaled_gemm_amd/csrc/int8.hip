@@ -25,6 +25,8 @@ constexpr int kBlock = 128;  // neighbours that share a scale of the kept activa
 
 __device__ __forceinline__ float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.0f); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // 8 consecutive values, of which the first n (0..8) are there; the rest are 0.
 // ONCE: nothing reads them again.
@@ -507,37 +509,66 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
 }
 
-// Codes and scale of one block, held by 16 neighbouring lanes.
-__device__ __forceinline__ void keep_block(const float (&v)[8], int8_t* ck, float* cs, int n, bool first) {
-  const Scale s = scale_of(group_max_u32<0xF>(amax8(v, 0)));
-  store8(ck, codes8(v, s), n);
-  if (first) *cs = s.s;
+// Where a group of 16 lanes is in a matrix of blocks of 128: its lanes take
+// the block's whole chunks of 8, and of a row's last block the up to 7 values
+// behind its last whole chunk, one to a lane (each in its own loads, they cost
+// a wave 7 of every kind).
+struct BlockAt {
+  int64_t row, b, c;  // block b; this lane's chunk begins at c
+  bool whole, one;    // the chunk is there; so is a value at `e`
+  int64_t e;
+  __device__ __forceinline__ BlockAt(const GluArgs& a, int64_t row_, int64_t b_, int t) : row(row_), b(b_) {
+    c = b * kBlock + t * 8;
+    whole = c + 8 <= a.cols;
+    e = (a.cols & ~(int64_t)7) + t;
+    one = b == a.nb - 1 && e < a.cols;
+  }
+};
+
+// What a group of 16 lanes keeps of one block of one row of g and u; ck and cs
+// are the row's.
+__device__ __forceinline__ void keep_block(const GluArgs& a, const BlockAt& at, const float (&g)[8],
+                                           const float (&u)[8], float g1, float u1, int8_t* ck, float* cs, bool first) {
+  const Scale sg = scale_of(group_max_u32<0xF>(amax8(g, __float_as_uint(g1) & 0x7FFFFFFFu)));
+  const Scale su = scale_of(group_max_u32<0xF>(amax8(u, __float_as_uint(u1) & 0x7FFFFFFFu)));
+  if (at.whole) {
+    store8(ck + at.c, codes8(g, sg), 8);
+    store8(ck + a.cols + at.c, codes8(u, su), 8);
+  }
+  if (at.one) {
+    ck[at.e] = (int8_t)(code_of(g1, sg.inv) & sg.keep);
+    ck[a.cols + at.e] = (int8_t)(code_of(u1, su.inv) & su.keep);
+  }
+  if (first) {
+    cs[at.b] = sg.s;
+    cs[a.nb + at.b] = su.s;
+  }
 }
 
-// One block of 128 of g and of u to 16 neighbouring lanes, 8 values of both
-// each; groups of lanes take the blocks of the matrix in turn.
+// One block of 128 of g and of u to 16 neighbouring lanes; groups of lanes take
+// the blocks of the matrix in turn.
 template <typename In>
 __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
   const int64_t units = a.rows * a.nb, stride = (int64_t)gridDim.x * 16;
   for (int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); unit < units; unit += stride) {
-    const int64_t row = unit / a.nb, b = unit - row * a.nb;
-    const int64_t c = b * kBlock + t * 8;
-    const int n = left8(a.cols, c);
-    const In* x = reinterpret_cast<const In*>(a.x) + row * a.ld + c;
-    float g[8], u[8];
-    load8(g, x, n);
-    load8(u, x + a.cols, n);
-    if (a.ck) {
-      int8_t* ck = a.ck + row * 2 * a.cols + c;
-      float* cs = a.cs + row * 2 * a.nb + b;
-      keep_block(g, ck, cs, n, t == 0);
-      keep_block(u, ck + a.cols, cs + a.nb, n, t == 0);
+    const int64_t row = unit / a.nb;
+    const BlockAt at(a, row, unit - row * a.nb, t);
+    const In* x = reinterpret_cast<const In*>(a.x) + at.row * a.ld;
+    float g[8], u[8], g1 = 0.0f, u1 = 0.0f;
+    load8(g, x + at.c, at.whole ? 8 : 0);
+    load8(u, x + a.cols + at.c, at.whole ? 8 : 0);
+    if (at.one) {
+      g1 = widen(x[at.e]);
+      u1 = widen(x[a.cols + at.e]);
     }
+    if (a.ck) keep_block(a, at, g, u, g1, u1, a.ck + at.row * 2 * a.cols, a.cs + at.row * 2 * a.nb, t == 0);
     if (a.a) {
+      In* o = reinterpret_cast<In*>(a.a) + at.row * a.cols;
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
-      store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, g, n);
+      if (at.whole) store8(o + at.c, g, 8);
+      if (at.one) store1(o + at.e, g1 * sigmoid(g1) * u1);
     }
   }
 }
@@ -549,62 +580,75 @@ __global__ __launch_bounds__(NT) void swiglu_row_kernel(GluArgs a) {
   __shared__ uint32_t red[NT / 64];
   const int64_t row = blockIdx.x;
   const In* x = reinterpret_cast<const In*>(a.x) + row * a.ld;
-  float h[CH ? CH : 1][8];
+  float h[CH ? CH : 1][8], h1 = 0.0f;
   uint32_t m = 0;
-  // chunk k of the row: its blocks, a, and a's maximum
+  // chunk k of the row (16 chunks a block): a, and on the first time what is
+  // kept, a's copy in dtype and its maximum
   auto chunk = [&](int64_t k, float (&o)[8], bool first_time) {
-    const int64_t c = k * 8;
-    const int n = left8(a.cols, c);
-    float g[8], u[8];
-    load8(g, x + c, n);
-    load8(u, x + a.cols + c, n);
-    if (first_time && a.ck && k / 16 < a.nb) {
-      int8_t* ck = a.ck + row * 2 * a.cols + c;
-      float* cs = a.cs + row * 2 * a.nb + k / 16;
-      keep_block(g, ck, cs, n, (k & 15) == 0);
-      keep_block(u, ck + a.cols, cs + a.nb, n, (k & 15) == 0);
+    const BlockAt at(a, row, k / 16, (int)(k & 15));
+    float g[8], u[8], g1 = 0.0f, u1 = 0.0f;
+    load8(g, x + at.c, at.whole ? 8 : 0);
+    load8(u, x + a.cols + at.c, at.whole ? 8 : 0);
+    if (at.one) {
+      g1 = widen(x[at.e]);
+      u1 = widen(x[a.cols + at.e]);
     }
+    if (first_time && a.ck && at.b < a.nb)
+      keep_block(a, at, g, u, g1, u1, a.ck + row * 2 * a.cols, a.cs + row * 2 * a.nb, (k & 15) == 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
+    if (at.one) h1 = g1 * sigmoid(g1) * u1;  // (of one chunk of a thread at most)
     if (first_time) {
       m = amax8(o, m);
-      if (a.a) store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, o, n);
+      if (a.a) {
+        In* out = reinterpret_cast<In*>(a.a) + row * a.cols;
+        if (at.whole) store8(out + at.c, o, 8);
+        if (at.one) store1(out + at.e, h1);
+      }
     }
-    return n;
   };
+  // chunks of the row, those of its last block's end included
+  const int64_t chunks = a.nb * 16;
   if constexpr (CH > 0) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) chunk(i * NT + threadIdx.x, h[i], true);
   } else {
-    for (int64_t k = threadIdx.x; k * 8 < (a.cols + kBlock - 1) / kBlock * kBlock; k += NT) chunk(k, h[0], true);
+    for (int64_t k = threadIdx.x; k < chunks; k += NT) chunk(k, h[0], true);
   }
+  m = umax_u32(m, __float_as_uint(h1) & 0x7FFFFFFFu);
   const Scale s = scale_of(row_max<NT>(m, red));
   int8_t* aq = a.aq + row * a.cols;
+  auto put = [&](int64_t k, const float (&o)[8]) {
+    if (k * 8 + 8 <= a.cols) store8(aq + k * 8, codes8(o, s), 8);
+    const BlockAt at(a, row, k / 16, (int)(k & 15));
+    if (at.one) aq[at.e] = (int8_t)(code_of(h1, s.inv) & s.keep);
+  };
   if constexpr (CH > 0) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int64_t c = ((int64_t)i * NT + threadIdx.x) * 8;
-      store8(aq + c, codes8(h[i], s), left8(a.cols, c));
-    }
+    for (int i = 0; i < CH; ++i) put((int64_t)i * NT + threadIdx.x, h[i]);
   } else {
-    for (int64_t k = threadIdx.x; k * 8 < a.cols; k += NT) {
-      const int n = chunk(k, h[0], false);
-      store8(aq + k * 8, codes8(h[0], s), n);
+    for (int64_t k = threadIdx.x; k < chunks; k += NT) {
+      chunk(k, h[0], false);
+      put(k, h[0]);
     }
   }
   if (threadIdx.x == 0) a.sa[row] = s.s;
 }
 
-// 8 codes times their scale
-__device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, float s, int n) {
-  if (n >= 8) {
-    const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_b*>(p));
+// 8 codes times their scale, or 0
+__device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, float s, bool there) {
+  u32x2 w = {0, 0};
+  if (there) w = __builtin_nontemporal_load(reinterpret_cast<const u32x2_b*>(p));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))) * s;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] * s : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3))) * s;
+}
+
+// Gradients of g and u, and a, from one value of each.
+__device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg, float& du, float& act) {
+  const float p = sigmoid(g), w = g * p;  // silu(g)
+  dg = d * u * (p * (1.0f + g * (1.0f - p)));
+  du = d * w;
+  act = w * u;
 }
 
 template <typename In>
@@ -612,27 +656,37 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
   const int64_t units = a.rows * a.nb, stride = (int64_t)gridDim.x * 16;
   for (int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); unit < units; unit += stride) {
-    const int64_t row = unit / a.nb, b = unit - row * a.nb;
-    const int64_t c = b * kBlock + t * 8;
-    const int n = left8(a.cols, c);
-    const float* cs = a.cs + row * 2 * a.nb + b;
-    const int8_t* ck = a.ck + row * 2 * a.cols + c;
-    float d[8], g[8], u[8], h[8];
-    load8(d, reinterpret_cast<const In*>(a.x) + row * a.ld + c, n);
-    load_codes(g, ck, cs[0], n);
-    load_codes(u, ck + a.cols, cs[a.nb], n);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = sigmoid(g[i]), w = g[i] * p;  // silu(g)
-      const float du = d[i] * w;
-      g[i] = d[i] * u[i] * (p * (1.0f + g[i] * (1.0f - p)));
-      h[i] = w * u[i];
-      u[i] = du;
+    const int64_t row = unit / a.nb;
+    const BlockAt at(a, row, unit - row * a.nb, t);
+    const float* cs = a.cs + at.row * 2 * a.nb + at.b;
+    const int8_t* ck = a.ck + at.row * 2 * a.cols;
+    const In* da = reinterpret_cast<const In*>(a.x) + at.row * a.ld;
+    const float sg = cs[0], su = cs[a.nb];
+    float d[8], g[8], u[8], d1 = 0.0f, g1 = 0.0f, u1 = 0.0f;
+    load8(d, da + at.c, at.whole ? 8 : 0);
+    load_codes(g, ck + at.c, sg, at.whole);
+    load_codes(u, ck + a.cols + at.c, su, at.whole);
+    if (at.one) {
+      d1 = widen(da[at.e]);
+      g1 = (float)ck[at.e] * sg;
+      u1 = (float)ck[a.cols + at.e] * su;
     }
-    In* o = reinterpret_cast<In*>(a.dgu) + row * a.lddgu + c;
-    store8(o, g, n);
-    store8(o + a.cols, u, n);
-    if (a.a) store8(reinterpret_cast<In*>(a.a) + row * a.cols + c, h, n);
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) swiglu_grad(d[i], g[i], u[i], g[i], u[i], h[i]);
+    In* o = reinterpret_cast<In*>(a.dgu) + at.row * a.lddgu;
+    In* act = reinterpret_cast<In*>(a.a) + (a.a ? at.row * a.cols : 0);
+    if (at.whole) {
+      store8(o + at.c, g, 8);
+      store8(o + a.cols + at.c, u, 8);
+      if (a.a) store8(act + at.c, h, 8);
+    }
+    if (at.one) {
+      swiglu_grad(d1, g1, u1, g1, u1, h[0]);
+      store1(o + at.e, g1);
+      store1(o + a.cols + at.e, u1);
+      if (a.a) store1(act + at.e, h[0]);
+    }
   }
 }
 
