@@ -681,32 +681,65 @@ def qsg_grad_clip(plan, sumsq, max_norm, norm_out=None, stream=None):
 # ---------------------------------------------------------------------------
 # INT8
 # ---------------------------------------------------------------------------
-def _here(*tensors):
-    """The library launches on the current device: its tensors are there."""
-    import torch
-
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != dev:
-            raise QsgError(f"a tensor is on device {t.get_device()}, the current device is {dev}")
+# Each tensor is asked for as little as accepts it, and has to be on the device
+# of the call's first one, which _launch compares with the current device; what
+# is not accepted goes to the checks above for the words of its refusal.
+def _refuse_device(t, name, dev):
+    raise QsgError(f"{name} is on device {t.get_device()}, the call's first tensor on device {dev}")
 
 
-def _codes(t, name):
+def _view(t, name, dev):
+    """(pointer, rows, cols, ld) of a view whose rows do not overlap."""
+    if t.get_device() == dev >= 0 and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 2:
+            return t.data_ptr(), shape[0], shape[1], shape[1] or 1
+    r = _rows(t, name)
+    if t.get_device() != dev:
+        _refuse_device(t, name, dev)
+    return r
+
+
+def _packed(t, name, numel, dtype, dev):
+    """Pointer of a required buffer that _buffer accepts."""
+    if isinstance(t, int):
+        return t
+    if (t is None or _NAMES.get(t.dtype) != dtype or t.numel() != numel or t.get_device() != dev
+            or not t.is_contiguous()):
+        _buffer(t, name, numel, dtype)
+        if t.get_device() != dev:
+            _refuse_device(t, name, dev)
+    return t.data_ptr()
+
+
+def _pair(codes, numel, cname, scales, n, sname, dev):
+    """Pointers of codes and the scales that belong to them, or of neither."""
+    if codes is None and scales is None:
+        return None, None
+    return _packed(codes, cname, numel, "i8", dev), _packed(scales, sname, n, "f32", dev)
+
+
+def _codes(t, name, dev):
     """(pointer, rows, cols, ld) of an INT8 operand."""
-    p, rows, cols, ld = _rows(t, name)
+    r = _view(t, name, dev)
     if _NAMES.get(t.dtype) != "i8":
         import torch
 
         if t.dtype is not torch.int8:
             raise QsgError(f"{name} must hold INT8 codes as int8 (got {t.dtype})")
-    return p, rows, cols, ld
+    return r
 
 
-def _pair(codes, numel, cname, scales, n, sname):
-    """Pointers of codes and the scales that belong to them, or of neither."""
-    if codes is None and scales is None:
-        return None, None
-    return _dense(codes, cname, numel, "i8"), _dense(scales, sname, n, "f32")
+def _launch_stream(stream, dev):
+    """The stream's handle; the library launches on the current device."""
+    import torch
+
+    now = torch.cuda.current_device()
+    if now != dev:
+        raise QsgError(f"the tensors are on device {dev}, the current device is {now}")
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(now)
 
 
 def qsg_quantize_int8_workspace(rows, cols):
@@ -722,85 +755,92 @@ def qsg_quantize_int8(x, q=None, s=None, qt=None, st=None, workspace=None, strea
     each row in s, and / or transposed qt (cols x rows) with one for each column
     in st, for which workspace holds qsg_quantize_int8_workspace(rows, cols)
     bytes."""
-    px, rows, cols, ld = _rows(x, "x")
+    dev = x.get_device()
+    px, rows, cols, ld = _view(x, "x", dev)
     dt = _float_code(x)[0]
-    pq, ps = _pair(q, rows * cols, "q", s, rows, "s")
-    pqt, pst = _pair(qt, rows * cols, "qt", st, cols, "st")
-    pw = None if qt is None else _workspace(workspace, qsg_quantize_int8_workspace(rows, cols))
-    _here(x, q, s, qt, st, workspace)
-    _check(load_library().qsg_quantize_int8(px, dt, rows, cols, ld, pq, ps, pqt, pst, pw, _stream(stream)))
+    pq, ps = _pair(q, rows * cols, "q", s, rows, "s", dev)
+    pqt = pst = pw = None
+    if qt is not None or st is not None:
+        pqt, pst = _pair(qt, rows * cols, "qt", st, cols, "st", dev)
+        pw = _workspace(workspace, qsg_quantize_int8_workspace(rows, cols))
+        if pw is not None and not isinstance(workspace, int) and workspace.get_device() != dev:
+            _refuse_device(workspace, "workspace", dev)
+    _check(load_library().qsg_quantize_int8(px, dt, rows, cols, ld, pq, ps, pqt, pst, pw, _launch_stream(stream, dev)))
 
 
 def qsg_gemm_int8(a, sa, b, sb, c, bias=None, stream=None):
     """C (M x N) = (A B^T) sa[:, None] sb (+ bias): A is M x K and B is N x K
     (int8), sa (M) and sb (N) fp32 scales, bias N values of fp32 or bf16."""
-    pa, M, K, lda = _codes(a, "A")
-    pb, N, Kb, ldb = _codes(b, "B")
+    dev = a.get_device()
+    ct = _float_code(c)[0]
+    pa, M, K, lda = _codes(a, "A", dev)
+    pb, N, Kb, ldb = _codes(b, "B", dev)
     if Kb != K:
         raise QsgError(f"K mismatch: A has {K}, B has {Kb}")
-    pc, Mc, Nc, ldc = _rows(c, "C")
-    if (Mc, Nc) != (M, N):
+    pc, Mc, Nc, ldc = _view(c, "C", dev)
+    if Mc != M or Nc != N:
         raise QsgError(f"C is {Mc}x{Nc}, expected {M}x{N}")
-    ct = _float_code(c)[0]
-    psa, psb = _dense(sa, "sa", M, "f32"), _dense(sb, "sb", N, "f32")
+    psa, psb = _packed(sa, "sa", M, "f32", dev), _packed(sb, "sb", N, "f32", dev)
     pbias, bt = None, 0
     if bias is not None:
         bt, bname = _float_code(bias)
-        pbias = _dense(bias, "bias", N, bname)
-    _here(a, sa, b, sb, c, bias)
-    _check(load_library().qsg_gemm_int8(pa, psa, pb, psb, M, N, K, lda, ldb, pbias, bt, pc, ct, ldc, _stream(stream)))
+        pbias = _packed(bias, "bias", N, bname, dev)
+    _check(load_library().qsg_gemm_int8(pa, psa, pb, psb, M, N, K, lda, ldb, pbias, bt, pc, ct, ldc,
+                                        _launch_stream(stream, dev)))
 
 
 def qsg_wgrad_int8(dy, q, s, c, accumulate=False, stream=None):
     """C (N x K) = dY^T bf16(q s[:, None]), or C += for an fp32 C: dY T x N
     (bf16), q T x K (int8) with T fp32 scales in s."""
-    pdy, T, N, lddy = _rows(dy, "dY")
-    if _dtype_code(dy) != BF16:
+    dev = dy.get_device()
+    pdy, T, N, lddy = _view(dy, "dY", dev)
+    if _float_code(dy)[0] != BF16:
         raise QsgError("qsg_wgrad_int8 takes a bf16 dY")
-    pq, Tq, K, ldq = _codes(q, "q")
+    pq, Tq, K, ldq = _codes(q, "q", dev)
     if Tq != T:
         raise QsgError(f"token count mismatch: dY has {T}, q has {Tq}")
-    pc, Nc, Kc, ldc = _rows(c, "C")
-    if (Nc, Kc) != (N, K):
+    pc, Nc, Kc, ldc = _view(c, "C", dev)
+    if Nc != N or Kc != K:
         raise QsgError(f"C is {Nc}x{Kc}, expected {N}x{K}")
     ct = _float_code(c)[0]
-    ps = _dense(s, "s", T, "f32")
-    _here(dy, q, s, c)
+    ps = _packed(s, "s", T, "f32", dev)
     _check(load_library().qsg_wgrad_int8(pdy, T, N, lddy, pq, ps, K, ldq, pc, ct, ldc, 1 if accumulate else 0,
-                                         _stream(stream)))
-
-
-def _gate_and_up(t, name):
-    p, rows, both, ld = _rows(t, name)
-    if both % 2:
-        raise QsgError(f"{name} has {both} columns: those of g, then as many of u are expected")
-    return p, rows, both // 2, ld
+                                         _launch_stream(stream, dev)))
 
 
 def qsg_swiglu_int8_store_fwd(gu, a=None, aq=None, sa=None, ck=None, cs=None, stream=None):
     """a = silu(g) u of gu = [g, u] (rows x 2 cols): a (rows x cols, the type of
     gu) and / or its INT8 copy (aq, sa as qsg_quantize_int8); ck (rows x 2 cols,
     int8) and cs (rows x 2 ceil(cols / 128)) keep g and u for backward."""
-    p, rows, cols, ld = _gate_and_up(gu, "gu")
+    dev = gu.get_device()
+    p, rows, both, ld = _view(gu, "gu", dev)
+    if both % 2:
+        raise QsgError(f"gu has {both} columns: those of g, then as many of u are expected")
+    cols = both // 2
     dt, dname = _float_code(gu)
-    pa = None if a is None else _dense(a, "a", rows * cols, dname)
-    paq, psa = _pair(aq, rows * cols, "aq", sa, rows, "sa")
-    pck, pcs = _pair(ck, rows * 2 * cols, "ck", cs, rows * 2 * -(-cols // 128), "cs")
-    _here(gu, a, aq, sa, ck, cs)
-    _check(load_library().qsg_swiglu_int8_store_fwd(p, dt, rows, cols, ld, pa, paq, psa, pck, pcs, _stream(stream)))
+    pa = None if a is None else _packed(a, "a", rows * cols, dname, dev)
+    paq, psa = _pair(aq, rows * cols, "aq", sa, rows, "sa", dev)
+    pck, pcs = _pair(ck, rows * both, "ck", cs, rows * 2 * -(-cols // 128), "cs", dev)
+    _check(load_library().qsg_swiglu_int8_store_fwd(p, dt, rows, cols, ld, pa, paq, psa, pck, pcs,
+                                                    _launch_stream(stream, dev)))
 
 
 def qsg_swiglu_int8_store_bwd(da, ck, cs, dgu, a=None, stream=None):
     """dgu = [dg, du] (rows x 2 cols) from da (rows x cols) and what the forward
     pass kept; a (rows x cols) is computed again on request.  One type for da,
     dgu and a."""
-    p, rows, cols, ldda = _rows(da, "da")
+    dev = da.get_device()
+    p, rows, cols, ldda = _view(da, "da", dev)
     dt, dname = _float_code(da)
-    po, lddgu = _same_matrix(dgu, "dgu", (rows, 2 * cols), da.dtype)
-    if po is None:
+    if dgu is None:
         raise QsgError("dgu is required")
-    pck = _dense(ck, "ck", rows * 2 * cols, "i8")
-    pcs = _dense(cs, "cs", rows * 2 * -(-cols // 128), "f32")
-    pa = None if a is None else _dense(a, "a", rows * cols, dname)
-    _here(da, ck, cs, dgu, a)
-    _check(load_library().qsg_swiglu_int8_store_bwd(p, dt, rows, cols, ldda, pck, pcs, po, lddgu, pa, _stream(stream)))
+    po, ro, co, lddgu = _view(dgu, "dgu", dev)
+    if ro != rows or co != 2 * cols:
+        raise QsgError(f"dgu is {ro}x{co}, expected {rows}x{2 * cols}")
+    if dgu.dtype is not da.dtype:
+        raise QsgError(f"dgu must be {da.dtype} (got {dgu.dtype})")
+    pck = _packed(ck, "ck", rows * 2 * cols, "i8", dev)
+    pcs = _packed(cs, "cs", rows * 2 * -(-cols // 128), "f32", dev)
+    pa = None if a is None else _packed(a, "a", rows * cols, dname, dev)
+    _check(load_library().qsg_swiglu_int8_store_bwd(p, dt, rows, cols, ldda, pck, pcs, po, lddgu, pa,
+                                                    _launch_stream(stream, dev)))

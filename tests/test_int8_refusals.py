@@ -156,4 +156,5 @@ def test_binding_refuses_other_devices(monkeypatch):
         lambda: q.qsg_swiglu_int8_store_bwd(Dev((4, 4), BF, **there), Dev((4, 8), I8), Dev((4, 2), F32), Dev((4, 8), BF)),
     ]
     for call in calls:
-        raises(call, "is on device 1, the current device is 0")
+        raises(call, "on device 1, the current device is 0|is on device 1, the call's first tensor on device 0|"
+               "is on device 0, the call's first tensor on device 1")
