@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
 // bf16.  Loads ask for no alignment.  Features past the end of an operand
 // only reach results that are not stored, so a row may be read past its end
 // where memory goes on, into the next row; only a step in which it might not
-// (the last one or two) is loaded element by element.
+// (the last one or two) is loaded with more care.
 template <int TILE>
 struct SmallStage {
   static constexpr int ROW = TILE * 2;                // bytes of a token
@@ -611,13 +611,34 @@ __device__ __forceinline__ int small_tr_offset(int fblk, int lane) {
 typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
 
-template <int TILE>
-__global__ __launch_bounds__(256) void gemm_wgrad_int8_kernel(Bf16Args g) {
+// 16 bytes at `at` of a matrix of `end` bytes; what lies past its end is 0
+__device__ __forceinline__ u32x4 tail_chunk(const uint8_t* p, int64_t at, int64_t end) {
+  if (end >= 16) {
+    const int64_t from = at < end - 16 ? at : end - 16;
+    return shift_down(*reinterpret_cast<const u32x4_b*>(p + from), (int)(at - from));
+  }
+  u32x4 r = {0, 0, 0, 0};
+  for (int64_t i = at; i < end; ++i) {
+    const int k = (int)(i - at);
+    const uint32_t b = (uint32_t)p[i] << (8 * (k & 3));
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (k >> 2 == d) r[d] |= b;
+  }
+  return r;
+}
+
+// GROUPS of 4 waves take the steps in turn and join their sums in the end: with
+// few tiles a workgroup is alone on its CU.  A step's loads are two of a group's
+// steps ahead, in registers, and go to LDS one step ahead.
+template <int TILE, int GROUPS>
+__global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args g) {
   using S = SmallStage<TILE>;
   constexpr int NT = TILE / 64;  // 32 x 32 MFMA tiles of a wave, each way
-  __shared__ __attribute__((aligned(16))) uint8_t la[2][BT * S::ROW];
-  __shared__ __attribute__((aligned(16))) uint8_t lx[2][BT * S::ROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(16))) uint8_t la[GROUPS][2][BT * S::ROW];
+  __shared__ __attribute__((aligned(16))) uint8_t lx[GROUPS][2][BT * S::ROW];
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), tid = threadIdx.x & 255;
+  const int lane = tid & 63, wave = tid >> 6;
   const int wn = wave >> 1, wk = wave & 1;
   const int64_t n0 = (int64_t)blockIdx.y * TILE, k0 = (int64_t)blockIdx.x * TILE;
   // chunk i of a thread: token at[i], features af (dY); token xt[i], codes xf
@@ -632,53 +653,64 @@ __global__ __launch_bounds__(256) void gemm_wgrad_int8_kernel(Bf16Args g) {
   const int64_t af = n0 + 8 * ac < a_last ? n0 + 8 * ac : a_last;
   const int64_t xf = k0 + 16 * xc < x_last ? k0 + 16 * xc : x_last;
   const int64_t a_end = (g.T - 1) * g.lddy + g.N, x_end = (g.T - 1) * g.ldx + g.K;  // elements that are there
+  const int64_t nsteps = (g.T + BT - 1) / BT;
 
-  u32x4 ra[S::AC], rx[S::XC];
-  float rs[S::XC];
-  auto fetch = [&](int64_t s) {
-    const int64_t t0 = s * BT, tl = t0 + BT - 1;
-    if (tl < g.T && tl * g.lddy + a_last + 8 <= a_end && tl * g.ldx + x_last + 16 <= x_end) {
+  struct Regs {
+    u32x4 a[S::AC], x[S::XC];
+    float s[S::XC];
+  };
+  // The first steps need no care, and the loop over them no branch (behind one
+  // the compiler waits for every load in flight, the youngest ones too).
+  int64_t plain = g.T / BT;
+  while (plain > 0) {
+    const int64_t tl = plain * BT - 1;
+    if (tl * g.lddy + a_last + 8 <= a_end && tl * g.ldx + x_last + 16 <= x_end) break;
+    --plain;
+  }
+  auto fetch_plain = [&](Regs& r, int64_t s) {
+    const int64_t t0 = s * BT;
 #pragma unroll
-      for (int i = 0; i < S::AC; ++i) ra[i] = *reinterpret_cast<const u32x4_e*>(g.dy + (t0 + at[i]) * g.lddy + af);
+    for (int i = 0; i < S::AC; ++i) r.a[i] = *reinterpret_cast<const u32x4_e*>(g.dy + (t0 + at[i]) * g.lddy + af);
 #pragma unroll
-      for (int i = 0; i < S::XC; ++i) {
-        rx[i] = *reinterpret_cast<const u32x4_b*>(g.q + (t0 + xt[i]) * g.ldx + xf);
-        rs[i] = g.qs[t0 + xt[i]];
-      }
-    } else {
-      // every element by a load of its own from an address that is there
-#pragma unroll
-      for (int i = 0; i < S::AC; ++i) {
-        const bool in = t0 + at[i] < g.T;
-        const uint16_t* p = g.dy + (in ? t0 + at[i] : g.T - 1) * g.lddy;
-        u32x4 r = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[e >> 1] |= (uint32_t)p[af + e < g.N ? af + e : g.N - 1] << (16 * (e & 1));
-        ra[i] = in ? r : u32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < S::XC; ++i) {
-        const bool in = t0 + xt[i] < g.T;
-        const int64_t t = in ? t0 + xt[i] : g.T - 1;
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(g.q) + t * g.ldx;
-        u32x4 r = {0, 0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 16; ++e) r[e >> 2] |= (uint32_t)p[xf + e < g.K ? xf + e : g.K - 1] << (8 * (e & 3));
-        rx[i] = r;
-        rs[i] = in ? g.qs[t] : 0.0f;
-      }
+    for (int i = 0; i < S::XC; ++i) {
+      r.x[i] = *reinterpret_cast<const u32x4_b*>(g.q + (t0 + xt[i]) * g.ldx + xf);
+      r.s[i] = g.qs[t0 + xt[i]];
     }
   };
-  auto put = [&](int st) {
+  auto fetch = [&](Regs& r, int64_t s) {
+    if (s >= nsteps) return;
+    if (s < plain) {
+      fetch_plain(r, s);
+      return;
+    }
+    // Tokens past the end read the last one, and are 0.  What would be read
+    // past the end of the matrix is read so far before it, and shifted.
+    const int64_t t0 = s * BT;
+#pragma unroll
+    for (int i = 0; i < S::AC; ++i) {
+      const bool in = t0 + at[i] < g.T;
+      const int64_t e = (in ? t0 + at[i] : g.T - 1) * g.lddy + af;
+      const u32x4 w = tail_chunk(reinterpret_cast<const uint8_t*>(g.dy), 2 * e, 2 * a_end);
+      r.a[i] = in ? w : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < S::XC; ++i) {
+      const bool in = t0 + xt[i] < g.T;
+      const int64_t t = in ? t0 + xt[i] : g.T - 1;
+      r.x[i] = tail_chunk(reinterpret_cast<const uint8_t*>(g.q), t * g.ldx + xf, x_end);
+      r.s[i] = in ? g.qs[t] : 0.0f;
+    }
+  };
+  auto put = [&](int st, const Regs& r) {
 #pragma unroll
     for (int i = 0; i < S::AC; ++i)
-      *reinterpret_cast<u32x4*>(la[st] + at[i] * S::ROW + small_swz<TILE>(at[i], ac) * 16) = ra[i];
+      *reinterpret_cast<u32x4*>(la[group][st] + at[i] * S::ROW + small_swz<TILE>(at[i], ac) * 16) = r.a[i];
 #pragma unroll
     for (int i = 0; i < S::XC; ++i) {
       u32x4 lo, hi;
-      widen16(rx[i], rs[i], lo, hi);
-      *reinterpret_cast<u32x4*>(lx[st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc) * 16) = lo;
-      *reinterpret_cast<u32x4*>(lx[st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc + 1) * 16) = hi;
+      widen16(r.x[i], r.s[i], lo, hi);
+      *reinterpret_cast<u32x4*>(lx[group][st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc) * 16) = lo;
+      *reinterpret_cast<u32x4*>(lx[group][st] + xt[i] * S::ROW + small_swz<TILE>(xt[i], 2 * xc + 1) * 16) = hi;
     }
   };
   auto frag = [&](const uint8_t* p) {
@@ -700,30 +732,81 @@ __global__ __launch_bounds__(256) void gemm_wgrad_int8_kernel(Bf16Args g) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  const int64_t nsteps = (g.T + BT - 1) / BT;
-  if (nsteps > 0) {
-    fetch(0);
-    put(0);
-  }
-  __syncthreads();
-  for (int64_t s = 0; s < nsteps; ++s) {
-    const int st = (int)(s & 1);
-    if (s + 1 < nsteps) fetch(s + 1);
+  // A workgroup barrier without a fence, which would wait for the fetches in
+  // flight.
+  auto barrier = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // Step s in stage st: the group's next one goes from `ready` to the other
+  // stage, and the one after it is fetched.
+  auto work = [&](int st) {
 #pragma unroll
     for (int ks = 0; ks < BT / 16; ++ks) {
       bf16x8 fa[NT], fx[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        fa[i] = frag(la[st] + ks * 16 * S::ROW + offa[i]);
-        fx[i] = frag(lx[st] + ks * 16 * S::ROW + offx[i]);
+        fa[i] = frag(la[group][st] + ks * 16 * S::ROW + offa[i]);
+        fx[i] = frag(lx[group][st] + ks * 16 * S::ROW + offx[i]);
       }
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fx[j], acc[i][j], 0, 0, 0);
     }
-    if (s + 1 < nsteps) put(st ^ 1);
+  };
+  auto step_plain = [&](int st, const Regs& ready, Regs& other, int64_t s) {
+    fetch_plain(other, s + 2 * GROUPS);
+    work(st);
+    put(st ^ 1, ready);
+    barrier();
+  };
+  auto step = [&](int st, const Regs& ready, Regs& other, int64_t s) {
+    fetch(other, s + 2 * GROUPS);
+    if (s < nsteps) work(st);
+    if (s + GROUPS < nsteps) put(st ^ 1, ready);
+    barrier();
+  };
+  Regs r0, r1;
+  fetch(r0, group);
+  fetch(r1, group + GROUPS);
+  if (group < nsteps) put(0, r0);
+  barrier();
+  int64_t s = 0;
+  for (; s + 4 * GROUPS <= plain; s += 2 * GROUPS) {
+    step_plain(0, r1, r0, s + group);
+    step_plain(1, r0, r1, s + GROUPS + group);
+  }
+  for (; s < nsteps; s += 2 * GROUPS) {
+    step(0, r1, r0, s + group);
+    if (s + GROUPS < nsteps) step(1, r0, r1, s + GROUPS + group);
+  }
+  if constexpr (GROUPS > 1) {
+    // the other groups' sums, added in their order, through the first stages
+    // (16 KB of each group; nothing of them is read any more)
+    static_assert(NT == 1 && 2 * BT * S::ROW >= 16384, "a group's sums fit its stages");
+    float* sums = reinterpret_cast<float*>(la[group][0]) + wave * 1024 + lane * 4;
+    if (group > 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(sums + q * 256) =
+            float4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+    }
     __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int o = 1; o < GROUPS; ++o) {
+      const float* p = reinterpret_cast<const float*>(la[o][0]) + wave * 1024 + lane * 4;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 w = *reinterpret_cast<const float4*>(p + q * 256);
+        acc[0][0][4 * q] += w.x;
+        acc[0][0][4 * q + 1] += w.y;
+        acc[0][0][4 * q + 2] += w.z;
+        acc[0][0][4 * q + 3] += w.w;
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -782,13 +865,19 @@ void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const
                    K % 16 == 0 && lddy < (1 << 24) && ldq < (1 << 24) && T > 0 && tiles(WT) <= 0x7FFFFF;
   if (dma && tiles(WT) >= 128) {
     hipLaunchKernelGGL(gemm_wgrad_bf16_dma_kernel<true>, dim3((unsigned)tiles(WT)), dim3(256), 0, st, g);
-  } else if (tiles(128) >= 256) {
-    hipLaunchKernelGGL(gemm_wgrad_int8_kernel<128>, dim3((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128)),
-                       dim3(256), 0, st, g);
-  } else {
-    hipLaunchKernelGGL(gemm_wgrad_int8_kernel<64>, dim3((unsigned)((K + 63) / 64), (unsigned)((N + 63) / 64)),
-                       dim3(256), 0, st, g);
+    return;
   }
+  // What fills the chip with the largest tiles; with no more 64 x 64 tiles than
+  // CUs four groups of waves share one (8192 x 1024 x 1024: 47 us, with two
+  // groups 54, with one 68), with more of them two, two workgroups to a CU
+  // (777 x 1000 x 1111, 288 tiles: 14.6 us, with four groups 19.6).
+  auto go = [&](auto kernel, int tile, int threads) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((K + tile - 1) / tile), (unsigned)((N + tile - 1) / tile)), dim3(threads),
+                       0, st, g);
+  };
+  if (tiles(128) >= 256) go(gemm_wgrad_int8_kernel<128, 1>, 128, 256);
+  else if (tiles(64) > 256) go(gemm_wgrad_int8_kernel<64, 2>, 64, 512);
+  else go(gemm_wgrad_int8_kernel<64, 4>, 64, 1024);
 }
 
 }  // namespace qsg

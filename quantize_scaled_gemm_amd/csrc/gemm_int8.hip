@@ -28,6 +28,7 @@ typedef int v4i_u __attribute__((ext_vector_type(4), aligned(1)));
 typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
 
 struct Int8Args {
   const int8_t* a;
@@ -41,30 +42,12 @@ struct Int8Args {
   int64_t tiles_m;
 };
 
-// v shifted down by n bytes (16 and more: nothing is left)
-__device__ __forceinline__ v4i shift_down(v4i v, int n) {
-  const int d = n >> 2;
-  uint32_t t[5];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int k = i; k < 4; ++k) w = d == k - i ? (uint32_t)v[k] : w;
-    t[i] = w;
-  }
-  t[4] = 0;
-  v4i r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = (int)__builtin_amdgcn_alignbyte(t[i + 1], t[i], n & 3);
-  return r;
-}
-
 // 16 bytes of a row of K bytes at k; what lies past its end is 0.  One load
 // without a branch where a row has 16 bytes: the last 16 of them, shifted.
 __device__ __forceinline__ v4i load_chunk(const int8_t* row, int64_t k, int64_t K) {
   if (K >= 16) {
     const int64_t at = k < K - 16 ? k : K - 16;
-    return shift_down(*reinterpret_cast<const v4i_u*>(row + at), (int)(k - at < 16 ? k - at : 16));
+    return __builtin_bit_cast(v4i, shift_down(*reinterpret_cast<const u32x4_b*>(row + at), (int)(k - at < 16 ? k - at : 16)));
   }
   v4i r = {0, 0, 0, 0};
 #pragma unroll
@@ -450,13 +433,19 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
     v4i a[LA], b[LB];
   };
   Regs x0, x1;
+  const int plain = K / TB;  // whole K tiles; the loop over them has no branch,
+                             // behind which the compiler waits for every load in flight
+  auto fetch_plain = [&](Regs& x, int kt) {
+    const int k = kt * TB + ch * 16;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) x.a[i] = *reinterpret_cast<const v4i_u*>(pa[i] + k);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) x.b[i] = *reinterpret_cast<const v4i_u*>(pb[i] + k);
+  };
   auto fetch = [&](Regs& x, int kt) {
     const int k = kt * TB + ch * 16;
-    if ((kt + 1) * TB <= K) {
-#pragma unroll
-      for (int i = 0; i < LA; ++i) x.a[i] = *reinterpret_cast<const v4i_u*>(pa[i] + k);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) x.b[i] = *reinterpret_cast<const v4i_u*>(pb[i] + k);
+    if (kt < plain) {
+      fetch_plain(x, kt);
     } else if (kt < nk) {
 #pragma unroll
       for (int i = 0; i < LA; ++i) x.a[i] = load_chunk(pa[i], k, K);
@@ -495,8 +484,9 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
       fb[s & 1][j] = *reinterpret_cast<const v4i*>(st + TM * TB + (wn * (TN / 2) + j * 32) * TB + fo[s]);
   };
   // K tile kt in `cur`; kt + 1 goes from `ready` to `next`, kt + 2 is fetched into `other`
-  auto step = [&](const uint8_t* cur, uint8_t* next, const Regs& ready, Regs& other, int kt) {
-    fetch(other, kt + 2);
+  auto step = [&](const uint8_t* cur, uint8_t* next, const Regs& ready, Regs& other, int kt, auto all_plain) {
+    if constexpr (decltype(all_plain)::value) fetch_plain(other, kt + 2);
+    else fetch(other, kt + 2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) {
@@ -519,11 +509,15 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
   lds_barrier_lgkm();
   read(st0, 0);
   int kt = 0;
-  for (; kt + 2 <= nk; kt += 2) {
-    step(st0, st1, x1, x0, kt);
-    step(st1, st0, x0, x1, kt + 1);
+  for (; kt + 4 <= plain; kt += 2) {
+    step(st0, st1, x1, x0, kt, std::true_type{});
+    step(st1, st0, x0, x1, kt + 1, std::true_type{});
   }
-  if (kt < nk) step(st0, st1, x1, x0, kt);
+  for (; kt + 2 <= nk; kt += 2) {
+    step(st0, st1, x1, x0, kt, std::false_type{});
+    step(st1, st0, x0, x1, kt + 1, std::false_type{});
+  }
+  if (kt < nk) step(st0, st1, x1, x0, kt, std::false_type{});
   lds_barrier_lgkm();  // no wave reads a stage any more
   constexpr int PART = 32 * kTilePitch<OUT_BF16, NJ>;
   static_assert(2 * PART <= sizeof(st0), "two waves' rows fit a stage");

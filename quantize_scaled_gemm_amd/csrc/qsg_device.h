@@ -27,6 +27,24 @@ __device__ __forceinline__ void st_stream8(void* p, uint32_t lo, uint32_t hi) {
   __builtin_nontemporal_store(v, reinterpret_cast<u32x2*>(p));
 }
 
+// v shifted down by n bytes (16: nothing is left)
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int n) {
+  const int d = n >> 2;
+  uint32_t t[5];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = i; k < 4; ++k) w = d == k - i ? v[k] : w;
+    t[i] = w;
+  }
+  t[4] = 0;
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_alignbyte(t[i + 1], t[i], n & 3);
+  return r;
+}
+
 constexpr int kE4M3 = 0;
 constexpr int kE5M2 = 1;
 
