@@ -223,7 +223,10 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_int8_ring_kernel(Int8Args g) 
   __shared__ __attribute__((aligned(1024))) uint8_t st2[R > 2 ? WAVES * STEP : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t st3[R > 3 ? WAVES * STEP : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tm = blockIdx.x % g.tiles_m, tn = blockIdx.x / g.tiles_m;
+  // Workgroups go to the 8 XCDs in turn, each with an L2 of its own: those that
+  // read the same rows of B follow each other on one XCD
+  const int64_t turn = blockIdx.x / 8, tm = turn % g.tiles_m, tn = turn / g.tiles_m * 8 + blockIdx.x % 8;
+  if (tn * (16 * NT) >= g.N) return;
   const int64_t m0 = tm * (16 * MT), n0 = tn * (16 * NT);
   // load i of a step fills 1 KB: rows 8 i + lane / 8 (B's rows, then A's),
   // position lane % 8
@@ -672,7 +675,7 @@ void launch_few(const Int8Args& g, bool bf16, hipStream_t st) {
 template <int MT, int NT, int WAVES, int R>
 void launch_ring(Int8Args g, bool bf16, hipStream_t st) {
   g.tiles_m = (g.M + 16 * MT - 1) / (16 * MT);
-  const dim3 grid((unsigned)(g.tiles_m * ((g.N + 16 * NT - 1) / (16 * NT)))), block(WAVES * 64);
+  const dim3 grid((unsigned)(g.tiles_m * ((g.N + 128 * NT - 1) / (128 * NT)) * 8)), block(WAVES * 64);
   if (bf16) hipLaunchKernelGGL((gemm_int8_ring_kernel<MT, NT, WAVES, R, true>), grid, block, 0, st, g);
   else hipLaunchKernelGGL((gemm_int8_ring_kernel<MT, NT, WAVES, R, false>), grid, block, 0, st, g);
 }
@@ -717,12 +720,13 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   }
   if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128, 4>(g, bf16, st);
   else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128, 4>(g, bf16, st);
-  else if (M > 32 && tiles(64, 64) >= 100) launch_tile<64, 64, 4>(g, bf16, st);
+  else if (M > 32 && tiles(64, 64) >= 160) launch_tile<64, 64, 4>(g, bf16, st);
+  else if (M > 64 && tiles(32, 64) >= 200) launch_ring<2, 4, 4, 2>(g, bf16, st);
+  else if (M > 32 || (M > 16 && N >= 12288)) launch_ring<2, 2, 4, 2>(g, bf16, st);
+  else if (M > 16) launch_ring<2, 1, 4, 3>(g, bf16, st);
   else if (M <= 4 && N >= 12288) launch_few(g, bf16, st);
-  else if (M <= 16 && N >= 12288) launch_ring<1, 2, 4, 2>(g, bf16, st);
-  else if (M <= 16) launch_ring<1, 1, 4, 4>(g, bf16, st);
-  else if (M <= 32 && N < 12288) launch_ring<2, 1, 4, 3>(g, bf16, st);
-  else launch_ring<2, 2, 4, 2>(g, bf16, st);
+  else if (N >= 12288) launch_ring<1, 2, 4, 2>(g, bf16, st);
+  else launch_ring<1, 1, 4, 4>(g, bf16, st);
 }
 
 }  // namespace qsg

@@ -204,6 +204,19 @@ def test_product_bias(q, M, N, K, bias):
     product(q, M, N, K, F32, bias)
 
 
+@pytest.mark.parametrize("out, bias", [(BF, None), (F32, F32), (BF, BF)])
+@pytest.mark.parametrize("M, N, K, pad", [
+    (1, 12300, 1040, 0), (4, 12288, 512, 16), (5, 12300, 640, 0), (16, 12301, 2064, 0),      # few rows, many columns
+    (3, 4100, 2064, 0), (16, 900, 4112, 16), (17, 900, 4112, 0), (32, 4100, 656, 0),         # few rows and columns
+    (20, 12300, 528, 0), (32, 12289, 400, 32), (33, 4100, 1040, 0), (64, 900, 16, 0),        # up to 64 rows
+    (61, 10250, 1040, 0), (64, 12289, 256, 16), (100, 4100, 2064, 0), (128, 4096, 1024, 0),
+    (300, 1000, 144, 0), (450, 4100, 784, 0), (511, 4097, 400, 16), (1021, 3100, 528, 0), (900, 4100, 112, 0),
+    (3, 800, 333, 0), (40, 700, 333, 0), (16, 7000, 129, 0), (1000, 3201, 333, 3), (900, 4100, 100, 1)])  # any alignment
+def test_product_forms(q, M, N, K, pad, out, bias):
+    """Every way that the sizes choose, with ragged edges and short K."""
+    test_large_product(q, M, N, K, pad, out, bias)
+
+
 @pytest.mark.parametrize("out, bias", [(BF, None), (F32, None), (BF, BF), (F32, F32), (BF, F32), (F32, BF)])
 @pytest.mark.parametrize("M, N, K, pad", [
     (4096, 2048, 512, 0), (2900, 4098, 256, 0), (4250, 4096, 768, 16),  # 128 tiles of 256 x 256, ragged, a tail launch
