@@ -333,6 +333,74 @@ __device__ __forceinline__ void tile_of(int b, int nx, int ny, int& tx, int& ty)
   tx = idx / h;
 }
 
+// 32 rows x 32 NJ columns of C from row n0 and column k0 on, out of a row of
+// accumulator tiles (lane l holds column l % 32 and rows 8 (v / 4) + 4 (l / 32)
+// + v % 4 of a tile), through the wave's own part of LDS: C is then written, and
+// read where it is added to, 16 bytes a lane in whole row segments, at any
+// alignment.  (Straight from the registers an element of 2 or 4 bytes of 32
+// columns and 2 rows is a store.)
+typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4)));
+template <int NJ>
+constexpr int kRowPitch = 32 * NJ + 8;  // floats; 4 rows further are 32 banks further
+template <int NJ, bool AGPR, typename Tiles>
+__device__ __forceinline__ void store_rows(const Bf16Args& g, const Tiles& acc, int64_t n0, int64_t k0, int lane,
+                                           float* lds) {
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      float val;
+      if constexpr (AGPR)  // (256 accumulators: plain reads make the compiler copy them in the K loop)
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(val) : "a"(acc[j][v]));
+      else
+        val = acc[j][v];
+      lds[(8 * (v / 4) + 4 * (lane >> 5) + v % 4) * kRowPitch<NJ> + j * 32 + (lane & 31)] = val;
+    }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // other lanes' writes
+  if (g.out_bf16) {
+    constexpr int LPR = 4 * NJ, RPI = 64 / LPR;  // lanes of a row, rows of a store
+    const int64_t k = k0 + lane % LPR * 8;
+#pragma unroll
+    for (int i = 0; i < 32 / RPI; ++i) {
+      const int r = i * RPI + lane / LPR;
+      const float4 a = *reinterpret_cast<const float4*>(lds + r * kRowPitch<NJ> + lane % LPR * 8);
+      const float4 b = *reinterpret_cast<const float4*>(lds + r * kRowPitch<NJ> + lane % LPR * 8 + 4);
+      const u32x4 w = {pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w)};
+      if (n0 + r < g.N) {
+        uint16_t* p = reinterpret_cast<uint16_t*>(g.c) + (n0 + r) * g.ldc + k;
+        if (k + 8 <= g.K) {
+          *reinterpret_cast<u32x4_e*>(p) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (k + e < g.K) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  } else {
+    constexpr int LPR = 8 * NJ, RPI = 64 / LPR;
+    const int64_t k = k0 + lane % LPR * 4;
+#pragma unroll
+    for (int i = 0; i < 32 / RPI; ++i) {
+      const int r = i * RPI + lane / LPR;
+      f32x4_e w = *reinterpret_cast<const f32x4_e*>(lds + r * kRowPitch<NJ> + lane % LPR * 4);
+      if (n0 + r < g.N) {
+        float* p = reinterpret_cast<float*>(g.c) + (n0 + r) * g.ldc + k;
+        if (k + 4 <= g.K) {
+          if (g.accumulate) w = *reinterpret_cast<const f32x4_e*>(p) + w;
+          *reinterpret_cast<f32x4_e*>(p) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            if (k + e < g.K) p[e] = g.accumulate ? p[e] + w[e] : w[e];
+        }
+      }
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the reads, before the next rows' writes
+}
+
 // An INT8 X (X8) cannot go to LDS as it lies in memory.  A thread loads 16
 // codes of one token (3 tokens a step, XL), and writes what they stand for,
 // 32 bytes of bf16, where the direct load of a bf16 X would have put them, so
@@ -520,6 +588,14 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
   if (s < nsteps) step(st1, st0, sx1, sx2, s++, std::false_type{});
   if (s < nsteps) step(st2, st1, sx2, sx0, s++, std::false_type{});
   wait_vm<0>();  // the loads past the last step (empty resources) have landed
+  if constexpr (X8) {
+    // behind the last step's barrier no wave reads a stage any more
+    static_assert(32 * kRowPitch<4> * 4 <= DOP, "a wave's rows fit a stage");
+    float* part = reinterpret_cast<float*>(wave == 0 ? st0 : wave == 1 ? st1 : wave == 2 ? st2 : sx0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) store_rows<4, true>(g, acc[i], n0 + wn * 128 + i * 32, k0 + wk * 128, lane, part);
+    return;
+  }
 
   // accumulator tile (i, j): lane l holds column k = l % 32 and rows
   // n = 8 (v / 4) + 4 (l / 32) + v % 4 of its 32 x 32 block.  A wave's store
@@ -608,7 +684,6 @@ __device__ __forceinline__ int small_tr_offset(int fblk, int lane) {
   return t * SmallStage<TILE>::ROW + small_swz<TILE>(t, c) * 16 + (q & 1) * 8;
 }
 
-typedef uint32_t u32x4_e __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
 
 // 16 bytes at `at` of a matrix of `end` bytes; what lies past its end is 0
@@ -808,24 +883,13 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
       }
     }
   }
+  // behind the last step's barrier no wave reads a stage any more
+  constexpr int PART = 32 * kRowPitch<NT>;
+  static_assert(2 * PART * 4 <= 2 * BT * S::ROW, "two waves' rows fit a group's stages");
+  float* part = reinterpret_cast<float*>(wave < 2 ? la[0][0] : lx[0][0]) + (wave & 1) * PART;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int64_t k = k0 + wk * (TILE / 2) + j * 32 + (lane & 31);
-      if (k >= g.K) continue;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t n = n0 + wn * (TILE / 2) + i * 32 + 8 * (v / 4) + 4 * (lane >> 5) + (v % 4);
-        if (n >= g.N) continue;
-        if (g.out_bf16) {
-          reinterpret_cast<uint16_t*>(g.c)[n * g.ldc + k] = (uint16_t)(pack_bf16x2(acc[i][j][v], 0.0f) & 0xFFFF);
-        } else {
-          float* cp = reinterpret_cast<float*>(g.c) + n * g.ldc + k;
-          *cp = g.accumulate ? *cp + acc[i][j][v] : acc[i][j][v];
-        }
-      }
-    }
+    store_rows<NT, false>(g, acc[i], n0 + wn * (TILE / 2) + i * 32, k0 + wk * (TILE / 2), lane, part);
 }
 
 }  // namespace
