@@ -69,7 +69,7 @@ def check_copies(got, x, name=""):
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 15), (129, 16), (64, 127), (17, 129), (300, 256), (33, 257), (2, 512), (70, 513),
           (9, 1000), (31, 1024), (5, 1025), (130, 2048), (3, 2049), (6, 4096), (4, 4097), (3, 8192), (2, 8193),
           (2, 16384), (1, 16385), (2, 32768), (2, 32769), (3, 40003), (1000, 63), (513, 65), (2051, 40), (255, 2056),
-          (257, 4095), (700, 2500), (520, 5001), (300, 9000), (8300, 2060), (1, 2100), (2, 9001)]
+          (257, 4095), (700, 2500), (520, 5001), (300, 9000), (3000, 600), (2101, 1500), (8300, 2060), (1, 2100), (2, 9001)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
