@@ -360,3 +360,22 @@ def test_wgrad_nan_scale(q):
         c = torch.zeros((24, K), device="cuda")
         q.qsg_wgrad_int8(dy, qq, s, c)
         assert torch.isnan(c).all()
+
+
+@pytest.mark.parametrize("N, K", [(2048, 4096), (2001, 2050), (500, 2100), (24, 33)])
+def test_wgrad_largest_values(q, N, K):
+    """A token whose maximum is bf16's largest value: 128 times its scale is
+    not finite, its codes times its scale are.  One product a sum, so exact."""
+    top = torch.finfo(BF).max
+    T, g = 70, torch.Generator(device="cuda").manual_seed(5)
+    s = torch.ones(T, device="cuda")
+    s[69] = float(np.float32(top) / np.float32(127))
+    qq = torch.randint(-127, 128, (T, K), dtype=torch.int8, device="cuda", generator=g)
+    qq[69, 0], qq[69, 1], qq[69, 2] = 127, -127, 0
+    dy = torch.zeros((T, N), dtype=BF, device="cuda")
+    dy[69] = 2.0 ** torch.randint(-6, -2, (N,), device="cuda", generator=g)
+    x = (qq[69].float() * s[69]).to(BF).float()
+    assert torch.isfinite(x).all() and x[0] == top
+    c = torch.full((N, K), 5.0, device="cuda")
+    q.qsg_wgrad_int8(dy, qq, s, c)
+    assert torch.equal(c, dy[69].float()[:, None] * x[None, :])
