@@ -471,7 +471,7 @@ template <typename In>
 void launch_quantize(const QuantArgs& a, hipStream_t st) {
   // both copies of rows that fit registers: one pass for the rows and the
   // columns' maxima
-  const bool fused = a.q && a.qt && a.cols <= 16384;
+  const bool fused = a.q && a.qt && a.rows > 0 && a.cols <= 16384;
   if (fused) {
     auto go = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(a.parts), dim3(threads), 0, st, a); };
     if (a.cols <= 512) go(int8_row_col_kernel<In, 64, 1>, 256);

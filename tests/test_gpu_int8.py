@@ -136,6 +136,20 @@ def test_empty(q):
         assert (got["s"] == 1).all() and (got["st"] == 1).all()
 
 
+def test_empty_with_addresses(q):
+    """A caller of the C interface may pass the addresses of copies that hold
+    nothing."""
+    buf = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(64, device="cuda")
+    p = buf.data_ptr()
+    q.qsg_quantize_int8(torch.empty((0, 64), dtype=BF, device="cuda"), q=p, s=p + 1024, qt=p + 2048, st=st,
+                        workspace=p + 3072)
+    s = torch.zeros(64, device="cuda")
+    q.qsg_quantize_int8(torch.empty((64, 0), dtype=BF, device="cuda"), q=p, s=s, qt=p + 2048, st=p + 1024,
+                        workspace=p + 3072)
+    assert (st == 1).all() and (s == 1).all() and not buf.any()
+
+
 def test_workspace_serves_smaller_shapes(q):
     ws = torch.empty(q.qsg_quantize_int8_workspace(700, 300), dtype=torch.uint8, device="cuda")
     for R, C in ((700, 300), (699, 300), (511, 299), (3, 300), (1, 1)):
