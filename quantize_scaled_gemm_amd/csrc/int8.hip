@@ -208,7 +208,7 @@ struct QuantArgs {
   float* st;
   float* part;  // column maxima of groups of rows
   int parts;
-  int64_t tile0;  // first tile of a launch of int8_col_kernel
+  int64_t tile0;  // first tile of a launch of int8_col_kernel, group of 64 columns of int8_colscale_kernel
 };
 
 // A row in the registers of TPR threads, CH chunks of 8 values each; the up to
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(256) void int8_colmax_kernel(QuantArgs a) {
 __global__ __launch_bounds__(1024) void int8_colscale_kernel(QuantArgs a) {
   __shared__ uint32_t red[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t col = (a.tile0 + blockIdx.x) * 64 + lane;
   const uint32_t* p = reinterpret_cast<const uint32_t*>(a.part) + (col < a.cols ? col : a.cols - 1);
   uint32_t m = 0;
   for (int k = wave; k < a.parts; k += 128) {
@@ -497,7 +497,11 @@ void launch_quantize(const QuantArgs& a, hipStream_t st) {
   if (a.st && a.cols > 0) {
     if (a.rows > 0 && !fused)
       hipLaunchKernelGGL(int8_colmax_kernel<In>, dim3((unsigned)((a.cols + 511) / 512), a.parts), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(int8_colscale_kernel, dim3((unsigned)((a.cols + 63) / 64)), dim3(1024), 0, st, a);
+    in_pieces((a.cols + 63) / 64, 1, [&](int64_t c, int64_t n) {
+      QuantArgs b = a;
+      b.tile0 = c;
+      hipLaunchKernelGGL(int8_colscale_kernel, dim3((unsigned)n), dim3(1024), 0, st, b);
+    });
     in_pieces((a.rows + 127) / 128 * ((a.cols + 63) / 64), 1, [&](int64_t t, int64_t n) {
       QuantArgs b = a;
       b.tile0 = t;

@@ -130,6 +130,22 @@ def test_nan_payloads(q):
     assert np.isnan(got["st"][[10, 299]]).all() and not got["qt"][[10, 299]].any()
 
 
+def test_many_columns(q):
+    """More columns than one launch has threads for their scales."""
+    cols = 2 ** 28 + 70
+    x = torch.zeros((1, cols), dtype=BF, device="cuda")
+    at = torch.tensor([0, 63, 64, 2 ** 27 - 1, 2 ** 27, 2 ** 28 - 1, 2 ** 28, 2 ** 28 + 69], device="cuda")
+    v = torch.tensor([1, -2, 3, -4, 5, -6, 7, -8], device="cuda").to(BF)
+    x[0, at] = v
+    qt, st = torch.full((cols, 1), 9, dtype=torch.int8, device="cuda"), torch.full((cols,), -1.0, device="cuda")
+    ws = torch.empty(q.qsg_quantize_int8_workspace(1, cols), dtype=torch.uint8, device="cuda")
+    q.qsg_quantize_int8(x, qt=qt, st=st, workspace=ws)
+    assert torch.equal(qt[at, 0], 127 * torch.sign(v.float()).to(torch.int8))
+    assert torch.equal(st[at], v.float().abs() / 127)
+    qt[at], st[at] = 0, 1.0
+    assert not qt.any() and (st == 1).all()
+
+
 def test_empty(q):
     for shape in ((0, 5), (5, 0), (0, 0)):
         got = quantize(q, torch.empty(shape, dtype=BF, device="cuda"))
