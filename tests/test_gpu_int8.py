@@ -409,3 +409,73 @@ def test_wgrad_largest_values(q, N, K):
     c = torch.full((N, K), 5.0, device="cuda")
     q.qsg_wgrad_int8(dy, qq, s, c)
     assert torch.equal(c, dy[69].float()[:, None] * x[None, :])
+
+
+# ---------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ---------------------------------------------------------------------------
+def far_rows(rows):
+    return torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device="cuda")
+
+
+def test_copies_beyond_32_bits(q):
+    rows, cols = 263000, 16400  # 4.3e9 values
+    x = torch.zeros((rows, cols), dtype=BF, device="cuda")
+    at = far_rows(rows)
+    v = torch.from_numpy(rng(31).standard_normal((5, cols))).to(BF).cuda()
+    x[at] = v
+    qq, s = torch.empty((rows, cols), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    qt, st = torch.empty((cols, rows), dtype=torch.int8, device="cuda"), torch.empty(cols, device="cuda")
+    ws = torch.empty(q.qsg_quantize_int8_workspace(rows, cols), dtype=torch.uint8, device="cuda")
+    q.qsg_quantize_int8(x, q=qq, s=s, qt=qt, st=st, workspace=ws)
+    vf = to_np(v)
+    check_copies({"q": to_np(qq[at]), "s": to_np(s[at])}, vf)
+    check_copies({"qt": to_np(qt[:, at].contiguous()), "st": to_np(st)}, vf)
+    assert int(torch.count_nonzero(s == 1)) == rows - 5
+    for part in qt.chunk(64):  # the other rows are zeros
+        part[:, at] = 0
+        assert not part.any()
+
+
+def test_activation_beyond_32_bits(q):
+    rows, cols = 132000, 16400  # 4.3e9 values of gu
+    gu = torch.zeros((rows, 2 * cols), dtype=BF, device="cuda")
+    at = far_rows(rows)
+    gu[at] = torch.from_numpy(rng(32).standard_normal((5, 2 * cols))).to(BF).cuda()
+    nb = -(-cols // 128)
+
+    def run(gu):
+        n = gu.shape[0]
+        o = [torch.empty((n, cols), dtype=BF, device="cuda"), torch.empty((n, cols), dtype=torch.int8, device="cuda"),
+             torch.empty(n, device="cuda"), torch.empty((n, 2 * cols), dtype=torch.int8, device="cuda"),
+             torch.empty((n, 2 * nb), device="cuda")]
+        q.qsg_swiglu_int8_store_fwd(gu, a=o[0], ck=o[3], cs=o[4])
+        q.qsg_swiglu_int8_store_fwd(gu, aq=o[1], sa=o[2])
+        dgu, a = torch.empty_like(gu), torch.empty_like(o[0])
+        q.qsg_swiglu_int8_store_bwd(o[0], o[3], o[4], dgu, a)
+        return [*o, dgu, a]
+
+    for big, small in zip(run(gu), run(gu[at].contiguous())):
+        assert torch.equal(big[at], small)
+
+
+@pytest.mark.parametrize("N, K", [(64, 16400), (61, 16401)])
+def test_products_beyond_32_bits(q, N, K):
+    rows = 263000  # 4.3e9 codes
+    a = torch.zeros((rows, K), dtype=torch.int8, device="cuda")
+    at = far_rows(rows)
+    ca = codes(33, 5, K)
+    a[at] = torch.from_numpy(ca).cuda()
+    cb = codes(34, N, K)
+    one, c = torch.ones(rows, device="cuda"), torch.full((rows, N), 5.0, device="cuda")
+    q.qsg_gemm_int8(a, one, torch.from_numpy(cb).cuda(), one[:N], c)
+    want = (ca.astype(np.int64) @ cb.astype(np.int64).T).astype(np.float32)
+    assert same(to_np(c[at]), want)
+    c[at] = 0
+    assert not c.any()
+    # the weight gradient of powers of two: every sum is exact
+    dy = torch.zeros((rows, N), dtype=BF, device="cuda")
+    dy[at] = 2.0 ** torch.arange(5, device="cuda", dtype=torch.float32).to(BF)[:, None]
+    w = torch.empty((N, K), device="cuda")
+    q.qsg_wgrad_int8(dy, a, one, w)
+    assert same(to_np(w), np.broadcast_to((ca * 2.0 ** np.arange(5)[:, None]).sum(0), (N, K)).astype(np.float32))
