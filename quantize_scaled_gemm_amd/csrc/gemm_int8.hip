@@ -3,13 +3,16 @@
 // Sums are 32-bit integers and exact, so they may be split and joined in any
 // order; only their scaling is rounded.
 //
-// Three kernels.  The 256 x 256 kernel of the FP8 products serves the large
-// ones (gemm_fast.hip); here are
-//   * few rows (a decode batch): bound by reading B once.  A workgroup owns 16
-//     columns (rows of B), its waves split K, and the operands go from memory
-//     straight into the registers of v_mfma_i32_16x16x64_i8, since no wave
-//     uses another's;
-//   * everything else: 128 x 128 tiles through LDS.
+// What bounds it depends on the rows of A: a decode batch reads B once (16 rows
+// through 28672 x 4096: 27 us, 4.4 TB/s), a training batch is matrix
+// instructions (32768 x 4096 x 4096: 437 us, 2.5 POP/s).  Five kernels:
+//   * 256 x 256 persistent tiles (gemm_fast.hip, the FP8 products' loop);
+//   * tiles of 64 and 128 by direct loads into a ring of LDS stages;
+//   * 16 to 32 rows of A by 16 to 64 of B, K split over a workgroup's waves, each
+//     with a ring of its own;
+//   * the same without LDS for 16 x 16, and tiles through registers: operands of
+//     any alignment.
+// launch_gemm_int8 says which serves what, with both sides' times.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -113,7 +116,9 @@ __device__ __forceinline__ void store4(const Int8Args& g, int64_t m, int64_t n, 
 // chunks of two instructions: both operands split K between lanes alike, so
 // every product is made once.  The instruction takes (B, A), and lane l then
 // holds row l % 16 of A and columns 4 (l / 16) .. +3.  The workgroup's waves
-// split K; a wave takes 8 steps at a time, all of their loads first.
+// split K; a wave takes 8 steps at a time, all of their loads first.  Bound by
+// the loads: one row through 28672 x 4096 in 22.3 us (5.3 TB/s), 16 rows in 34
+// (a lane's chunk of A costs the vector-memory path a clock as one of B does).
 constexpr int kFewWaves = 4, kFewSteps = 8;
 
 template <bool OUT_BF16>
@@ -210,7 +215,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* p, int
 // its own loads only.  16-byte chunk c of row r is at position c ^ ring_swz(r):
 // of a fragment read (lane l: row l % 16, chunk l / 16 or 4 + l / 16) the lanes
 // that the LDS serves together (8p .. 8p+7 with 8p+32 .. 8p+39) then meet
-// distinct banks.
+// distinct banks.  61 rows through 4096 x 14336 in 21 us, against 39 from
+// registers; through 28672 x 4096 in 32 against 65.
 __device__ __forceinline__ int ring_swz(int r) { return ((r >> 1) & 1) | ((r >> 3) & 1) << 1 | ((r >> 2) & 1) << 2; }
 
 template <int MT, int NT, int WAVES, int R, bool OUT_BF16>
@@ -333,7 +339,7 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_int8_ring_kernel(Int8Args g) 
 }
 
 // ---------------------------------------------------------------------------
-// 128 x 128 tiles
+// tiles
 // ---------------------------------------------------------------------------
 constexpr int TB = 128;  // rows of either operand, and bytes of K, of a tile
 
@@ -413,7 +419,9 @@ __device__ __forceinline__ void store_tile(const Int8Args& g, const v16i (&acc)[
 // Any alignment: through registers, two K tiles ahead.  A K tile is four phases
 // of 32 K, and a phase's fragments are read during the phase before; the
 // barrier behind which the next K tile is there lies before the last phase,
-// whose instructions cover the first reads from it.
+// whose instructions cover the first reads from it.  1021 x 4095 x 4095 in 41
+// us: loads of 16 bytes at any address are what bounds it (aligned, through
+// the kernel below, 22).
 template <int TM, int TN, bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
   constexpr int NI = TM / 64, NJ = TN / 64, LA = TM / 32, LB = TN / 32;
@@ -528,24 +536,21 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
                                (wave < 2 ? st0 : st1) + (wave & 1) * PART);
 }
 
-// TM x TN tiles of operands of whole 16 bytes: the loads go to LDS directly, S
-// - 1 K tiles ahead in a ring of S stages.  (Through registers and one tile
-// ahead, as above, a workgroup a CU waits for each tile's loads.)  A K tile is
-// four phases of 32 K, and a phase's fragments are read during the phase
-// before; the barrier behind which the next K tile is there lies before the
-// last phase, whose instructions cover the first reads from it.
-template <int TM, int TN, int S, bool OUT_BF16>
+// TM x TN tiles of operands of whole 16 bytes: the loads go to LDS directly, 3
+// K tiles ahead in a ring of 4 stages.  (Through registers and fewer tiles
+// ahead, as above, a workgroup a CU waits for each tile's loads: 1021 x 4096 x
+// 4096 with 128 x 128 tiles 37 us, 22 here.)  Phases as above.
+template <int TM, int TN, bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
   constexpr int NI = TM / 64, NJ = TN / 64;   // 32 x 32 tiles of a wave
   constexpr int LA = TM / 32, LB = TN / 32;   // loads of a wave and K tile
-  constexpr int STAGE = (TM + TN) * TB, WAIT = (S - 2) * (LA + LB);
+  constexpr int STAGE = (TM + TN) * TB, AHEAD = 3, WAIT = (AHEAD - 1) * (LA + LB);
   // distinct objects: reads of one stage wait for no load into another; A's
   // rows of 128 bytes, then B's
   __shared__ __attribute__((aligned(1024))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t st3[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t st4[S > 4 ? STAGE : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   // Workgroups go to the 8 XCDs in turn: each XCD gets a contiguous part of an
@@ -611,7 +616,7 @@ __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
       constexpr int L3 = (LA + LB + 2) / 3;
       if (s < 3) {
 #pragma unroll
-        for (int i = s * L3; i < (s + 1) * L3 && i < LA + LB; ++i) issue1(dst, kt + S - 1, i);
+        for (int i = s * L3; i < (s + 1) * L3 && i < LA + LB; ++i) issue1(dst, kt + AHEAD, i);
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i)
@@ -630,34 +635,19 @@ __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
   issue(st0, 0);
   issue(st1, 1);
   issue(st2, 2);
-  if constexpr (S > 4) issue(st3, 3);
   wait_vm<WAIT>();
   lds_barrier();
   read(st0, 0);
   int kt = 0;
-  if constexpr (S == 4) {
-    for (; kt + 4 <= nk; kt += 4) {
-      step(st0, st1, st3, kt);
-      step(st1, st2, st0, kt + 1);
-      step(st2, st3, st1, kt + 2);
-      step(st3, st0, st2, kt + 3);
-    }
-    if (kt < nk) step(st0, st1, st3, kt++);
-    if (kt < nk) step(st1, st2, st0, kt++);
-    if (kt < nk) step(st2, st3, st1, kt++);
-  } else {
-    for (; kt + 5 <= nk; kt += 5) {
-      step(st0, st1, st4, kt);
-      step(st1, st2, st0, kt + 1);
-      step(st2, st3, st1, kt + 2);
-      step(st3, st4, st2, kt + 3);
-      step(st4, st0, st3, kt + 4);
-    }
-    if (kt < nk) step(st0, st1, st4, kt++);
-    if (kt < nk) step(st1, st2, st0, kt++);
-    if (kt < nk) step(st2, st3, st1, kt++);
-    if (kt < nk) step(st3, st4, st2, kt++);
+  for (; kt + 4 <= nk; kt += 4) {
+    step(st0, st1, st3, kt);
+    step(st1, st2, st0, kt + 1);
+    step(st2, st3, st1, kt + 2);
+    step(st3, st0, st2, kt + 3);
   }
+  if (kt < nk) step(st0, st1, st3, kt++);
+  if (kt < nk) step(st1, st2, st0, kt++);
+  if (kt < nk) step(st2, st3, st1, kt++);
   wait_vm<0>();  // the loads past the last K tile have landed, and
   lds_barrier();  // no wave reads a stage any more
   constexpr int PART = 32 * kTilePitch<OUT_BF16, NJ>;
@@ -688,12 +678,12 @@ void launch_any(Int8Args g, bool bf16, hipStream_t st) {
   else hipLaunchKernelGGL((gemm_int8_kernel<TM, TN, false>), grid, dim3(256), 0, st, g);
 }
 
-template <int TM, int TN, int S>
+template <int TM, int TN>
 void launch_tile(Int8Args g, bool bf16, hipStream_t st) {
   g.tiles_m = (g.M + TM - 1) / TM;
   const dim3 grid((unsigned)(g.tiles_m * ((g.N + TN - 1) / TN)));
-  if (bf16) hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, S, true>), grid, dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, S, false>), grid, dim3(256), 0, st, g);
+  if (bf16) hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, true>), grid, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, false>), grid, dim3(256), 0, st, g);
 }
 
 }  // namespace
@@ -707,23 +697,46 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   g.bias_bf16 = bias_dtype == QSG_BF16;
   g.M = M; g.N = N; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.c = c;
   const bool bf16 = c_dtype == QSG_BF16;
+  // 256 x 256 tiles where they occupy half of the CUs (2048 x 4096 x 4096: 46 us,
+  // with 128 x 128 tiles 49; 4096 x 4096 x 4096: 61 and 97)
   if (M > 64 && launch_gemm_int8_fast(a, sa, b, sb, M, N, K, lda, ldb, bias, g.bias_bf16, c, c_dtype, ldc, st)) return;
   // direct loads: whole chunks, 31-bit offsets in 128 rows
   const bool dma = (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && K % 16 == 0 &&
                    K > 0 && lda < (1 << 24) && ldb < (1 << 24);
   auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
   if (!dma) {
+    // 128 x 128 tiles where they occupy the chip (1021 x 4095 x 4095: 41 us, with
+    // 64 x 64 58); 16 rows and few columns split K over waves instead (16 x 4095
+    // x 4095: 17.1 us, with 64 x 64 20; one row of 14001 x 4095: 33 and 24)
     if (M > 64 && tiles(128, 128) >= 192) launch_any<128, 128>(g, bf16, st);
     else if (M > 16 || tiles(64, 64) >= 100) launch_any<64, 64>(g, bf16, st);
     else launch_few(g, bf16, st);
     return;
   }
-  if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128, 4>(g, bf16, st);
-  else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128, 4>(g, bf16, st);
-  else if (M > 32 && tiles(64, 64) >= 160) launch_tile<64, 64, 4>(g, bf16, st);
+  // The largest tiles that still occupy most of the chip (us with tiles of 128 x
+  // 128, 64 x 128 and 64 x 64):
+  //   256 x 28672 x 4096 (448 tiles of 128 x 128)   55   74   73
+  //   1021 x 4096 x 4096 (256)                      22   27   29
+  //   512 x 4096 x 4096 (256 of 64 x 128)           18   15   16
+  //   1021 x 1024 x 4096 (256 of 64 x 64)           18   13   10
+  //   256 x 4096 x 4096 (256)                       17   13   11
+  if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128>(g, bf16, st);
+  else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128>(g, bf16, st);
+  else if (M > 32 && tiles(64, 64) >= 160) launch_tile<64, 64>(g, bf16, st);
+  // fewer tiles: K split over the waves.  Tiles of 64 x 64, rings of 32 x 64 and
+  // of 32 x 32:
+  //   61 x 14336 x 4096 (224 tiles of 64 x 64)      18    -   23
+  //   256 x 4096 x 14336 (256)                      37   48    -
+  //   128 x 4096 x 14336 (128; 256 of 32 x 64)      37   27   33
+  //   61 x 4096 x 14336 (64; 128)                   38    -   21
   else if (M > 64 && tiles(32, 64) >= 200) launch_ring<2, 4, 4, 2>(g, bf16, st);
+  // rings of 32 x 32 or 32 x 16, 16 x 32 or 16 x 16: enough workgroups, then
+  // fewer reads of A (32 x 28672 x 4096: 30 and 35 us; 32 x 4096 x 14336: 22 and
+  // 18; 16 x 28672 x 4096: 27 and 30; 16 x 4096 x 14336: 18 and 14)
   else if (M > 32 || (M > 16 && N >= 12288)) launch_ring<2, 2, 4, 2>(g, bf16, st);
   else if (M > 16) launch_ring<2, 1, 4, 3>(g, bf16, st);
+  // up to 4 rows read A's lines so seldom that LDS does not pay (28672 x 4096:
+  // one row 22 us, with the ring 26; 4 rows 24 and 26; 8 rows 28 and 26)
   else if (M <= 4 && N >= 12288) launch_few(g, bf16, st);
   else if (N >= 12288) launch_ring<1, 2, 4, 2>(g, bf16, st);
   else launch_ring<1, 1, 4, 4>(g, bf16, st);
