@@ -111,7 +111,7 @@ __device__ __forceinline__ void store4(const Int8Args& g, int64_t m, int64_t n, 
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-// 16 rows of A against 16 rows of B, any alignment.  Lane l holds row l % 16
+// 16 rows of A against 16 rows of B to a workgroup, any alignment.  Lane l holds row l % 16
 // of either operand and, of a step of 128 K, bytes 32 (l / 16) .. +31 as two
 // chunks of two instructions: both operands split K between lanes alike, so
 // every product is made once.  The instruction takes (B, A), and lane l then
@@ -125,10 +125,10 @@ template <bool OUT_BF16>
 __global__ __launch_bounds__(kFewWaves * 64) void gemm_int8_few_kernel(Int8Args g) {
   __shared__ v4i red[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t m0 = (int64_t)blockIdx.y * 16, n0 = (int64_t)blockIdx.x * 16;
   const int at = (lane >> 4) * 32;
   // rows past the end read the last one; their results are not stored
-  const int64_t m = (lane & 15) < g.M ? (lane & 15) : g.M - 1;
+  const int64_t m = m0 + (lane & 15) < g.M ? m0 + (lane & 15) : g.M - 1;
   const int64_t n = n0 + (lane & 15) < g.N ? n0 + (lane & 15) : g.N - 1;
   const int8_t* a = g.a + m * g.lda;
   const int8_t* b = g.b + n * g.ldb;
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void gemm_int8_few_kernel(Int8Args 
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w) v += red[w][lane];
     const int sum[4] = {v[0], v[1], v[2], v[3]};
-    store4<OUT_BF16>(g, lane & 15, n0 + 4 * (lane >> 4), sum, sa, cols);
+    store4<OUT_BF16>(g, m0 + (lane & 15), n0 + 4 * (lane >> 4), sum, sa, cols);
   }
 }
 
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
 }
 
 void launch_few(const Int8Args& g, bool bf16, hipStream_t st) {
-  const dim3 grid((unsigned)((g.N + 15) / 16)), block(kFewWaves * 64);
+  const dim3 grid((unsigned)((g.N + 15) / 16), (unsigned)((g.M + 15) / 16)), block(kFewWaves * 64);
   if (bf16) hipLaunchKernelGGL(gemm_int8_few_kernel<true>, grid, block, 0, st, g);
   else hipLaunchKernelGGL(gemm_int8_few_kernel<false>, grid, block, 0, st, g);
 }
@@ -706,11 +706,14 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
   if (!dma) {
     // 128 x 128 tiles where they occupy the chip (1021 x 4095 x 4095: 41 us, with
-    // 64 x 64 58); 16 rows and few columns split K over waves instead (16 x 4095
-    // x 4095: 17.1 us, with 64 x 64 20; one row of 14001 x 4095: 33 and 24)
+    // 64 x 64 58).  K split over waves instead where that needs no more workgroups
+    // than CUs (53 x 608 x 12275: 33 us, with 64 x 64 43; 130 x 130 x 333: 3.9 and
+    // 5.8; beyond, 64 x 2000 x 4095: 31 and 19), or for one row of blocks that 64 x
+    // 64 would fill to a quarter (16 x 4095 x 4095: 17 and 20; one row of 14001 x
+    // 4095: 33 and 24)
     if (M > 64 && tiles(128, 128) >= 192) launch_any<128, 128>(g, bf16, st);
-    else if (M > 16 || tiles(64, 64) >= 100) launch_any<64, 64>(g, bf16, st);
-    else launch_few(g, bf16, st);
+    else if (tiles(16, 16) <= 256 || (M <= 16 && tiles(64, 64) < 100)) launch_few(g, bf16, st);
+    else launch_any<64, 64>(g, bf16, st);
     return;
   }
   // The largest tiles that still occupy most of the chip (us with tiles of 128 x
