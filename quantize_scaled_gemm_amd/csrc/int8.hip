@@ -212,7 +212,9 @@ struct QuantArgs {
 };
 
 // A row in the registers of TPR threads, CH chunks of 8 values each; the up to
-// 7 values behind the last whole chunk go one to a thread.
+// 7 values behind the last whole chunk go one to a thread.  Bound by memory, x
+// read once and its codes written: 32768 x 4096 bf16 in 64 us (6.3 TB/s), 32768
+// x 1111 in 22, one row of 4096 in 2.8.
 template <typename In, int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_row_kernel(QuantArgs a) {
   constexpr int NT = TPR < 256 ? 256 : TPR;
@@ -247,7 +249,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_row_kernel(QuantAr
   if (t == 0) a.s[row] = s.s;
 }
 
-// Rows that are too long for registers are read twice.
+// Rows that are too long for registers are read twice (4096 x 28672 bf16 in 95
+// us this way, in 58 from registers; rows of 40000 have no other).
 template <typename In>
 __global__ __launch_bounds__(1024) void int8_long_row_kernel(QuantArgs a) {
   __shared__ uint32_t red[16];
@@ -398,7 +401,8 @@ __global__ __launch_bounds__(1024) void int8_colscale_kernel(QuantArgs a) {
 
 // A tile of 128 rows x 64 columns: a thread encodes 4 rows x 8 columns and
 // puts each column's 4 codes into LDS as one word; a column's 128 codes then
-// leave as one run of 8 lanes.
+// leave as one run of 8 lanes.  Bound by reading x a second time: of the 111 us
+// of both copies of 14336 x 4096 fp32 this pass takes half.
 constexpr int kColRow = 33;  // words of an LDS column: 32, and one that spreads the banks
 template <typename In>
 __global__ __launch_bounds__(256) void int8_col_kernel(QuantArgs a) {
@@ -481,15 +485,16 @@ void launch_quantize(const QuantArgs& a, hipStream_t st) {
     else if (a.cols <= 8192) go(int8_row_col_kernel<In, 512, 2>, 512);
     else go(int8_row_col_kernel<In, 1024, 2>, 1024);
   } else if (a.s) {  // by the scales: an empty copy may have no address
+    // as few threads as hold a row with 4 chunks each (32768 x 4096 bf16: 64 us,
+    // with one chunk 75; 8192 x 12000: 50 and, with two, 55; 4096 x 28672: 58 and,
+    // read twice, 95); narrow rows fewer of them, which chunks past the end cost
+    // more than they hide (32768 x 700: 15 us with two, 16.5 with four; 100000 x
+    // 300: 26 with one, 34; 32768 x 256: 6.2 with 16 threads a row, 9.1 with 64)
     if (a.cols <= 256) launch_rows<In, 16, 2>(a, st);
     else if (a.cols <= 512) launch_rows<In, 64, 1>(a, st);
     else if (a.cols <= 1024) launch_rows<In, 64, 2>(a, st);
-    else if (a.cols <= 1536) launch_rows<In, 64, 3>(a, st);
     else if (a.cols <= 2048) launch_rows<In, 64, 4>(a, st);
-    else if (a.cols <= 4096) launch_rows<In, 256, 2>(a, st);
-    else if (a.cols <= 6144) launch_rows<In, 256, 3>(a, st);
     else if (a.cols <= 8192) launch_rows<In, 256, 4>(a, st);
-    else if (a.cols <= 12288) launch_rows<In, 512, 3>(a, st);
     else if (a.cols <= 16384) launch_rows<In, 512, 4>(a, st);
     else if (a.cols <= 32768) launch_rows<In, 1024, 4>(a, st);
     else launch_rows<In, 1024, 0>(a, st);
@@ -576,7 +581,8 @@ __device__ __forceinline__ void keep_block(const GluArgs& a, const BlockAt& at, 
 }
 
 // One block of 128 of g and of u to 16 neighbouring lanes; groups of lanes take
-// the blocks of the matrix in turn.
+// the blocks of the matrix in turn.  Bound by memory: 16384 x 14336 bf16 in 339
+// us (5.5 TB/s: gu read, a and the codes written), 333 x 1111 fp32 in 4.6.
 template <typename In>
 __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
@@ -604,7 +610,8 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
 }
 
 // With an INT8 copy of a: a row to a workgroup, which holds a in registers (CH
-// > 0, CH chunks of 8 a thread) or computes it twice (CH == 0).
+// > 0, CH chunks of 8 a thread) or computes it twice (CH == 0).  8192 x 14336
+// bf16 with gu kept in 147-150 us (5.5 TB/s), 61 x 14336 in 7.
 template <typename In, int NT, int CH>
 __global__ __launch_bounds__(NT) void swiglu_row_kernel(GluArgs a) {
   __shared__ uint32_t red[NT / 64];
@@ -681,6 +688,8 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg
   act = w * u;
 }
 
+// Blocks of 128 as the forward pass takes them; bound by memory: 16384 x 14336
+// bf16 with a in 422 us, without 324 (5.6 and 5.8 TB/s), 333 x 1111 fp32 in 4.7.
 template <typename In>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
@@ -744,8 +753,11 @@ void launch_glu_row(const GluArgs& all, hipStream_t st) {
 template <typename In>
 void launch_glu_fwd(const GluArgs& a, hipStream_t st) {
   if (a.sa) {  // an empty copy may have no address
-    // few rows: more threads a row, for the latency of its loads (61 x 14336:
-    // 7.5 us with 512 threads, 5.5 with 1024)
+    // few rows: more threads a row, for the latency of its loads (aq alone of 61 x
+    // 14336: 7.5 us with 512 threads, 5.5 with 1024); many rows: more chunks a
+    // thread (16384 x 8192: 157 us with 512 threads of two, 164 with 1024 of one;
+    // 32768 x 2048: 86 with 256, 111 with 512; 4096 x 28672: 170, and 217 without
+    // registers)
     const bool few = a.rows <= 256;
     if (few && a.cols > 8192 && a.cols <= 16384) launch_glu_row<In, 1024, 2>(a, st);
     else if (few && a.cols > 2048 && a.cols <= 8192) launch_glu_row<In, 1024, 1>(a, st);
