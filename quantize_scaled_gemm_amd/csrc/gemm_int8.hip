@@ -496,8 +496,12 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
   };
   // K tile kt in `cur`; kt + 1 goes from `ready` to `next`, kt + 2 is fetched into `other`
   auto step = [&](const uint8_t* cur, uint8_t* next, const Regs& ready, Regs& other, int kt, auto all_plain) {
-    if constexpr (decltype(all_plain)::value) fetch_plain(other, kt + 2);
-    else fetch(other, kt + 2);
+    if constexpr (decltype(all_plain)::value) {
+      fetch_plain(other, kt + 2);
+      __builtin_amdgcn_sched_barrier(0);  // the loads first, not where their registers are needed
+    } else {
+      fetch(other, kt + 2);
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) {
@@ -708,9 +712,9 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
     // 128 x 128 tiles where they occupy the chip (1021 x 4095 x 4095: 41 us, with
     // 64 x 64 58).  K split over waves instead where that needs no more workgroups
     // than CUs (53 x 608 x 12275: 33 us, with 64 x 64 43; 130 x 130 x 333: 3.9 and
-    // 5.8; beyond, 64 x 2000 x 4095: 31 and 19), or for one row of blocks that 64 x
+    // 5.8; beyond, 64 x 2000 x 4095: 31 and 18), or for one row of blocks that 64 x
     // 64 would fill to a quarter (16 x 4095 x 4095: 17 and 20; one row of 14001 x
-    // 4095: 33 and 24)
+    // 4095: 33 and 22)
     if (M > 64 && tiles(128, 128) >= 192) launch_any<128, 128>(g, bf16, st);
     else if (tiles(16, 16) <= 256 || (M <= 16 && tiles(64, 64) < 100)) launch_few(g, bf16, st);
     else launch_any<64, 64>(g, bf16, st);
