@@ -660,25 +660,29 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
 
 // ---- INT8 X, any shape and alignment, and few tiles ----
 //
-// TILE x TILE outputs to a workgroup of 4 waves, (TILE / 2) x (TILE / 2) each;
-// 64 tokens a step through registers into one of two LDS stages, in the
+// TILE x TILE outputs to 4 waves, (TILE / 2) x (TILE / 2) each, or 32 x 32 to
+// one; 64 tokens a step through registers into one of two LDS stages, in the
 // layout that the transpose reads want: dY as it lies in memory, X widened to
 // bf16.  Loads ask for no alignment.  Features past the end of an operand
 // only reach results that are not stored, so a row may be read past its end
 // where memory goes on, into the next row; only a step in which it might not
-// (the last one or two) is loaded with more care.  777 x 1000 x 1111 in 16 us and
-// 8192 x 1024 x 1024 in 46: with few tiles a step's latency bounds it, which two
-// steps of loads in flight and the groups below hide in part.
+// (the last one or two) is loaded with more care.  777 x 1000 x 1111 in 15.6 us,
+// 8192 x 1024 x 1024 in 41: the loads bound it, at a lane's 16 bytes a clock (34
+// to 50 bytes a ns on a CU), not their latency (twice as many in flight change
+// nothing).
 template <int TILE>
 struct SmallStage {
-  static constexpr int ROW = TILE * 2;                // bytes of a token
-  static constexpr int AC = TILE / 32, XC = TILE / 64;  // 16-byte chunks of dY, of X a thread loads per step
+  static constexpr int ROW = TILE * 2;                   // bytes of a token
+  static constexpr int WAVES = TILE >= 64 ? 4 : 1;       // that share a stage
+  static constexpr int STAGES = WAVES > 1 ? 2 : 1;       // a wave's LDS accesses are in order: one is enough
+  static constexpr int NT = TILE >= 64 ? TILE / 64 : 1;  // 32 x 32 MFMA tiles of a wave, each way
+  static constexpr int AC = TILE / 8 / WAVES, XC = TILE / 16 / WAVES;  // 16-byte chunks of dY, of X a thread loads per step
 };
 
 // chunk c of token row t: 4 consecutive rows x 4 chunks on distinct banks
 template <int TILE>
 __device__ __forceinline__ int small_swz(int t, int c) {
-  return TILE >= 128 ? c ^ ((t & 3) << 2) : c ^ (((t >> 1) & 1) << 2);
+  return TILE >= 128 ? c ^ ((t & 3) << 2) : TILE >= 64 ? c ^ (((t >> 1) & 1) << 2) : c;
 }
 template <int TILE>
 __device__ __forceinline__ int small_tr_offset(int fblk, int lane) {
@@ -707,16 +711,16 @@ __device__ __forceinline__ u32x4 tail_chunk(const uint8_t* p, int64_t at, int64_
   return r;
 }
 
-// GROUPS of 4 waves take the steps in turn and join their sums in the end: with
-// few tiles a workgroup is alone on its CU.  A step's loads are two of a group's
-// steps ahead, in registers, and go to LDS one step ahead.
+// GROUPS of these waves take the steps in turn and join their sums in the end:
+// with few tiles a workgroup is alone on its CU.  A step's loads are two of a
+// group's steps ahead, in registers, and go to LDS one step ahead.
 template <int TILE, int GROUPS>
-__global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args g) {
+__global__ __launch_bounds__(64 * SmallStage<TILE>::WAVES * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args g) {
   using S = SmallStage<TILE>;
-  constexpr int NT = TILE / 64;  // 32 x 32 MFMA tiles of a wave, each way
-  __shared__ __attribute__((aligned(16))) uint8_t la[GROUPS][2][BT * S::ROW];
-  __shared__ __attribute__((aligned(16))) uint8_t lx[GROUPS][2][BT * S::ROW];
-  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), tid = threadIdx.x & 255;
+  constexpr int NT = S::NT, TH = 64 * S::WAVES;
+  __shared__ __attribute__((aligned(16))) uint8_t la[GROUPS][S::STAGES][BT * S::ROW];
+  __shared__ __attribute__((aligned(16))) uint8_t lx[GROUPS][S::STAGES][BT * S::ROW];
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / TH), tid = threadIdx.x % TH;
   const int lane = tid & 63, wave = tid >> 6;
   const int wn = wave >> 1, wk = wave & 1;
   const int64_t n0 = (int64_t)blockIdx.y * TILE, k0 = (int64_t)blockIdx.x * TILE;
@@ -724,9 +728,9 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
   int at[S::AC], xt[S::XC];
   const int ac = tid % (TILE / 8), xc = tid % (TILE / 16);
 #pragma unroll
-  for (int i = 0; i < S::AC; ++i) at[i] = (i * 256 + tid) / (TILE / 8);
+  for (int i = 0; i < S::AC; ++i) at[i] = (i * TH + tid) / (TILE / 8);
 #pragma unroll
-  for (int i = 0; i < S::XC; ++i) xt[i] = (i * 256 + tid) / (TILE / 16);
+  for (int i = 0; i < S::XC; ++i) xt[i] = (i * TH + tid) / (TILE / 16);
   // a chunk that begins past the end reads the last one that does not
   const int64_t a_last = (g.N - 1) / 8 * 8, x_last = (g.K - 1) / 16 * 16;
   const int64_t af = n0 + 8 * ac < a_last ? n0 + 8 * ac : a_last;
@@ -812,11 +816,16 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
   // A workgroup barrier without a fence, which would wait for the fetches in
-  // flight.
+  // flight.  (A wave that has a stage of its own only waits for its writes.)
+  // Nothing moves across: the widening of the next step's codes would, and then
+  // wait for loads just issued (8192 x 1024 x 1024: 47 us, 42 with both this and
+  // the fetches kept in front of the work).
   auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+    if constexpr (S::WAVES > 1) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   };
   // Step s in stage st: the group's next one goes from `ready` to the other
   // stage, and the one after it is fetched.
@@ -837,14 +846,15 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
   };
   auto step_plain = [&](int st, const Regs& ready, Regs& other, int64_t s) {
     fetch_plain(other, s + 2 * GROUPS);
+    __builtin_amdgcn_sched_barrier(0);
     work(st);
-    put(st ^ 1, ready);
+    put((st ^ 1) & (S::STAGES - 1), ready);
     barrier();
   };
   auto step = [&](int st, const Regs& ready, Regs& other, int64_t s) {
     fetch(other, s + 2 * GROUPS);
     if (s < nsteps) work(st);
-    if (s + GROUPS < nsteps) put(st ^ 1, ready);
+    if (s + GROUPS < nsteps) put((st ^ 1) & (S::STAGES - 1), ready);
     barrier();
   };
   Regs r0, r1;
@@ -852,19 +862,22 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
   fetch(r1, group + GROUPS);
   if (group < nsteps) put(0, r0);
   barrier();
+  // nothing in flight before the loop: else what the compiler knows of the loads
+  // above makes every turn wait for the loads that it has just issued
+  wait_vm<0>();
   int64_t s = 0;
   for (; s + 4 * GROUPS <= plain; s += 2 * GROUPS) {
     step_plain(0, r1, r0, s + group);
-    step_plain(1, r0, r1, s + GROUPS + group);
+    step_plain(S::STAGES - 1, r0, r1, s + GROUPS + group);
   }
   for (; s < nsteps; s += 2 * GROUPS) {
     step(0, r1, r0, s + group);
-    if (s + GROUPS < nsteps) step(1, r0, r1, s + GROUPS + group);
+    if (s + GROUPS < nsteps) step(S::STAGES - 1, r0, r1, s + GROUPS + group);
   }
   if constexpr (GROUPS > 1) {
     // the other groups' sums, added in their order, through the first stages
-    // (16 KB of each group; nothing of them is read any more)
-    static_assert(NT == 1 && 2 * BT * S::ROW >= 16384, "a group's sums fit its stages");
+    // (nothing of them is read any more)
+    static_assert(NT == 1 && S::STAGES * BT * S::ROW >= 4096 * S::WAVES, "a group's sums fit its stages");
     float* sums = reinterpret_cast<float*>(la[group][0]) + wave * 1024 + lane * 4;
     if (group > 0) {
 #pragma unroll
@@ -889,7 +902,8 @@ __global__ __launch_bounds__(256 * GROUPS) void gemm_wgrad_int8_kernel(Bf16Args 
   }
   // behind the last step's barrier no wave reads a stage any more
   constexpr int PART = 32 * kRowPitch<NT>;
-  static_assert(2 * PART * 4 <= 2 * BT * S::ROW, "two waves' rows fit a group's stages");
+  static_assert(2 * PART * 4 <= 2 * BT * S::ROW || (S::WAVES == 1 && GROUPS > 1 && PART * 4 <= 2 * BT * S::ROW),
+                "two waves' rows fit a group's stages, or one's two groups'");
   float* part = reinterpret_cast<float*>(wave < 2 ? la[0][0] : lx[0][0]) + (wave & 1) * PART;
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -937,15 +951,19 @@ void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const
     return;
   }
   // What fills the chip with the largest tiles (2048 x 2000 x 3111, 400 tiles of
-  // 128 x 128: 52 us, with 64 x 64 91); with no more 64 x 64 tiles than
-  // CUs four groups of waves share one (8192 x 1024 x 1024: 47 us, with two
-  // groups 54, with one 68), with more of them two, two workgroups to a CU
-  // (777 x 1000 x 1111, 288 tiles: 15 us, with four groups 20).
+  // 128 x 128: 52 us, with 64 x 64 91).  With no more 64 x 64 tiles than CUs four
+  // groups of waves share one (8192 x 1024 x 1024: 41 us; earlier, 47 against 54
+  // with two groups and 68 with one), with more of them two, two workgroups to a
+  // CU (777 x 1000 x 1111, 288 tiles: 16 us, with four groups 20).  With no more
+  // 32 x 32 tiles than CUs these, eight waves each (15339 x 541 x 172: 57 us, with
+  // 64 x 64 75; 2048 x 512 x 512: 12.6 and 14.9; beyond, 8192 x 640 x 640, 400
+  // tiles: 48 and 37).
   auto go = [&](auto kernel, int tile, int threads) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((K + tile - 1) / tile), (unsigned)((N + tile - 1) / tile)), dim3(threads),
                        0, st, g);
   };
-  if (tiles(128) >= 256) go(gemm_wgrad_int8_kernel<128, 1>, 128, 256);
+  if (tiles(32) <= 256) go(gemm_wgrad_int8_kernel<32, 8>, 32, 512);
+  else if (tiles(128) >= 256) go(gemm_wgrad_int8_kernel<128, 1>, 128, 256);
   else if (tiles(64) > 256) go(gemm_wgrad_int8_kernel<64, 2>, 64, 512);
   else go(gemm_wgrad_int8_kernel<64, 4>, 64, 1024);
 }

@@ -347,7 +347,7 @@ def wgrad(q, T, N, K, out, accumulate=False, whole=False, pad=0):
 
 WGRAD = [(1, 1, 1), (1, 8, 16), (7, 33, 40), (16, 256, 256), (47, 8, 16), (48, 64, 128), (49, 264, 272), (63, 100, 257),
          (64, 256, 300), (65, 512, 16), (97, 24, 48), (144, 300, 256), (145, 256, 512), (200, 130, 77), (777, 264, 400),
-         (1000, 40, 304)]
+         (1000, 40, 304), (1500, 72, 333), (2600, 72, 333), (2113, 520, 500), (1601, 600, 650), (1601, 1100, 1050), (600, 2050, 2100)]
 
 
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
