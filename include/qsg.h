@@ -15,6 +15,9 @@
  *   "How to reduce cuda memory usage of fp8?" (TransformerEngine issue 1764):
  *     the backward pass of a Linear reads a transposed FP8 copy of its input,
  *     hence the fused cast + transpose.
+ *   Beside FP8: NVFP4, and INT8 with a scale for each token and channel (the
+ *     products of an MLP, its gated activation and the weight gradient); their
+ *     sections below define them.
  *   Outside the pages: the FP8 bit layouts of the OCP 8-bit floating point
  *   specification (E4M3 max 448, E5M2 max 57344) and the E8M0 scale byte of
  *   the OCP Microscaling v1.0 specification.
@@ -416,15 +419,18 @@ int qsg_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int6
  *     C[m, n] = fp32(fp32(sum_k A[m, k] * B[n, k]) * sa[m]) * sb[n] + bias[n]
  *
  * The sum is exact (32-bit integers; K <= 131071, QSG_ERR_UNSUPPORTED beyond);
- * its scaling is binary32 and C is rounded once.
+ * its scaling is binary32 and C is rounded once.  K == 0 writes the bias, or
+ * zeros.
  *   a, sa  M x K codes (lda) with M fp32 scales;  b, sb  N x K (ldb) with N.
  *   bias   N values of bias_dtype (QSG_F32 or QSG_BF16), or NULL.
  *   c      M x N (ldc) of c_dtype, aligned to its element size; it may not
  *          overlap an input.
- * fprop takes the row-wise copies of X and W, dgrad those of dY and the
+ * M and N up to 2^26, and C of up to 2^23 tiles of 128 x 128
+ * (QSG_ERR_UNSUPPORTED).  fprop takes the row-wise copies of X and W, dgrad those of dY and the
  * transposed copy of W.  Any shape and alignment: 16-byte aligned operands
- * with leading dimensions of whole 16 bytes and K % 256 == 0 select the
- * fastest kernel where C has at least 128 tiles of 256 x 256. */
+ * with leading dimensions of whole 16 bytes and K % 256 == 0 (and a bias on 4
+ * bytes, for a bf16 one with even N) select the fastest kernel where C has at
+ * least 128 tiles of 256 x 256; K % 16 == 0 with that alignment direct loads. */
 int qsg_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N, int64_t K,
                   int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype, int64_t ldc,
                   void* stream);
@@ -442,7 +448,8 @@ int qsg_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float
  * exact in binary32 and are summed there.  T == 0 writes zeros (or adds +0).
  * Accumulation into bf16 returns QSG_ERR_UNSUPPORTED.  Any alignment; 16-byte
  * aligned dy and q with lddy % 8 == 0, ldq % 16 == 0, N % 8 == 0 and
- * K % 16 == 0 select the fast path. */
+ * K % 16 == 0 select the fast path where C has at least 128 tiles of 256 x
+ * 256.  N <= 65535 * 128 and K <= 2^26 (QSG_ERR_UNSUPPORTED). */
 int qsg_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int8_t* q, const float* s, int64_t K,
                    int64_t ldq, void* c, int c_dtype, int64_t ldc, int accumulate, void* stream);
 
