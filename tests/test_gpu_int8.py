@@ -159,10 +159,10 @@ def test_empty_with_addresses(q):
     st = torch.zeros(64, device="cuda")
     p = buf.data_ptr()
     q.qsg_quantize_int8(torch.empty((0, 64), dtype=BF, device="cuda"), q=p, s=p + 1024, qt=p + 2048, st=st,
-                        workspace=p + 3072)
+                        workspace=p + 3328)
     s = torch.zeros(64, device="cuda")
     q.qsg_quantize_int8(torch.empty((64, 0), dtype=BF, device="cuda"), q=p, s=s, qt=p + 2048, st=p + 1024,
-                        workspace=p + 3072)
+                        workspace=p + 3328)
     assert (st == 1).all() and (s == 1).all() and not buf.any()
 
 
