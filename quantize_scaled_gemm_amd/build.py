@@ -26,6 +26,8 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
     "-Wno-unused-function",
+    # sources side by side (4 min -> 1 min 45 s with 8 CPUs)
+    "-parallel-jobs=6",
 ]
 
 
