@@ -479,3 +479,26 @@ def test_products_beyond_32_bits(q, N, K):
     w = torch.empty((N, K), device="cuda")
     q.qsg_wgrad_int8(dy, a, one, w)
     assert same(to_np(w), np.broadcast_to((ca * 2.0 ** np.arange(5)[:, None]).sum(0), (N, K)).astype(np.float32))
+
+
+@pytest.mark.parametrize("out, accumulate", [(BF, False), (F32, False), (F32, True)])
+@pytest.mark.parametrize("T, N, K, pad", [
+    (1, 2056, 4112, 0), (47, 2056, 4112, 16), (49, 2304, 3856, 0), (96, 2048, 4096, 0), (144, 2056, 4112, 8),
+    (145, 4096, 2320, 16), (337, 2056, 4112, 0),                                   # direct loads, 128 tiles and more
+    (200, 2000, 2500, 0), (333, 2001, 2050, 3), (70, 1100, 1050, 5), (333, 600, 650, 1), (600, 130, 333, 0),
+    (2600, 40, 70, 7), (5000, 33, 129, 1)])                                        # other tiles
+def test_wgrad_into_views(q, T, N, K, pad, out, accumulate):
+    """C with rows further apart: every output, exactly (whole numbers of few
+    bits), and nothing beside it written."""
+    g = torch.Generator("cuda").manual_seed(T + N + K)
+    dy = torch.randint(-4, 5, (T, N + pad), device="cuda", generator=g).to(BF)[:, :N]
+    qq = torch.randint(-8, 9, (T, K + pad), device="cuda", dtype=torch.int8, generator=g)[:, :K]
+    s = 2.0 ** torch.randint(0, 3, (T,), device="cuda", generator=g).float()
+    full = torch.randint(-9, 10, (N, K + pad), device="cuda", generator=g).to(out)
+    before = full.clone()
+    q.qsg_wgrad_int8(dy, qq, s, full[:, :K], accumulate=accumulate)
+    want = dy.double().t().contiguous() @ (qq.double() * s.double()[:, None])
+    if accumulate:
+        want += before[:, :K].double()
+    assert torch.equal(full[:, :K], want.to(out))
+    assert torch.equal(full[:, K:], before[:, K:])
