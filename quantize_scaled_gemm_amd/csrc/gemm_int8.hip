@@ -4,7 +4,7 @@
 // order; only their scaling is rounded.
 //
 // What bounds it depends on the rows of A: a decode batch reads B once (16 rows
-// through 28672 x 4096: 27 us, 4.4 TB/s), a training batch is matrix
+// through 28672 x 4096: 25 us, 4.7 TB/s), a training batch is matrix
 // instructions (32768 x 4096 x 4096: 437 us, 2.5 POP/s).  Five kernels:
 //   * 256 x 256 persistent tiles (gemm_fast.hip, the FP8 products' loop);
 //   * tiles of 64 and 128 by direct loads into a ring of LDS stages;
@@ -43,6 +43,12 @@ struct Int8Args {
   int64_t M, N, K, lda, ldb, ldc;
   void* c;
   int64_t tiles_m;
+  // Rows of B a multiple of 4096 bytes apart begin in the same few memory
+  // channels, and workgroups that read B in step meet there: each group of 8
+  // neighbours then begins at another K step (a sum has no order) and goes
+  // round (16 x 28672 x 4096: 27.2 -> 25.0 us, 32 x 16384 x 8192: 31.7 -> 27.8;
+  // other row lengths, and more rows than 64, gain nothing).
+  int turn;
 };
 
 // 16 bytes of a row of K bytes at k; what lies past its end is 0.  One load
@@ -247,9 +253,11 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_int8_ring_kernel(Int8Args g) 
     vb[i] = (8 * i + pr) * (uint32_t)g.ldb + ch[i] * 16;
   }
   const int K = (int)g.K, nk = (K + 127) / 128, rounds = (nk + WAVES - 1) / WAVES;
+  const int first = g.turn ? (int)(tn / 8 * WAVES % nk) : 0;  // the step to begin with
   uint32_t mine = wave * STEP;
   auto issue = [&](uint8_t* st, int round) {
-    const int k = (round * WAVES + wave) * 128;
+    const int at = round * WAVES + wave, turned = at + first < nk ? at + first : at + first - nk;
+    const int k = at < nk ? turned * 128 : K;
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
       const uint32_t off = k + ch[i & 1] * 16 < K ? vb[i & 1] + (uint32_t)(i >> 1) * 16 * (uint32_t)g.ldb + k : OUT_OF_RANGE;
@@ -572,12 +580,14 @@ __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
   const __amdgpu_buffer_rsrc_t ra = rows_rsrc(g.a, m0, g.M, g.lda, TM), rb = rows_rsrc(g.b, n0, g.N, g.ldb, TN);
   const TileScales<NI, NJ> scales(g, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane);
   const int K = (int)g.K, nk = (K + TB - 1) / TB;
+  const int first = g.turn ? (int)(in / high / 8 % nk) : 0;  // the K tile to begin with
   // load i (of A's and then B's) of K tile kt; past the last row, or the
   // last 16 bytes of a row, 0 is read
   auto issue1 = [&](uint8_t* dst, int kt, int i) {
     const bool is_a = i < LA;
     const int j = is_a ? i : i - LA;
-    const uint32_t off = kt * TB + ch * 16 < K ? kt * TB : OUT_OF_RANGE;
+    const int kr = kt + first < nk ? kt + first : kt + first - nk;
+    const uint32_t off = kt < nk && kr * TB + ch * 16 < K ? kr * TB : OUT_OF_RANGE;
     const uint32_t v = is_a ? va + j * 32 * (uint32_t)g.lda : vb + j * 32 * (uint32_t)g.ldb;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb,
                                              (lds_ptr_t)(dst + (is_a ? 0 : TM * TB) + (j * 4 + wave) * 1024), 16, v + off,
@@ -707,6 +717,7 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   // direct loads: whole chunks, 31-bit offsets in 128 rows
   const bool dma = (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && K % 16 == 0 &&
                    K > 0 && lda < (1 << 24) && ldb < (1 << 24);
+  g.turn = M <= 64 && ldb % 4096 == 0;
   auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
   if (!dma) {
     // 128 x 128 tiles where they occupy the chip (1021 x 4095 x 4095: 41 us, with
@@ -730,8 +741,9 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128>(g, bf16, st);
   else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128>(g, bf16, st);
   else if (M > 32 && tiles(64, 64) >= 160) launch_tile<64, 64>(g, bf16, st);
-  // fewer tiles: K split over the waves.  Tiles of 64 x 64, rings of 32 x 64 and
-  // of 32 x 32:
+  // fewer tiles: K split over the waves.  (These and the next times are of the
+  // forms without g.turn, which takes 1 to 3 us off both sides.)  Tiles of 64 x
+  // 64, rings of 32 x 64 and of 32 x 32:
   //   61 x 14336 x 4096 (224 tiles of 64 x 64)      18    -   23
   //   256 x 4096 x 14336 (256)                      37   48    -
   //   128 x 4096 x 14336 (128; 256 of 32 x 64)      37   27   33

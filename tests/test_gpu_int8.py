@@ -240,6 +240,8 @@ def test_product_bias(q, M, N, K, bias):
     (3, 4100, 2064, 0), (16, 900, 4112, 16), (17, 900, 4112, 0), (32, 4100, 656, 0),         # few rows and columns
     (20, 12300, 528, 0), (32, 12289, 400, 32), (33, 4100, 1040, 0), (64, 900, 16, 0),        # up to 64 rows
     (61, 10250, 1040, 0), (64, 12289, 256, 16), (100, 4100, 2064, 0), (128, 4096, 1024, 0),
+    (61, 28700, 4096, 0), (16, 12301, 4096, 0), (40, 4100, 4096, 0), (7, 900, 8192, 0), (16, 130, 12288, 0),  # far rows
+    (33, 10300, 4000, 96), (20, 900, 4064, 32),                                              # in a wider matrix
     (300, 1000, 144, 0), (450, 4100, 784, 0), (511, 4097, 400, 16), (1021, 3100, 528, 0), (900, 4100, 112, 0),
     (3, 800, 333, 0), (40, 700, 333, 0), (16, 7000, 129, 0), (200, 700, 333, 0), (53, 608, 1227, 5), (1000, 3201, 333, 3), (900, 4100, 100, 1)])  # any alignment
 def test_product_forms(q, M, N, K, pad, out, bias):
