@@ -47,7 +47,8 @@ struct Int8Args {
   // channels, and workgroups that read B in step meet there: each group of 8
   // neighbours then begins at another K step (a sum has no order) and goes
   // round (16 x 28672 x 4096: 27.2 -> 25.0 us, 32 x 16384 x 8192: 31.7 -> 27.8;
-  // other row lengths, and more rows than 64, gain nothing).
+  // other row lengths, and more rows than 64, gain nothing, and the kernels that
+  // serve those are without it: 1021 x 4096 x 4096 22 us, with it 24).
   int turn;
 };
 
@@ -253,11 +254,12 @@ __global__ __launch_bounds__(WAVES * 64) void gemm_int8_ring_kernel(Int8Args g) 
     vb[i] = (8 * i + pr) * (uint32_t)g.ldb + ch[i] * 16;
   }
   const int K = (int)g.K, nk = (K + 127) / 128, rounds = (nk + WAVES - 1) / WAVES;
-  const int first = g.turn ? (int)(tn / 8 * WAVES % nk) : 0;  // the step to begin with
+  constexpr bool TURN = NT < 4;  // up to 64 rows take no wider one
+  const int first = TURN && g.turn ? (int)(tn / 8 * WAVES % nk) : 0;  // the step to begin with
   uint32_t mine = wave * STEP;
   auto issue = [&](uint8_t* st, int round) {
-    const int at = round * WAVES + wave, turned = at + first < nk ? at + first : at + first - nk;
-    const int k = at < nk ? turned * 128 : K;
+    const int at = round * WAVES + wave, turned = !TURN || at + first < nk ? at + first : at + first - nk;
+    const int k = !TURN || at < nk ? turned * 128 : K;
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
       const uint32_t off = k + ch[i & 1] * 16 < K ? vb[i & 1] + (uint32_t)(i >> 1) * 16 * (uint32_t)g.ldb + k : OUT_OF_RANGE;
@@ -552,7 +554,7 @@ __global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args g) {
 // K tiles ahead in a ring of 4 stages.  (Through registers and fewer tiles
 // ahead, as above, a workgroup a CU waits for each tile's loads: 1021 x 4096 x
 // 4096 with 128 x 128 tiles 37 us, 22 here.)  Phases as above.
-template <int TM, int TN, bool OUT_BF16>
+template <int TM, int TN, bool TURN, bool OUT_BF16>
 __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
   constexpr int NI = TM / 64, NJ = TN / 64;   // 32 x 32 tiles of a wave
   constexpr int LA = TM / 32, LB = TN / 32;   // loads of a wave and K tile
@@ -580,14 +582,14 @@ __global__ __launch_bounds__(256) void gemm_int8_tile_kernel(Int8Args g) {
   const __amdgpu_buffer_rsrc_t ra = rows_rsrc(g.a, m0, g.M, g.lda, TM), rb = rows_rsrc(g.b, n0, g.N, g.ldb, TN);
   const TileScales<NI, NJ> scales(g, m0 + wm * (TM / 2), n0 + wn * (TN / 2), lane);
   const int K = (int)g.K, nk = (K + TB - 1) / TB;
-  const int first = g.turn ? (int)(in / high / 8 % nk) : 0;  // the K tile to begin with
+  const int first = TURN ? (int)(in / high / 8 % nk) : 0;  // the K tile to begin with
   // load i (of A's and then B's) of K tile kt; past the last row, or the
   // last 16 bytes of a row, 0 is read
   auto issue1 = [&](uint8_t* dst, int kt, int i) {
     const bool is_a = i < LA;
     const int j = is_a ? i : i - LA;
-    const int kr = kt + first < nk ? kt + first : kt + first - nk;
-    const uint32_t off = kt < nk && kr * TB + ch * 16 < K ? kr * TB : OUT_OF_RANGE;
+    const int kr = !TURN || kt + first < nk ? kt + first : kt + first - nk;
+    const uint32_t off = (!TURN || kt < nk) && kr * TB + ch * 16 < K ? kr * TB : OUT_OF_RANGE;
     const uint32_t v = is_a ? va + j * 32 * (uint32_t)g.lda : vb + j * 32 * (uint32_t)g.ldb;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb,
                                              (lds_ptr_t)(dst + (is_a ? 0 : TM * TB) + (j * 4 + wave) * 1024), 16, v + off,
@@ -692,12 +694,12 @@ void launch_any(Int8Args g, bool bf16, hipStream_t st) {
   else hipLaunchKernelGGL((gemm_int8_kernel<TM, TN, false>), grid, dim3(256), 0, st, g);
 }
 
-template <int TM, int TN>
+template <int TM, int TN, bool TURN = false>
 void launch_tile(Int8Args g, bool bf16, hipStream_t st) {
   g.tiles_m = (g.M + TM - 1) / TM;
   const dim3 grid((unsigned)(g.tiles_m * ((g.N + TN - 1) / TN)));
-  if (bf16) hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, true>), grid, dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, false>), grid, dim3(256), 0, st, g);
+  if (bf16) hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, TURN, true>), grid, dim3(256), 0, st, g);
+  else hipLaunchKernelGGL((gemm_int8_tile_kernel<TM, TN, TURN, false>), grid, dim3(256), 0, st, g);
 }
 
 }  // namespace
@@ -740,7 +742,10 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   //   256 x 4096 x 4096 (256)                       17   13   11
   if (M > 64 && tiles(128, 128) >= 192) launch_tile<128, 128>(g, bf16, st);
   else if (M > 64 && tiles(64, 128) >= 224) launch_tile<64, 128>(g, bf16, st);
-  else if (M > 32 && tiles(64, 64) >= 160) launch_tile<64, 64>(g, bf16, st);
+  else if (M > 32 && tiles(64, 64) >= 160) {
+    if (g.turn) launch_tile<64, 64, true>(g, bf16, st);
+    else launch_tile<64, 64>(g, bf16, st);
+  }
   // fewer tiles: K split over the waves.  (These and the next times are of the
   // forms without g.turn, which takes 1 to 3 us off both sides.)  Tiles of 64 x
   // 64, rings of 32 x 64 and of 32 x 32:
