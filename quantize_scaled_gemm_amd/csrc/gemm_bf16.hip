@@ -591,7 +591,9 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
   if (s < nsteps) step(st2, st1, sx2, sx0, s++, std::false_type{});
   wait_vm<0>();  // the loads past the last step (empty resources) have landed
   if constexpr (X8) {
-    // behind the last step's barrier no wave reads a stage any more
+    // every wave's loads into the stages have landed (those past the last step
+    // write zeros there), and behind the last step's barrier none reads one
+    lds_barrier();
     static_assert(32 * kRowPitch<4> * 4 <= DOP, "a wave's rows fit a stage");
     float* part = reinterpret_cast<float*>(wave == 0 ? st0 : wave == 1 ? st1 : wave == 2 ? st2 : sx0);
 #pragma unroll
