@@ -365,7 +365,10 @@ int qsg_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int6
   if (rows >= kMostInt8 || cols >= kMostInt8) return fail(QSG_ERR_UNSUPPORTED, "%s: rows and cols must be below 2^30", fn);
   const bool empty = rows == 0 || cols == 0;
   if (!q && !qt && !s && !st && !empty) return fail(QSG_ERR_ARG, "%s: q and qt are both null", fn);
-  if (!empty && (!q != !s || !qt != !st)) return fail(QSG_ERR_ARG, "%s: codes and scales of a copy go together", fn);
+  // (codes that there are none of may have no address; a row without columns, and
+  // a column without rows, has a scale)
+  if (empty ? (q && !s && rows > 0) || (qt && !st && cols > 0) : !q != !s || !qt != !st)
+    return fail(QSG_ERR_ARG, "%s: codes and scales of a copy go together", fn);
   if (!aligned(s, 4) || !aligned(st, 4)) return fail(QSG_ERR_ALIGN, "%s: scales not aligned", fn);
   if (!empty && qt) {
     if (!workspace) return fail(QSG_ERR_ARG, "%s: the transposed copy needs a workspace", fn);

@@ -70,6 +70,16 @@ def test_nothing_to_do_is_no_error(lib):
     assert lib.qsg_swiglu_int8_store_bwd(*dict(BWD, cols=0).values(), None) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(cols=0, s=None), dict(cols=0, s=None, ws=None), dict(cols=0, s=None, qt=None, st=None),
+    dict(rows=0, st=None), dict(rows=0, st=None, q=None, s=None)])
+def test_empty_codes_without_the_scales_that_are_there(lib, kw):
+    """Of a matrix without columns every row has a scale, which is written; of
+    one without rows every column of the transposed copy."""
+    assert lib.qsg_quantize_int8(*dict(QUANT, **kw).values(), None) == -1
+    assert b"go together" in lib.qsg_last_error()
+
+
 def test_workspace_sizes(lib):
     for bad in ((-1, 4), (4, -1), (BIG, 4), (4, BIG)):
         with pytest.raises(q.QsgError):
