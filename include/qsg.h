@@ -466,7 +466,9 @@ int qsg_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const int
  *           one may be shorter), then those of u's; or both NULL (a forward
  *           pass that no backward pass follows).
  * One of a, aq and ck is needed.  The formula is evaluated in binary32 from gu
- * itself.  No output may overlap gu or another output.  rows and cols below 2^30
+ * itself: for fp32 data with a relative error below 2^-21, for bf16 data (and
+ * aq, sa from them) below 2^-23 (|g| + 4), as long as 1 + exp(-g) is below
+ * 2^126 (g > -87); beyond, a may be 0.  No output may overlap gu or another output.  rows and cols below 2^30
  * (QSG_ERR_UNSUPPORTED). */
 int qsg_swiglu_int8_store_fwd(const void* gu, int dtype, int64_t rows, int64_t cols, int64_t ld, void* a, int8_t* aq,
                               float* sa, int8_t* ck, float* cs, void* stream);

@@ -121,12 +121,20 @@ def sigmoid_error(g, p):
     return p * (2 * (np.abs(g) + 1) * (1 - p) + 3) * U + 2.0 ** -125
 
 
-def swiglu_bounds(da, g, u, half_step):
+def sigmoid_error_f32(g, p):
+    """The same of what fp32 data take: the exponent's fraction, at most a half,
+    carries two roundings of 2^-25, 0.7 u of the exponential, whose own step is
+    2 u; (1 - p) of that reaches p; the sum and the division round by u.  Where
+    1 + exp is not finite, p is taken for 0."""
+    return p * (2.7 * (1 - p) + 2) * U + 2.0 ** -128
+
+
+def swiglu_bounds(da, g, u, half_step, error=sigmoid_error):
     """Bounds of (a, dg, du) against swiglu and swiglu_bwd; da may be None (a
-    alone)."""
+    alone); error is that of p."""
     g, u = np.asarray(g, np.float64), np.asarray(u, np.float64)
     p = sigmoid(g)
-    dp = sigmoid_error(g, p)
+    dp = error(g, p)
     floor = 2.0 ** -126
 
     def out(value, err):

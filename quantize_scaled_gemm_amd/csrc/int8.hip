@@ -540,8 +540,32 @@ struct GluArgs {
   int64_t lddgu;
 };
 
+// 1 + exp(-g), and silu(g) = g / (1 + exp(-g)) and 1 / (1 + exp(-g)) from it.
+// g log2(e) rounded to binary32 is off by up to 2^-24 |g log2(e)|, an error
+// that the exponential turns into a relative one.  bf16 results do not show it;
+// for fp32 data whole number and fraction of the exponent are formed apart, the
+// fraction from both halves of log2(e), and the division is correctly rounded
+// (silu against 64 bits at g = -20: 1.7e-7, without either 1.0e-6; at -87
+// 1.2e-7 and 3.9e-6).  fp32 hides this behind its memory traffic (8192 x 14336
+// with everything kept in 306 us either way, backward 440; 333 x 1111 in 4.8,
+// without 4.7), bf16 does not: 16384 x 14336 367 us, without 341.
+constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299e-8f;
+__device__ __forceinline__ float one_plus_exp(float g) {
+  // (beyond 128 the exponential is infinite or lost in the sum)
+  const float x = __builtin_amdgcn_fmed3f(g, -128.0f, 128.0f);
+  const float n = __builtin_rintf(x * -kLog2e);
+  const float f = fmaf(x, -kLog2eLow, fmaf(x, -kLog2e, -n));
+  return 1.0f + __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+}
+template <typename In>
 __device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
+  if constexpr (sizeof(In) == 4) return __fdiv_rn(1.0f, one_plus_exp(g));
+  else return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -kLog2e));
+}
+template <typename In>
+__device__ __forceinline__ float silu(float g) {
+  if constexpr (sizeof(In) == 4) return __fdiv_rn(g, one_plus_exp(g));
+  else return g * sigmoid<In>(g);
 }
 
 // Where a group of 16 lanes is in a matrix of blocks of 128: its lanes take
@@ -602,9 +626,9 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
     if (a.a) {
       In* o = reinterpret_cast<In*>(a.a) + at.row * a.cols;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
+      for (int i = 0; i < 8; ++i) g[i] = silu<In>(g[i]) * u[i];
       if (at.whole) store8(o + at.c, g, 8);
-      if (at.one) store1(o + at.e, g1 * sigmoid(g1) * u1);
+      if (at.one) store1(o + at.e, silu<In>(g1) * u1);
     }
   }
 }
@@ -633,8 +657,8 @@ __global__ __launch_bounds__(NT) void swiglu_row_kernel(GluArgs a) {
     if (first_time && a.ck && at.b < a.nb)
       keep_block(a, at, g, u, g1, u1, a.ck + row * 2 * a.cols, a.cs + row * 2 * a.nb, (k & 15) == 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
-    if (at.one) h1 = g1 * sigmoid(g1) * u1;  // (of one chunk of a thread at most)
+    for (int i = 0; i < 8; ++i) o[i] = silu<In>(g[i]) * u[i];
+    if (at.one) h1 = silu<In>(g1) * u1;  // (of one chunk of a thread at most)
     if (first_time) {
       m = amax8(o, m);
       if (a.a) {
@@ -681,8 +705,9 @@ __device__ __forceinline__ void load_codes(float (&v)[8], const int8_t* p, float
 }
 
 // Gradients of g and u, and a, from one value of each.
+template <typename In>
 __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg, float& du, float& act) {
-  const float p = sigmoid(g), w = g * p;  // silu(g)
+  const float p = sigmoid<In>(g), w = g * p;  // silu(g)
   dg = d * u * (p * (1.0f + g * (1.0f - p)));
   du = d * w;
   act = w * u;
@@ -712,7 +737,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
     }
     float h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) swiglu_grad(d[i], g[i], u[i], g[i], u[i], h[i]);
+    for (int i = 0; i < 8; ++i) swiglu_grad<In>(d[i], g[i], u[i], g[i], u[i], h[i]);
     In* o = reinterpret_cast<In*>(a.dgu) + at.row * a.lddgu;
     In* act = reinterpret_cast<In*>(a.a) + (a.a ? at.row * a.cols : 0);
     if (at.whole) {
@@ -721,7 +746,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
       if (a.a) store8(act + at.c, h, 8);
     }
     if (at.one) {
-      swiglu_grad(d1, g1, u1, g1, u1, h[0]);
+      swiglu_grad<In>(d1, g1, u1, g1, u1, h[0]);
       store1(o + at.e, g1);
       store1(o + a.cols + at.e, u1);
       if (a.a) store1(act + at.e, h[0]);

@@ -219,3 +219,25 @@ def test_past_32_bits(q):  # noqa: F811
     for r in at:
         check_backward(to_np(gu[r:r + 1]), None, np.full((1, C), 0.5), to_np(ck[r:r + 1]), to_np(cs[r:r + 1]), BF)
     assert int((gu != 0).any(dim=1).sum()) == len(at)
+
+
+@pytest.mark.parametrize("R, C", [(3, 1111), (300, 512), (2, 33001)])
+def test_fp32_far_gates(q, R, C):  # noqa: F811
+    """fp32 keeps its bits however far the gate is from 0, where a rounded
+    exponent would cost |g| of them."""
+    x = rng(34, R, C).standard_normal((R, 2 * C))
+    x[:, :C] = rng(35, R, C).uniform(-100, 100, (R, C))
+    gd, gf = tensor(x, F32)
+    g, u = gf[:, :C], gf[:, C:]
+    bound = o.swiglu_bounds(None, g, u, HALF[F32], o.sigmoid_error_f32)[0]
+    for outs in (dict(a=1), dict(a=1, aq=1, sa=1, ck=1, cs=1)):
+        bad = ~(np.abs(make(q, gd, C, **outs)["a"] - o.swiglu(g, u)) <= bound)
+        assert not bad.any(), (int(bad.sum()), g[bad][:4])
+    ck, cs = o.keep(gf)
+    g, u = o.kept(ck, cs)
+    dd, df = tensor(rng(36, R, C).standard_normal((R, C)), F32)
+    dgu, a = backward(q, dd, ck, cs, True)
+    bounds = o.swiglu_bounds(df, g, u, HALF[F32], o.sigmoid_error_f32)
+    for got, ref, e in zip((a, dgu[:, :C], dgu[:, C:]), (o.swiglu(g, u), *o.swiglu_bwd(df, g, u)), bounds):
+        bad = ~(np.abs(got - ref) <= e)
+        assert not bad.any(), (int(bad.sum()), g[bad][:4])
