@@ -241,3 +241,13 @@ def test_fp32_far_gates(q, R, C):  # noqa: F811
     for got, ref, e in zip((a, dgu[:, :C], dgu[:, C:]), (o.swiglu(g, u), *o.swiglu_bwd(df, g, u)), bounds):
         bad = ~(np.abs(got - ref) <= e)
         assert not bad.any(), (int(bad.sum()), g[bad][:4])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R, C", [(257, 2049), (300, 4104), (257, 8192), (260, 8193), (257, 14337), (258, 16384)])
+def test_copy_of_many_rows(q, R, C, dtype):  # noqa: F811
+    """More than 256 rows of 2049 columns and more hold a row's INT8 copy in
+    fewer threads than few rows do."""
+    gd, gf = tensor(rng(37, R, C).standard_normal((R, 2 * C)) * 4, dtype)
+    check_forward(make(q, gd, C, a=1, aq=1, sa=1, ck=1, cs=1), gf, dtype)
+    check_forward(make(q, gd, C, aq=1, sa=1), gf, dtype)
