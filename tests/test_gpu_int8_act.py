@@ -251,3 +251,16 @@ def test_copy_of_many_rows(q, R, C, dtype):  # noqa: F811
     gd, gf = tensor(rng(37, R, C).standard_normal((R, 2 * C)) * 4, dtype)
     check_forward(make(q, gd, C, a=1, aq=1, sa=1, ck=1, cs=1), gf, dtype)
     check_forward(make(q, gd, C, aq=1, sa=1), gf, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gates_at_the_ends(q, dtype):  # noqa: F811
+    """Infinities, NaN and the largest finite gates, as g / (1 + exp(-g)) has them."""
+    top = torch.finfo(dtype).max
+    g = np.array([np.inf, -np.inf, np.nan, top, -top, 1e30, -1e30, 128, -128, 0.0, 2.0 ** -126])
+    want = np.array([np.inf, np.nan, np.nan, top / 2, 0, 5e29, 0, 64, 0, 0, 2.0 ** -128])
+    gd, gf = tensor(np.concatenate([g, np.full(11, 0.5)])[None], dtype)
+    want[5] = gf[0, 5] / 2
+    a = make(q, gd, 11, a=1, aq=1, sa=1)["a"][0]
+    assert np.array_equal(a, make(q, gd, 11, a=1)["a"][0], equal_nan=True)
+    assert np.array_equal(a, want, equal_nan=True)
