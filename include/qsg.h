@@ -401,7 +401,8 @@ int64_t qsg_quantize_int8_workspace(int64_t rows, int64_t cols);
 /* INT8 copies of a matrix.
  *   x      rows x cols (dtype, ld), aligned to its element size.
  *   q, s   out: rows x cols codes (dense) with rows fp32 scales, one for each
- *          row; or both NULL.
+ *          row; or both NULL.  (Codes or scales that there are none of, of an
+ *          empty matrix, may be NULL alone.)
  *   qt, st out: the transposed copy, cols x rows codes (dense) with cols fp32
  *          scales, one for each column of x; or both NULL.
  *   workspace  for qt: qsg_quantize_int8_workspace(rows, cols) bytes of device
@@ -428,9 +429,11 @@ int qsg_quantize_int8(const void* x, int dtype, int64_t rows, int64_t cols, int6
  * M and N up to 2^26, and C of up to 2^23 tiles of 128 x 128
  * (QSG_ERR_UNSUPPORTED).  fprop takes the row-wise copies of X and W, dgrad those of dY and the
  * transposed copy of W.  Any shape and alignment: 16-byte aligned operands
- * with leading dimensions of whole 16 bytes and K % 256 == 0 (and a bias on 4
- * bytes, for a bf16 one with even N) select the fastest kernel where C has at
- * least 128 tiles of 256 x 256; K % 16 == 0 with that alignment direct loads. */
+ * of less than 4 GiB each with leading dimensions of whole 16 bytes and
+ * K % 256 == 0 (and a bias on 4 bytes, for a bf16 one with even N) select the
+ * fastest kernel where M > 64 and C has at least 128 tiles of 256 x 256;
+ * K % 16 == 0 with that alignment and leading dimensions below 2^24 direct loads
+ * (but for M <= 4 with N >= 12288, which do not gain by them). */
 int qsg_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const float* sb, int64_t M, int64_t N, int64_t K,
                   int64_t lda, int64_t ldb, const void* bias, int bias_dtype, void* c, int c_dtype, int64_t ldc,
                   void* stream);
