@@ -406,8 +406,8 @@ __device__ __forceinline__ void store_rows(const Bf16Args& g, const Tiles& acc, 
 // 32 bytes of bf16, where the direct load of a bf16 X would have put them, so
 // the rest of the kernel is the same.  The codes of step s + 2 replace those
 // of step s + 1 in their registers once these are widened, in the shadow of
-// step s's MFMAs.  4096 x 4096 over 32768 tokens in 929 us (1.18 PFLOP/s), of a
-// bf16 X in 741-784: 48 values a thread and step are widened beside 48 MFMAs,
+// step s's MFMAs.  4096 x 4096 over 32768 tokens in 905 to 957 us (1.15 to 1.21
+// PFLOP/s), of a bf16 X in 741-784: 48 values a thread and step are widened beside 48 MFMAs,
 // and the two share the issue slots (matrix pipe busy 62% of the cycles, 85%
 // with a bf16 X, at 1.78 and 1.62 GHz).  x' is a bf16 tensor by definition, so
 // nothing of this is rounded twice.
@@ -514,7 +514,9 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
   // Step s on stage `cur`: the loads of step s + 2 go into `next2` (the
   // stage of step s - 1, which every wave left before the last barrier), the
   // MFMAs run on `cur`, then the wait for step s + 1's loads (at most the
-  // younger step's 2 DLOADS loads are still in flight) and a barrier.
+  // younger step's LOADS loads are still in flight: those of both operands into
+  // LDS, or for an INT8 X dY's into LDS and the codes' and scales' into
+  // registers) and a barrier.
   // FIRST: the first MFMA of each accumulator tile starts from C = 0.
   // INT8 X: curx holds its step s; step s + 1 goes to nextx.
   auto step = [&](const uint8_t* cur, uint8_t* next2, const uint8_t* curx, uint8_t* nextx, int64_t s, auto first) {
@@ -668,8 +670,8 @@ __global__ __launch_bounds__(256, 1) void gemm_wgrad_bf16_dma_kernel(Bf16Args g)
 // bf16.  Loads ask for no alignment.  Features past the end of an operand
 // only reach results that are not stored, so a row may be read past its end
 // where memory goes on, into the next row; only a step in which it might not
-// (the last one or two) is loaded with more care.  777 x 1000 x 1111 in 15.6 us,
-// 8192 x 1024 x 1024 in 41: the loads bound it, at a lane's 16 bytes a clock (34
+// (the last one or two) is loaded with more care.  777 x 1000 x 1111 in 13.7 us,
+// 8192 x 1024 x 1024 in 40 to 43: the loads bound it, at a lane's 16 bytes a clock (34
 // to 50 bytes a ns on a CU), not their latency (twice as many in flight change
 // nothing).
 template <int TILE>
@@ -956,7 +958,7 @@ void launch_wgrad_int8(const void* dy, int64_t T, int64_t N, int64_t lddy, const
   // 128 x 128: 52 us, with 64 x 64 91).  With no more 64 x 64 tiles than CUs four
   // groups of waves share one (8192 x 1024 x 1024: 41 us; earlier, 47 against 54
   // with two groups and 68 with one), with more of them two, two workgroups to a
-  // CU (777 x 1000 x 1111, 288 tiles: 16 us, with four groups 20).  With no more
+  // CU (777 x 1000 x 1111, 288 tiles: 13.7 us, with four groups 18.7).  With no more
   // 32 x 32 tiles than CUs these, eight waves each (15339 x 541 x 172: 57 us, with
   // 64 x 64 75; 2048 x 512 x 512: 12.6 and 14.9; beyond, 8192 x 640 x 640, 400
   // tiles: 48 and 37).

@@ -332,11 +332,14 @@ __device__ __forceinline__ void mfma_range(v16f (&acc)[TMW][TN], const Frags<TN>
 
 // INT8: the two halves of a fragment are the operands of two 32-K
 // instructions, each lane half's 16 bytes being 16 of their K values (both
-// operands are split alike, and integer sums have no order).  They run at half
-// the rate of the scaled FP8 instruction, so the fetches hide more easily: 32768
-// x 4096 x 4096 in 437 us to bf16 (2.5 POP/s; 71% of the matrix pipe's cycles at
-// the 1.65 GHz that its power allows) and 474 to fp32, 32768 x 14336 x 4096 in
-// 1505, 32768 x 4096 x 14336 in 1400 (2.75 POP/s).
+// operands are split alike, and integer sums have no order).  Each has half the
+// operations of the scaled FP8 instruction and takes half its time: 2.51 POP/s
+// at 1.65 GHz with the pipe busy 71% of the cycles are 8300 operations a clock
+// and CU, the FP8 product's 2.885 PFLOP/s at 1.86 GHz and 74% 8200.  So the
+// matrix pipe bounds it, at the clock that its power allows: 32768 x 4096 x 4096
+// to bf16 in 422 us among other calls and 437 to 460 back to back, to fp32 474
+// to 495, 32768 x 14336 x 4096 in 1505 to 1573, 32768 x 4096 x 14336 in 1400 to
+// 1451 (2.65 to 2.75 POP/s).
 template <bool MX, int FA, int FB, int LO, int HI, int TN, int OPS = 0>
 __device__ __forceinline__ void mfma_range(v16i (&acc)[TMW][TN], const Frags<TN>& f) {
 #pragma unroll
@@ -1187,6 +1190,8 @@ bool launch_gemm_int8_fast(const int8_t* a, const float* sa, const int8_t* b, co
                            int64_t K, int64_t lda, int64_t ldb, const void* bias, bool bias_bf16, void* c, int c_dtype,
                            int64_t ldc, hipStream_t st) {
   if (bias && ((uintptr_t)bias % 4 || (bias_bf16 && N % 2))) return false;
+  // (the loop takes K tiles in pairs; other K have 128 x 128 tiles, which are
+  // slower: 4096 x 4096 x 4224 103 us, 4096 x 4096 x 4096 here 64)
   if (K <= 0 || K % (2 * FBK) != 0) return false;
   if ((uintptr_t)a % 16 || (uintptr_t)b % 16 || lda % 16 || ldb % 16) return false;
   if (M * lda >= (int64_t)1 << 32 || N * ldb >= (int64_t)1 << 32) return false;

@@ -5,7 +5,7 @@
 //
 // What bounds it depends on the rows of A: a decode batch reads B once (16 rows
 // through 28672 x 4096: 25 us, 4.7 TB/s), a training batch is matrix
-// instructions (32768 x 4096 x 4096: 437 us, 2.5 POP/s).  Five kernels:
+// instructions (32768 x 4096 x 4096: 422 to 460 us, 2.4 to 2.6 POP/s).  Five kernels:
 //   * 256 x 256 persistent tiles (gemm_fast.hip, the FP8 products' loop);
 //   * tiles of 64 and 128 by direct loads into a ring of LDS stages;
 //   * 16 to 32 rows of A by 16 to 64 of B, K split over a workgroup's waves, each
@@ -713,8 +713,18 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   g.bias_bf16 = bias_dtype == QSG_BF16;
   g.M = M; g.N = N; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc; g.c = c;
   const bool bf16 = c_dtype == QSG_BF16;
-  // 256 x 256 tiles where they occupy half of the CUs (2048 x 4096 x 4096: 46 us,
-  // with 128 x 128 tiles 49; 4096 x 4096 x 4096: 61 and 97)
+  // 256 x 256 tiles where there are 128 of them, for half of the CUs (us with
+  // them, and with the kernels below):
+  //   2048 x 4096 x 4096 (128 tiles)     46    49
+  //   4096 x 4096 x 4096 (256)           64    97
+  //   32768 x 256 x 4096 (128)           57    58
+  //   257 x 28672 x 4096 (224)           52    61
+  // The number says nothing of how full they are; where less than 100 full ones
+  // would do, the smaller tiles are the faster:
+  //   32768 x 192 x 4096 (128, 96 full ones' work)   56    53
+  //   32768 x 128 x 4096 (128, 64)                   58    40
+  //   130 x 32768 x 4096 (128, 65)                   52    49
+  //   65 x 32768 x 4096 (128, 33)                    50    38
   if (M > 64 && launch_gemm_int8_fast(a, sa, b, sb, M, N, K, lda, ldb, bias, g.bias_bf16, c, c_dtype, ldc, st)) return;
   // direct loads: whole chunks, 31-bit offsets in 128 rows
   const bool dma = (uintptr_t)a % 16 == 0 && (uintptr_t)b % 16 == 0 && lda % 16 == 0 && ldb % 16 == 0 && K % 16 == 0 &&
@@ -722,6 +732,8 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   g.turn = M <= 64 && ldb % 4096 == 0;
   auto tiles = [&](int64_t tm, int64_t tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); };
   if (!dma) {
+    // Bound by loads of 16 bytes at any address, a lane a clock: codes realigned
+    // once would need a workspace, which this call does not take.
     // 128 x 128 tiles where they occupy the chip (1021 x 4095 x 4095: 41 us, with
     // 64 x 64 58).  K split over waves instead where that needs no more workgroups
     // than CUs (53 x 608 x 12275: 33 us, with 64 x 64 43; 130 x 130 x 333: 3.9 and
@@ -755,12 +767,21 @@ void launch_gemm_int8(const int8_t* a, const float* sa, const int8_t* b, const f
   //   61 x 4096 x 14336 (64; 128)                   38    -   21
   else if (M > 64 && tiles(32, 64) >= 200) launch_ring<2, 4, 4, 2>(g, bf16, st);
   // rings of 32 x 32 or 32 x 16, 16 x 32 or 16 x 16: enough workgroups, then
-  // fewer reads of A (32 x 28672 x 4096: 30 and 35 us; 32 x 4096 x 14336: 22 and
-  // 18; 16 x 28672 x 4096: 27 and 30; 16 x 4096 x 14336: 18 and 14)
+  // fewer reads of A.  32 columns a workgroup from 384 workgroups on, one and a
+  // half a CU (us with 32 and with 16 columns; from 256 workgroups to there
+  // either may win):
+  //                         N = 4096     8192        10240       12288       14336       28672
+  //   16 x N x 4096      6.2   6.1    8.7  9.3   12.9 12.7   13.6 14.9   14.1 16.7   25.3 28.5
+  //   32 x N x 4096      6.7   6.4    9.4 11.0   14.8 15.4   15.5 17.6   16.4 20.3   28.6 33.9
+  //   16 x N x 14336    18.3  14.7   22.9 26.1      -         38.9 37.9      -           -
+  //   32 x N x 14336    22.1  18.1   25.6 33.0      -         44.2 48.2      -           -
   else if (M > 32 || (M > 16 && N >= 12288)) launch_ring<2, 2, 4, 2>(g, bf16, st);
   else if (M > 16) launch_ring<2, 1, 4, 3>(g, bf16, st);
-  // up to 4 rows read A's lines so seldom that LDS does not pay (28672 x 4096:
-  // one row 22 us, with the ring 26; 4 rows 24 and 26; 8 rows 28 and 26)
+  // up to 4 rows read A's lines so seldom that LDS does not pay, from the same
+  // number of columns on (us without it and with the ring of 16, K = 4096: one row
+  // through 8192 columns 8.3 and 8.8, 12288 11.7 and 13.6, 28672 22 and 26; 4 rows
+  // 8.8 and 8.9, 12.3 and 13.8, 24 and 26; 8 rows through 28672 28 and 26; K =
+  // 14336, where the ring is the faster: 4 rows through 12288 36 and 33)
   else if (M <= 4 && N >= 12288) launch_few(g, bf16, st);
   else if (N >= 12288) launch_ring<1, 2, 4, 2>(g, bf16, st);
   else launch_ring<1, 1, 4, 4>(g, bf16, st);

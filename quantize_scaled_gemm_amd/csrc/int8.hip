@@ -213,7 +213,7 @@ struct QuantArgs {
 
 // A row in the registers of TPR threads, CH chunks of 8 values each; the up to
 // 7 values behind the last whole chunk go one to a thread.  Bound by memory, x
-// read once and its codes written: 32768 x 4096 bf16 in 64 us (6.3 TB/s), 32768
+// read once and its codes written: 32768 x 4096 bf16 in 62-64 us (6.4 TB/s), 32768
 // x 1111 in 22, one row of 4096 in 2.8.
 template <typename In, int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int8_row_kernel(QuantArgs a) {
@@ -606,7 +606,7 @@ __device__ __forceinline__ void keep_block(const GluArgs& a, const BlockAt& at, 
 
 // One block of 128 of g and of u to 16 neighbouring lanes; groups of lanes take
 // the blocks of the matrix in turn.  Bound by memory: 16384 x 14336 bf16 in 339
-// us (5.5 TB/s: gu read, a and the codes written), 333 x 1111 fp32 in 4.6.
+// us (5.5 TB/s: gu read, a and the codes written), 333 x 1111 fp32 in 4.8.
 template <typename In>
 __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
@@ -635,7 +635,8 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GluArgs a) {
 
 // With an INT8 copy of a: a row to a workgroup, which holds a in registers (CH
 // > 0, CH chunks of 8 a thread) or computes it twice (CH == 0).  8192 x 14336
-// bf16 with gu kept in 147-150 us (5.5 TB/s), 61 x 14336 in 7.
+// bf16 with gu kept in 147-151 us (5.5 TB/s), without in 104; 61 x 14336 without
+// in 5.6.
 template <typename In, int NT, int CH>
 __global__ __launch_bounds__(NT) void swiglu_row_kernel(GluArgs a) {
   __shared__ uint32_t red[NT / 64];
@@ -714,7 +715,7 @@ __device__ __forceinline__ void swiglu_grad(float d, float g, float u, float& dg
 }
 
 // Blocks of 128 as the forward pass takes them; bound by memory: 16384 x 14336
-// bf16 with a in 422 us, without 324 (5.6 and 5.8 TB/s), 333 x 1111 fp32 in 4.7.
+// bf16 with a in 422 us, without 329 (5.6 and 5.7 TB/s), 333 x 1111 fp32 in 4.9.
 template <typename In>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GluArgs a) {
   const int t = threadIdx.x & 15;
@@ -779,7 +780,7 @@ template <typename In>
 void launch_glu_fwd(const GluArgs& a, hipStream_t st) {
   if (a.sa) {  // an empty copy may have no address
     // few rows: more threads a row, for the latency of its loads (aq alone of 61 x
-    // 14336: 7.5 us with 512 threads, 5.5 with 1024); many rows: more chunks a
+    // 14336: 7.5 us with 512 threads, 5.6 with 1024); many rows: more chunks a
     // thread (16384 x 8192: 157 us with 512 threads of two, 164 with 1024 of one;
     // 32768 x 2048: 86 with 256, 111 with 512; 4096 x 28672: 170, and 217 without
     // registers)
